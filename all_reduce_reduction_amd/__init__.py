@@ -47,6 +47,7 @@ DEBUG = {"epoch": 0, "spin_limit": 1, "ll_wait_skew": 2, "fill_ll": 3, "log": 4,
               "phased": 14, "phased_min": 15, "phased_expired": 16, "phased_last": 17,
          "phased_layout": 18, "phased_whole_last": 19}
 MAX_RANKS = 16
+ROUTE_MAX_EXPERTS, ROUTE_MAX_TOPK, DISTILL_MAX_TOPK = 1024, 32, 256
 LL_MAX_BYTES_PER_RANK = 1 << 20
 
 
@@ -62,6 +63,7 @@ def _load() -> ctypes.CDLL:
                           "(hipcc --offload-arch=gfx950) first")
     lib = ctypes.CDLL(LIBPATH)
     vp, sz, i, d = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_double
+    i64, f, psz = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(ctypes.c_size_t)
     pp = ctypes.POINTER(ctypes.c_void_p)
     sig = {
         "sim_init": ([i, i, sz], i),
@@ -91,13 +93,21 @@ def _load() -> ctypes.CDLL:
         "sim_debug_set": ([i, ctypes.c_uint64], i),
         "sim_debug_get": ([i, ctypes.POINTER(ctypes.c_uint64)], i),
         "sim_debug_set_epoch": ([ctypes.c_uint32], i),
+        "sim_route_work": ([i64, i, i, i, psz], i),
+        "sim_route": ([vp, i64, i, vp, i64, i, i, i, vp, vp, vp, vp, vp, sz, vp], i),
+        "sim_route_grad": ([vp, i64, i, vp, i64, i, i, i, vp, vp, vp, vp, f, vp, i64, vp, vp], i),
+        "sim_distill_work": ([i64, i64, i, psz], i),
+        "sim_distill_step": ([vp, i64, i, i64, i64, vp, vp, i, i, f, vp, f, vp, i64, vp, vp, sz, vp], i),
+        "sim_distill_parts": ([vp, i64, i, i64, i64, i64, i64, vp, vp, i, i, f, vp, vp, sz, vp], i),
+        "sim_distill_join": ([vp, i, i64, i64, vp, vp, i, i, f, vp, vp, vp], i),
+        "sim_distill_grad": ([vp, i64, i, i64, i64, i64, i64, vp, vp, i, i, f, vp, vp, f, vp, i64, vp], i),
         "sim_status_string": ([i], ctypes.c_char_p),
         "sim_version": ([], i),
     }
     for name, (args, res) in sig.items():
-        f = getattr(lib, name)
-        f.argtypes = args
-        f.restype = res
+        fn = getattr(lib, name)
+        fn.argtypes = args
+        fn.restype = res
     return lib
 
 
@@ -238,6 +248,61 @@ def sim_copy_streams(src_ptrs, dst_ptrs, k: int, nbytes: int, workgroups: int = 
                                 stream or None)
 
 
+def sim_route_work(tokens: int, experts: int, topk: int, dtype) -> int:
+    """Workspace bytes of sim_route."""
+    n = ctypes.c_size_t(0)
+    _check(lib.sim_route_work(tokens, experts, topk, _code(DTYPES, dtype, "dtype"), ctypes.byref(n)),
+           "sim_route_work")
+    return n.value
+
+
+def sim_route(logits, row_stride, dtype, keep, tokens, experts, topk, normalize, chosen, weights, counts, prob_sums,
+              work, work_bytes, stream=0) -> int:
+    return lib.sim_route(logits, row_stride, _code(DTYPES, dtype, "dtype"), keep, tokens, experts, topk, normalize,
+                         chosen, weights, counts, prob_sums, work, work_bytes, stream or None)
+
+
+def sim_route_grad(logits, row_stride, dtype, keep, tokens, experts, topk, normalize, chosen, dweights, counts,
+                   prob_sums, coef, dlogits, drow_stride, loss, stream=0) -> int:
+    return lib.sim_route_grad(logits, row_stride, _code(DTYPES, dtype, "dtype"), keep, tokens, experts, topk,
+                              normalize, chosen, dweights, counts, prob_sums, coef, dlogits, drow_stride, loss,
+                              stream or None)
+
+
+def sim_distill_work(rows: int, columns: int, dtype) -> int:
+    """Workspace bytes of sim_distill_step (columns: the vocabulary) and sim_distill_parts."""
+    n = ctypes.c_size_t(0)
+    _check(lib.sim_distill_work(rows, columns, _code(DTYPES, dtype, "dtype"), ctypes.byref(n)), "sim_distill_work")
+    return n.value
+
+
+def sim_distill_step(logits, row_stride, dtype, rows, vocab, ids, teacher, teacher_dtype, topk, temperature,
+                     row_scale, coef, dlogits, drow_stride, loss, work, work_bytes, stream=0) -> int:
+    return lib.sim_distill_step(logits, row_stride, _code(DTYPES, dtype, "dtype"), rows, vocab, ids, teacher,
+                                _code(DTYPES, teacher_dtype, "dtype"), topk, temperature, row_scale, coef, dlogits,
+                                drow_stride, loss, work, work_bytes, stream or None)
+
+
+def sim_distill_parts(logits, row_stride, dtype, rows, columns, first, vocab, ids, teacher, teacher_dtype, topk,
+                      temperature, parts, work, work_bytes, stream=0) -> int:
+    return lib.sim_distill_parts(logits, row_stride, _code(DTYPES, dtype, "dtype"), rows, columns, first, vocab, ids,
+                                 teacher, _code(DTYPES, teacher_dtype, "dtype"), topk, temperature, parts, work,
+                                 work_bytes, stream or None)
+
+
+def sim_distill_join(parts, nparts, rows, vocab, ids, teacher, teacher_dtype, topk, temperature, loss, norm,
+                     stream=0) -> int:
+    return lib.sim_distill_join(parts, nparts, rows, vocab, ids, teacher, _code(DTYPES, teacher_dtype, "dtype"), topk,
+                                temperature, loss, norm, stream or None)
+
+
+def sim_distill_grad(logits, row_stride, dtype, rows, columns, first, vocab, ids, teacher, teacher_dtype, topk,
+                     temperature, norm, row_scale, coef, dlogits, drow_stride, stream=0) -> int:
+    return lib.sim_distill_grad(logits, row_stride, _code(DTYPES, dtype, "dtype"), rows, columns, first, vocab, ids,
+                                teacher, _code(DTYPES, teacher_dtype, "dtype"), topk, temperature, norm, row_scale,
+                                coef, dlogits, drow_stride, stream or None)
+
+
 def sim_config_set(key, value: int) -> None:
     _check(lib.sim_config_set(_code(CONFIG, key, "config key"), int(value)), "sim_config_set")
 
@@ -374,3 +439,171 @@ def all_gather(inputs: Sequence, outputs: Sequence, algo="auto", stream=None):
                         _stream(stream))
     _check(st, "sim_all_gather")
     return outputs
+
+
+# ---- routing and losses (torch tensors; marshalling only) --------------------------
+def _rows(t, what, cols=None, like=None):
+    """(pointer, row stride) of a 2-D device tensor whose rows are contiguous."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{what} must be a 2-D device tensor")
+    n, c = t.shape
+    st = t.stride()
+    if c > 1 and st[1] != 1:
+        raise ValueError(f"{what}'s rows must be contiguous")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+        raise ValueError(f"{what} must have the logits' shape and dtype")
+    return t.data_ptr(), (st[0] if n > 1 else c)
+
+
+def _vec(t, what, shape, dtypes, device):
+    """Pointer of a contiguous device tensor of the given shape and one of the given dtypes (None: None)."""
+    if t is None:
+        return None
+    if t.device != device or not t.is_contiguous() or t.shape != shape or t.dtype not in dtypes:
+        raise ValueError(f"{what} must be a contiguous tensor {tuple(shape)} of "
+                         f"{' or '.join(str(d) for d in dtypes)} on {device}")
+    return t.data_ptr()
+
+
+def _work(nbytes, device, stream):
+    """A call's scratch: (tensor, pointer); kept from reuse by other streams until the call's work is done."""
+    if nbytes == 0:
+        return None, None
+    w = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        w.record_stream(stream)
+    return w, w.data_ptr()
+
+
+def route(logits, topk: int, keep=None, normalize: bool = True, out=None, stream=None):
+    """Softmax gate of logits [tokens, experts]: (chosen int32 [tokens, topk], weights fp32 [tokens, topk], counts
+    int32 [experts + 1], prob_sums fp32 [experts]); ``sim_route`` in include/simar.h says what each holds.  keep:
+    bool or uint8 [tokens].  out: the same four tensors, to write into."""
+    ptr, ld = _rows(logits, "logits")
+    n, e = logits.shape
+    dev, dt = logits.device, DTYPES[_dtype_name(logits)]
+    if out is None:
+        out = (torch.empty((n, topk), dtype=torch.int32, device=dev), torch.empty((n, topk), device=dev),
+               torch.empty(e + 1, dtype=torch.int32, device=dev), torch.empty(e, device=dev))
+    i32, f32 = (torch.int32,), (torch.float32,)
+    nb = ctypes.c_size_t(0)
+    _check(lib.sim_route_work(n, e, topk, dt, ctypes.byref(nb)), "sim_route_work")
+    w, wp = _work(nb.value, dev, stream)
+    _check(lib.sim_route(ptr, ld, dt, _vec(keep, "keep", (n,), (torch.bool, torch.uint8), dev), n, e, topk,
+                         bool(normalize), _vec(out[0], "chosen", (n, topk), i32, dev),
+                         _vec(out[1], "weights", (n, topk), f32, dev), _vec(out[2], "counts", (e + 1,), i32, dev),
+                         _vec(out[3], "prob_sums", (e,), f32, dev), wp, nb.value, _stream(stream) or None),
+           "sim_route")
+    return out
+
+
+def route_grad(logits, chosen, dweights=None, counts=None, prob_sums=None, coef: float = 0.0, keep=None,
+               normalize: bool = True, out=None, stream=None):
+    """Balance loss of the (reduced) counts and prob_sums, and the gradient of that loss and of the combine weights
+    for the logits: (loss fp32 [1], dlogits); ``sim_route_grad`` in include/simar.h says what each holds.  out: the
+    same two tensors, to write into (dlogits may be the logits)."""
+    ptr, ld = _rows(logits, "logits")
+    n, e = logits.shape
+    dev = logits.device
+    topk = chosen.shape[1]
+    if out is None:
+        out = (torch.empty(1, device=dev), torch.empty((n, e), dtype=logits.dtype, device=dev))
+    dptr, dld = _rows(out[1], "dlogits", like=logits)
+    i32, f32 = (torch.int32,), (torch.float32,)
+    _check(lib.sim_route_grad(ptr, ld, DTYPES[_dtype_name(logits)],
+                              _vec(keep, "keep", (n,), (torch.bool, torch.uint8), dev), n, e, topk, bool(normalize),
+                              _vec(chosen, "chosen", (n, topk), i32, dev),
+                              _vec(dweights, "dweights", (n, topk), f32, dev),
+                              _vec(counts, "counts", (e + 1,), i32, dev), _vec(prob_sums, "prob_sums", (e,), f32, dev),
+                              coef, dptr, dld, _vec(out[0], "loss", (1,), f32, dev), _stream(stream) or None),
+           "sim_route_grad")
+    return out
+
+
+def _slots(ids, teacher, rows, device):
+    """(ids pointer, teacher pointer, its dtype code, topk)"""
+    shape = ids.shape
+    if len(shape) != 2 or shape[0] != rows:
+        raise ValueError("ids must be [rows, topk]")
+    return (_vec(ids, "ids", shape, (torch.int32,), device),
+            _vec(teacher, "teacher", shape, (torch.float32, torch.float16, torch.bfloat16), device),
+            DTYPES[_dtype_name(teacher)], shape[1])
+
+
+def distill_step(logits, ids, teacher, temperature: float = 1.0, row_scale=None, coef: float = 1.0, out=None,
+                 stream=None):
+    """Distillation of logits [rows, vocab] from a teacher's top logits (ids int32 [rows, topk], teacher [rows,
+    topk]): (loss fp32 [rows], dlogits); ``sim_distill_step`` in include/simar.h says what each holds.  out: the same
+    two tensors, to write into (dlogits may be the logits)."""
+    ptr, ld = _rows(logits, "logits")
+    n, v = logits.shape
+    dev, dt = logits.device, DTYPES[_dtype_name(logits)]
+    if out is None:
+        out = (torch.empty(n, device=dev), torch.empty((n, v), dtype=logits.dtype, device=dev))
+    dptr, dld = _rows(out[1], "dlogits", like=logits)
+    ip, tp, tdt, k = _slots(ids, teacher, n, dev)
+    f32 = (torch.float32,)
+    nb = ctypes.c_size_t(0)
+    _check(lib.sim_distill_work(n, v, dt, ctypes.byref(nb)), "sim_distill_work")
+    w, wp = _work(nb.value, dev, stream)
+    _check(lib.sim_distill_step(ptr, ld, dt, n, v, ip, tp, tdt, k, temperature,
+                                _vec(row_scale, "row_scale", (n,), f32, dev), coef, dptr, dld,
+                                _vec(out[0], "loss", (n,), f32, dev), wp, nb.value, _stream(stream) or None),
+           "sim_distill_step")
+    return out
+
+
+def distill_parts(logits, ids, teacher, temperature: float = 1.0, first: int = 0, vocab: Optional[int] = None,
+                  out=None, stream=None):
+    """A vocabulary shard's statistics, fp32 [4, rows]: logits hold the columns from `first` on of `vocab` (default:
+    up to the shard's end)."""
+    ptr, ld = _rows(logits, "logits")
+    n, c = logits.shape
+    dev, dt = logits.device, DTYPES[_dtype_name(logits)]
+    if out is None:
+        out = torch.empty((4, n), device=dev)
+    ip, tp, tdt, k = _slots(ids, teacher, n, dev)
+    nb = ctypes.c_size_t(0)
+    _check(lib.sim_distill_work(n, c, dt, ctypes.byref(nb)), "sim_distill_work")
+    w, wp = _work(nb.value, dev, stream)
+    _check(lib.sim_distill_parts(ptr, ld, dt, n, c, first, first + c if vocab is None else vocab, ip, tp, tdt, k,
+                                 temperature, _vec(out, "parts", (4, n), (torch.float32,), dev), wp, nb.value,
+                                 _stream(stream) or None), "sim_distill_parts")
+    return out
+
+
+def distill_join(parts, ids, teacher, temperature: float = 1.0, vocab: Optional[int] = None, out=None, stream=None):
+    """Loss of all shards' parts [nparts, 4, rows], as all_gather leaves them: (loss fp32 [rows], norm fp32 [2,
+    rows]).  vocab: the whole vocabulary (ids outside it are empty slots; default: none is, but the negative)."""
+    if parts.dim() != 3 or parts.shape[1] != 4:
+        raise ValueError("parts must be [nparts, 4, rows]")
+    p, _, n = parts.shape
+    dev = parts.device
+    if out is None:
+        out = (torch.empty(n, device=dev), torch.empty((2, n), device=dev))
+    ip, tp, tdt, k = _slots(ids, teacher, n, dev)
+    f32 = (torch.float32,)
+    _check(lib.sim_distill_join(_vec(parts, "parts", (p, 4, n), f32, dev), p, n,
+                                2 ** 31 - 1 if vocab is None else vocab, ip, tp, tdt, k, temperature,
+                                _vec(out[0], "loss", (n,), f32, dev), _vec(out[1], "norm", (2, n), f32, dev),
+                                _stream(stream) or None), "sim_distill_join")
+    return out
+
+
+def distill_grad(logits, ids, teacher, norm, temperature: float = 1.0, row_scale=None, coef: float = 1.0,
+                 first: int = 0, vocab: Optional[int] = None, out=None, stream=None):
+    """The gradient of a vocabulary shard's logits from the joined norm [2, rows].  out: the gradient, to write into
+    (it may be the logits)."""
+    ptr, ld = _rows(logits, "logits")
+    n, c = logits.shape
+    dev = logits.device
+    if out is None:
+        out = torch.empty((n, c), dtype=logits.dtype, device=dev)
+    dptr, dld = _rows(out, "dlogits", like=logits)
+    ip, tp, tdt, k = _slots(ids, teacher, n, dev)
+    f32 = (torch.float32,)
+    _check(lib.sim_distill_grad(ptr, ld, DTYPES[_dtype_name(logits)], n, c, first,
+                                first + c if vocab is None else vocab, ip, tp, tdt, k, temperature,
+                                _vec(norm, "norm", (2, n), f32, dev), _vec(row_scale, "row_scale", (n,), f32, dev),
+                                coef, dptr, dld, _stream(stream) or None), "sim_distill_grad")
+    return out

@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "kernels.h"
+#include "loss.h"
 #include "schedule.h"
 #include "select.h"
 #include "simar.h"
@@ -1319,6 +1320,13 @@ int parse_algo_env(const char* v) {
 }
 
 }  // namespace
+
+// what the routing and distillation entry points (api_loss.cpp) need of the
+// library context
+bool library_ready() { return g.init; }
+int library_device() { return use_device(); }
+int library_cus() { return g.cu_count; }
+
 }  // namespace simar
 
 using namespace simar;

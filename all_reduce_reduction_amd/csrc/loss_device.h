@@ -1,0 +1,92 @@
+// loss_device.h -- device helpers shared by the routing and distillation
+// kernels: rows of 16-byte vectors of any alignment, wave reductions, the
+// base-2 exponential.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.h"
+
+namespace simar {
+
+constexpr float kNegInf = -__builtin_inff();
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// A row of logits may start at any element (a column slice, an odd stride):
+// its 16-byte accesses are typed with the alignment of one element.  gfx950
+// serves them from the same global_load/store_dwordx4.
+typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_at4 __attribute__((ext_vector_type(4), aligned(4)));
+template <int E> struct RowVec;
+template <> struct RowVec<2> {
+  typedef __attribute__((address_space(1))) const u32x4_at2 CG;
+  typedef __attribute__((address_space(1))) u32x4_at2 G;
+};
+template <> struct RowVec<4> {
+  typedef __attribute__((address_space(1))) const u32x4_at4 CG;
+  typedef __attribute__((address_space(1))) u32x4_at4 G;
+};
+template <int DT>
+__device__ __forceinline__ u32x4 ld_row(const void* row, int64_t elem) {
+  return *(typename RowVec<Ty<DT>::E>::CG*)((const char*)row + elem * Ty<DT>::E);
+}
+template <int DT>
+__device__ __forceinline__ void st_row(void* row, int64_t elem, u32x4 v) {
+  *(typename RowVec<Ty<DT>::E>::G*)((char*)row + elem * Ty<DT>::E) = v;
+}
+
+// 2^x (v_exp_f32: 1 ulp; results below the normal range are flushed, far
+// under what a sum that holds 1 can see)
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Sums and maxima over the 64 lanes of a wave, the same value in every lane;
+// the order of a sum is fixed.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+  return v;
+}
+
+// A softmax's running maximum m and sum s of 2^((x - m) c), over the x seen
+// so far (m = -inf, s = 0 for none).  While m is -inf the exponents are
+// taken against 0, where a -inf counts 0.  A NaN never enters m and makes s
+// NaN; so does +inf.
+struct Running {
+  float m, s;
+};
+// factor that brings a sum taken against m over to the maximum top >= m
+__device__ __forceinline__ float rebase(float m, float top, float c) {
+  return m == top ? 1.0f : exp2_hw((m - top) * c);
+}
+template <int N>
+__device__ __forceinline__ void running_add(Running& r, const float (&x)[N], float c) {
+  float top = r.m;
+#pragma unroll
+  for (int i = 0; i < N; i++) top = fmaxf(top, x[i]);
+  r.s *= rebase(r.m, top, c);
+  r.m = top;
+  const float at = top == kNegInf ? 0.0f : top;
+#pragma unroll
+  for (int i = 0; i < N; i++) r.s += exp2_hw((x[i] - at) * c);
+}
+__device__ __forceinline__ Running running_join(const Running& a, const Running& b, float c) {
+  Running r;
+  r.m = fmaxf(a.m, b.m);
+  r.s = a.s * rebase(a.m, r.m, c) + b.s * rebase(b.m, r.m, c);
+  return r;
+}
+__device__ __forceinline__ Running wave_running(Running r, float c) {
+  const float top = wave_max(r.m);
+  r.s = wave_sum(r.s * rebase(r.m, top, c));
+  r.m = top;
+  return r;
+}
+
+}  // namespace simar

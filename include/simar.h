@@ -430,6 +430,121 @@ int sim_verify_schedule(int algo, int p, char* diag, size_t diag_len);
 int sim_verify_custom(int algo, int p, int nchunks, int rounds, int nsteps, const int* counts,
                       const int* xfers, char* diag, size_t diag_len);
 
+/* ---- routing and losses --------------------------------------------------
+ * The arithmetic of a data-parallel training step that stands next to the
+ * collectives: each call makes a rank's small statistic that the collectives
+ * then combine over the ranks, or turns the combined statistic into a loss
+ * and a gradient.  One call serves one rank's data.
+ *
+ *   sim_route -> counts, prob_sums -> sim_allreduce (int32, fp32; sum)
+ *             -> sim_route_grad -> loss, dlogits
+ *   sim_distill_step                            (a rank holds whole rows)
+ *   sim_distill_parts -> sim_all_gather -> sim_distill_join
+ *                     -> sim_distill_grad       (a rank holds a vocabulary shard)
+ *
+ * They follow the conventions at the top of this file (sim_init first,
+ * asynchronous on `stream`, nothing enqueued on an error, capture allowed),
+ * with these differences:
+ *   - Logits and their gradients are rows of `dtype` (SIM_FP32, SIM_FP16 or
+ *     SIM_BF16; int32 is SIM_ERR_INVALID_ARG) whose starts lie row_stride
+ *     elements apart, row_stride >= the row's columns; they and every other
+ *     array need only the alignment of their own elements (SIM_ERR_ALIGN).
+ *     The other arrays are contiguous.
+ *   - A gradient may be written over its logits (same address and stride).
+ *     Any other overlap of an output with an input or another output is
+ *     SIM_ERR_ALIAS.
+ *   - Statistics are fp32 whatever `dtype` is, and every sum is taken in an
+ *     order that depends on the sizes alone: the same call on the same data
+ *     gives the same bits.
+ *   - Library memory is not used.  `work` is the caller's scratch of at
+ *     least the bytes the matching *_work function says (0: it may be NULL),
+ *     4-byte aligned, free for reuse once the call's stream work is done;
+ *     too little is SIM_ERR_NOMEM.
+ *   - Rows are processed where 0 rows is a no-op apart from the outputs that
+ *     do not depend on the row count (zero counts and sums, the loss).
+ */
+#define SIM_ROUTE_MAX_EXPERTS 1024
+#define SIM_ROUTE_MAX_TOPK 32
+#define SIM_DISTILL_MAX_TOPK 256
+
+/* Softmax gate of `tokens` rows of `experts` logits x.  With p the softmax of
+ * a row, the topk experts with the largest logits are chosen (ties: the
+ * lowest index; -inf and NaN are never chosen):
+ *   chosen[t][j]   the j-th largest logit's expert; -1 where fewer than topk
+ *                  can be chosen
+ *   weights[t][j]  p at chosen[t][j], divided by the row's sum of those where
+ *                  `normalize`; 0 where chosen is -1
+ *   counts[e]      (t, j) pairs with chosen[t][j] == e; counts[experts] is
+ *                  the number of rows that are not empty
+ *   prob_sums[e]   sum of p_te over the rows that are not empty
+ * A row is empty if keep (may be NULL: all kept) is 0 for it, whatever its
+ * logits hold, or if all its logits are -inf: chosen -1, weights 0, nothing
+ * counted.  A NaN or +inf logit of a kept row makes the row's p NaN. */
+int sim_route_work(int64_t tokens, int experts, int topk, int dtype, size_t* bytes);
+int sim_route(const void* logits, int64_t row_stride, int dtype, const uint8_t* keep, int64_t tokens, int experts,
+              int topk, int normalize, int32_t* chosen, float* weights, int32_t* counts, float* prob_sums,
+              void* work, size_t work_bytes, void* stream);
+
+/* Balance loss of the (reduced) statistics, and the gradient of that loss and
+ * of the weights for one rank's logits.  With N = counts[experts] and
+ * f_e = experts * counts[e] / (topk * N) (a constant of the gradient):
+ *   loss[0]      = coef * sum_e f_e * prob_sums[e] / N     (0 where N is 0)
+ *   dlogits[t]   = the gradient of  coef / N * sum_e f_e p_te
+ *                                   + sum_j dweights[t][j] * weights[t][j]
+ * `chosen` and `normalize` are sim_route's (a row's chosen experts are
+ * different ones; an index outside [0, experts) is an empty slot).  counts
+ * and prob_sums may both be NULL (then loss may be: no balance term, loss 0),
+ * and so may dweights (no weight term).  Empty rows get zeros. */
+int sim_route_grad(const void* logits, int64_t row_stride, int dtype, const uint8_t* keep, int64_t tokens,
+                   int experts, int topk, int normalize, const int32_t* chosen, const float* dweights,
+                   const int32_t* counts, const float* prob_sums, float coef, void* dlogits, int64_t drow_stride,
+                   float* loss, void* stream);
+
+/* Distillation from a teacher's topk largest logits.  ids[rows][topk] and
+ * teacher[rows][topk] (teacher_dtype: SIM_FP32, SIM_FP16 or SIM_BF16) are a
+ * row's slots; a slot whose id is outside [0, vocab) is empty and its logit is
+ * not used.  With q the softmax of teacher/temperature over the row's slots
+ * and p the softmax of logits/temperature over the whole vocabulary:
+ *   loss[t]       = sum_k q_k (log q_k - log p[ids_k])     (terms of q_k = 0
+ *                   are dropped)
+ *   dlogits[t][v] = coef * row_scale[t] / temperature *
+ *                   (p_v - the sum of q_k over the slots with id v)
+ * row_scale (may be NULL: all 1) is the upstream gradient of loss[t]; neither
+ * it nor coef scales loss.  A row with no slot, or with teacher logits of
+ * -inf in all of them, has loss 0 and a zero gradient whatever its logits
+ * hold (its logits are not read).  Otherwise a NaN, a +inf or a row of -inf
+ * alone makes that row's loss and gradient NaN; an id whose own logit is -inf
+ * makes the loss +inf.
+ *
+ * sim_distill_step: rows of the whole vocabulary, loss and gradient. */
+int sim_distill_work(int64_t rows, int64_t columns, int dtype, size_t* bytes);
+int sim_distill_step(const void* logits, int64_t row_stride, int dtype, int64_t rows, int64_t vocab,
+                     const int32_t* ids, const void* teacher, int teacher_dtype, int topk, float temperature,
+                     const float* row_scale, float coef, void* dlogits, int64_t drow_stride, float* loss,
+                     void* work, size_t work_bytes, void* stream);
+
+/* The same over vocabulary shards: the logits hold columns [first,
+ * first + columns) of the vocabulary.
+ *   sim_distill_parts  parts[4][rows] of the shard: the largest logit m, the
+ *                      sum of exp((x - m)/temperature), the sum of q_k over
+ *                      the slots in the shard, and the sum of
+ *                      q_k (x[ids_k] - m)/temperature over them
+ *   sim_distill_join   parts[nparts][4][rows] of all shards (in rank order,
+ *                      as sim_all_gather leaves them) -> loss[rows] and
+ *                      norm[2][rows]: the row's largest logit and the sum of
+ *                      exp((x - largest)/temperature)
+ *   sim_distill_grad   norm -> the gradient of the shard's columns */
+int sim_distill_parts(const void* logits, int64_t row_stride, int dtype, int64_t rows, int64_t columns,
+                      int64_t first, int64_t vocab, const int32_t* ids, const void* teacher, int teacher_dtype,
+                      int topk, float temperature, float* parts, void* work, size_t work_bytes, void* stream);
+int sim_distill_join(const float* parts, int nparts, int64_t rows, int64_t vocab, const int32_t* ids,
+                     const void* teacher, int teacher_dtype, int topk, float temperature, float* loss, float* norm,
+                     void* stream);
+int sim_distill_grad(const void* logits, int64_t row_stride, int dtype, int64_t rows, int64_t columns,
+                     int64_t first, int64_t vocab, const int32_t* ids, const void* teacher, int teacher_dtype,
+                     int topk, float temperature, const float* norm, const float* row_scale, float coef,
+                     void* dlogits, int64_t drow_stride, void* stream);
+
 /* ---- test hooks --------------------------------------------------------- */
 enum {
   SIM_DEBUG_EPOCH = 0,         /* set the LL epoch counter (next call uses value+1) */
