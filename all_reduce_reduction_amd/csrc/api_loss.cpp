@@ -203,9 +203,14 @@ int sim_distill_step(const void* logits, int64_t row_stride, int dtype, int64_t 
   a.splits = distill_splits(rows, vocab, dtype);
   a.span = distill_span(vocab, a.splits);
   if ((int64_t)a.splits * rows > kMaxGrid) return SIM_ERR_INVALID_ARG;
-  const hipError_t e = launch_distill_stats(a, dtype, (hipStream_t)stream);
+  const hipStream_t s = (hipStream_t)stream;
+  if (distill_whole_rows(rows, vocab, dtype))
+    return hip_status(dtype == SIM_FP32   ? launch_distill_row_fp32(a, s)
+                      : dtype == SIM_FP16 ? launch_distill_row_fp16(a, s)
+                                          : launch_distill_row_bf16(a, s));
+  const hipError_t e = launch_distill_stats(a, dtype, s);
   if (e != hipSuccess) return SIM_ERR_HIP;
-  return hip_status(launch_distill_grad(a, dtype, (hipStream_t)stream));
+  return hip_status(launch_distill_grad(a, dtype, s));
 }
 
 int sim_distill_parts(const void* logits, int64_t row_stride, int dtype, int64_t rows, int64_t columns,

@@ -1,0 +1,190 @@
+// distill_row.h -- a distillation step with one workgroup per row (gfx950):
+// the row is read once, stays in registers while its maximum and sum are
+// found, and its gradient is written from there, so that a step moves the
+// logits' bytes twice instead of three times.
+//
+// A workgroup of NT threads holds R 16-byte vectors per thread: 16 vectors
+// are 64 of the 128 VGPRs that four waves per SIMD leave, and 1024 threads of
+// them hold a row of 256 KiB (131,072 16-bit logits).  What a row has beyond
+// NT * R vectors is read a second time for its gradient.
+//
+// While the row's loads are in flight, wave 0 reads the slots and their own
+// logits (before anything is written: the gradient may lie on the logits) and
+// hangs each slot on the thread that holds its column.  A thread writes its
+// vectors and then the full values of its slots' columns: its own stores to
+// one address stay in order, so no barrier is needed behind the stores.
+#pragma once
+
+#include "distill_device.h"
+#include "launch.h"
+
+namespace simar {
+
+template <int DT> constexpr uint32_t neg_inf_bits() {
+  return DT == SIM_FP32 ? 0xff800000u : DT == SIM_FP16 ? 0xfc00fc00u : 0xff80ff80u;
+}
+
+// the vectors of a row that may reach past its end
+template <int DT>
+__device__ __forceinline__ u32x4 load_guarded(const void* row, int64_t col, int64_t cols) {
+  constexpr int V = epv<DT>();
+  const uint32_t n = neg_inf_bits<DT>();
+  u32x4 v = {n, n, n, n};
+  if (col + V <= cols) {
+    v = ld_row<DT>(row, col);
+  } else if (col < cols) {
+    float x[V];
+    load_cols<DT>(row, col, cols, x);
+    v = pack<DT>(x);
+  }
+  return v;
+}
+template <int DT>
+__device__ __forceinline__ void store_guarded(void* row, int64_t col, int64_t cols, const float (&x)[epv<DT>()]) {
+  constexpr int V = epv<DT>();
+  if (col + V <= cols) {
+    st_row<DT>(row, col, pack<DT>(x));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i++)
+      if (col + i < cols) store_elem<DT>(row, col + i, x[i]);
+  }
+}
+
+// of the R vectors of a thread, the last GUARD may lie past the row's end
+template <int DT, int NT, int R, int GUARD>
+__global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
+  constexpr int V = epv<DT>(), W = NT / 64;
+  __shared__ int head[NT];
+  __shared__ int next_s[SIM_DISTILL_MAX_TOPK], id_s[SIM_DISTILL_MAX_TOPK];
+  __shared__ float q_s[SIM_DISTILL_MAX_TOPK], x_s[SIM_DISTILL_MAX_TOPK];
+  __shared__ float m_s[W], s_s[W];
+  __shared__ int live_s;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t row = blockIdx.x;
+  const void* x = row_at(a.x, row, a.stride, Ty<DT>::E);
+  void* dx = row_at(a.dx, row, a.dstride, Ty<DT>::E);
+  const float c = kLog2e / a.tau;
+  const float up = (a.row_scale ? a.row_scale[row] : 1.0f) * (a.coef / a.tau);
+  u32x4 v[R];
+#pragma unroll
+  for (int i = 0; i < R; i++) {
+    if (i < R - GUARD) v[i] = ld_row_lane<DT>(x, i * NT * V, tid * V);
+    else v[i] = load_guarded<DT>(x, (int64_t)(i * NT + tid) * V, a.cols);
+  }
+  head[tid] = -1;
+  Slots sl;
+  if (wave == 0) {
+    sl = load_slots(a, row, lane);
+#pragma unroll
+    for (int i = 0; i < kSlotsPerLane; i++) {
+      const int k = lane + 64 * i;
+      if (k < a.topk) {
+        id_s[k] = sl.id[i];
+        q_s[k] = sl.q[i];
+        if (sl.id[i] >= 0) x_s[k] = load_elem<DT>(x, sl.id[i]);
+      }
+    }
+    if (lane == 0) live_s = sl.live;
+  }
+  Running r{kNegInf, 0.0f};
+#pragma unroll
+  for (int i = 0; i < R; i++) {
+    float f[V];
+    unpack<DT>(v[i], f);
+    running_add(r, f, c);
+  }
+  for (int64_t col = (int64_t)(R * NT + tid) * V; col < a.cols; col += NT * V) {
+    float f[V];
+    load_cols<DT>(x, col, a.cols, f);
+    running_add(r, f, c);
+  }
+  r = wave_running(r, c);
+  if (lane == 0) {
+    m_s[wave] = r.m;
+    s_s[wave] = r.s;
+  }
+  __syncthreads();
+  r.m = lane < W ? m_s[lane] : kNegInf;
+  r.s = lane < W ? s_s[lane] : 0.0f;
+  r = wave_running(r, c);
+  const bool live = live_s;
+  if (wave == 0) {
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSlotsPerLane; i++) {
+      const int k = lane + 64 * i;
+      if (sl.id[i] < 0) continue;
+      const float at = x_s[k];
+      if (!(sl.q[i] == 0.0f)) dot += at == kNegInf ? sl.q[i] * kNegInf : sl.q[i] * ((at - r.m) / a.tau);
+      // the slots with this id, in their order
+      float q = 0.0f;
+      for (int j = 0; j < a.topk; j++)
+        if (id_s[j] == sl.id[i]) q += q_s[j];
+      if (live) {
+        x_s[k] = up * (exp2_hw((at - r.m) * c) / r.s - q);
+        next_s[k] = atomicExch(&head[(sl.id[i] / V) % NT], k);
+      }
+    }
+    dot = wave_sum(dot);
+    if (lane == 0) a.loss[row] = live ? sl.entropy + __logf(r.s) - dot : 0.0f;
+  }
+  const float k2 = live ? up / r.s : 0.0f;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < R; i++) {
+    // widened again here: kept from above, the fp32 values would take the
+    // registers of two more rows
+    asm volatile("" : "+v"(v[i]));
+    float f[V];
+    unpack<DT>(v[i], f);
+#pragma unroll
+    for (int j = 0; j < V; j++) f[j] = live ? exp2_hw((f[j] - r.m) * c) * k2 : 0.0f;
+    if (i < R - GUARD) st_row_lane<DT>(dx, i * NT * V, tid * V, pack<DT>(f));
+    else store_guarded<DT>(dx, (int64_t)(i * NT + tid) * V, a.cols, f);
+  }
+  for (int64_t col = (int64_t)(R * NT + tid) * V; col < a.cols; col += NT * V) {
+    float f[V];
+    load_cols<DT>(x, col, a.cols, f);
+#pragma unroll
+    for (int j = 0; j < V; j++) f[j] = live ? exp2_hw((f[j] - r.m) * c) * k2 : 0.0f;
+    store_guarded<DT>(dx, col, a.cols, f);
+  }
+  for (int k = head[tid]; k >= 0; k = next_s[k]) store_elem<DT>(dx, id_s[k], x_s[k]);
+}
+
+// The workgroup and the vectors per thread for a row of n vectors: the
+// smallest workgroup that holds it in 16 vectors per thread.  R comes in
+// steps of 2 from 4 on, so the last two vectors of a thread may lie past the
+// row's end.
+template <int DT, int NT, int R>
+hipError_t launch_row_as(const DistillArgs& a, hipStream_t s) {
+  constexpr int G = R < 4 ? 1 : 2;
+  return launch<k_distill_row<DT, NT, R, G>>(dim3((unsigned)a.rows), dim3(NT), s, a);
+}
+template <int DT, int NT, bool SHORT>
+hipError_t launch_row_with(const DistillArgs& a, int64_t vectors, hipStream_t s) {
+  const int r = (int)((vectors + NT - 1) / NT);
+  if constexpr (SHORT) {
+    if (r <= 1) return launch_row_as<DT, NT, 1>(a, s);
+    if (r <= 2) return launch_row_as<DT, NT, 2>(a, s);
+    if (r <= 3) return launch_row_as<DT, NT, 3>(a, s);
+  }
+  if (r <= 4) return launch_row_as<DT, NT, 4>(a, s);
+  if (r <= 6) return launch_row_as<DT, NT, 6>(a, s);
+  if (r <= 8) return launch_row_as<DT, NT, 8>(a, s);
+  if (r <= 10) return launch_row_as<DT, NT, 10>(a, s);
+  if (r <= 12) return launch_row_as<DT, NT, 12>(a, s);
+  if (r <= 14) return launch_row_as<DT, NT, 14>(a, s);
+  return launch_row_as<DT, NT, 16>(a, s);
+}
+template <int DT>
+hipError_t launch_row(const DistillArgs& a, hipStream_t s) {
+  const int64_t n = (a.cols + epv<DT>() - 1) / epv<DT>();
+  if (n <= 64 * 16) return launch_row_with<DT, 64, true>(a, n, s);
+  if (n <= 256 * 16) return launch_row_with<DT, 256, false>(a, n, s);
+  if (n <= 512 * 16) return launch_row_with<DT, 512, false>(a, n, s);
+  return launch_row_with<DT, 1024, false>(a, n, s);
+}
+
+}  // namespace simar

@@ -78,6 +78,11 @@ int64_t distill_span(int64_t cols, int splits);
 hipError_t launch_distill_stats(const DistillArgs& a, int dtype, hipStream_t s);
 hipError_t launch_distill_join(const DistillArgs& a, float* loss, float* norm, hipStream_t s);
 hipError_t launch_distill_grad(const DistillArgs& a, int dtype, hipStream_t s);
+// one workgroup per row: statistics and gradient in one launch
+bool distill_whole_rows(int64_t rows, int64_t cols, int dtype);
+hipError_t launch_distill_row_fp32(const DistillArgs& a, hipStream_t s);
+hipError_t launch_distill_row_fp16(const DistillArgs& a, hipStream_t s);
+hipError_t launch_distill_row_bf16(const DistillArgs& a, hipStream_t s);
 // a shard's parts from those of its splits
 hipError_t launch_distill_merge(const DistillArgs& a, float* out, hipStream_t s);
 

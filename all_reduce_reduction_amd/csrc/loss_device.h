@@ -37,6 +37,19 @@ __device__ __forceinline__ void st_row(void* row, int64_t elem, u32x4 v) {
   *(typename RowVec<Ty<DT>::E>::G*)((char*)row + elem * Ty<DT>::E) = v;
 }
 
+// The same with a workgroup-uniform element offset (kept in scalar registers)
+// and a lane's own, which has 32 bits.
+template <int DT>
+__device__ __forceinline__ u32x4 ld_row_lane(const void* row, int64_t elem, uint32_t lane_elem) {
+  const char* p = (const char*)row + elem * Ty<DT>::E;
+  return *(typename RowVec<Ty<DT>::E>::CG*)(p + lane_elem * (uint32_t)Ty<DT>::E);
+}
+template <int DT>
+__device__ __forceinline__ void st_row_lane(void* row, int64_t elem, uint32_t lane_elem, u32x4 v) {
+  char* p = (char*)row + elem * Ty<DT>::E;
+  *(typename RowVec<Ty<DT>::E>::G*)(p + lane_elem * (uint32_t)Ty<DT>::E) = v;
+}
+
 // 2^x (v_exp_f32: 1 ulp; results below the normal range are flushed, far
 // under what a sum that holds 1 can see)
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
