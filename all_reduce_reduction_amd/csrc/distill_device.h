@@ -65,19 +65,6 @@ __device__ __forceinline__ Slots load_slots(const DistillArgs& a, int64_t row, i
   return s;
 }
 
-// The columns [lo, hi) of a row, EPV at a time; what lies outside reads as
-// -inf (which changes no maximum and no sum).
-template <int DT>
-__device__ __forceinline__ void load_cols(const void* row, int64_t col, int64_t hi, float (&x)[epv<DT>()]) {
-  constexpr int V = epv<DT>();
-  if (col + V <= hi) {
-    unpack<DT>(ld_row<DT>(row, col), x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; i++) x[i] = col + i < hi ? load_elem<DT>(row, col + i) : kNegInf;
-  }
-}
-
 __device__ __forceinline__ void* row_at(const void* base, int64_t row, int64_t stride, int esize) {
   return (char*)base + row * stride * esize;
 }

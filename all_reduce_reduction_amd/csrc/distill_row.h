@@ -20,37 +20,6 @@
 
 namespace simar {
 
-template <int DT> constexpr uint32_t neg_inf_bits() {
-  return DT == SIM_FP32 ? 0xff800000u : DT == SIM_FP16 ? 0xfc00fc00u : 0xff80ff80u;
-}
-
-// the vectors of a row that may reach past its end
-template <int DT>
-__device__ __forceinline__ u32x4 load_guarded(const void* row, int64_t col, int64_t cols) {
-  constexpr int V = epv<DT>();
-  const uint32_t n = neg_inf_bits<DT>();
-  u32x4 v = {n, n, n, n};
-  if (col + V <= cols) {
-    v = ld_row<DT>(row, col);
-  } else if (col < cols) {
-    float x[V];
-    load_cols<DT>(row, col, cols, x);
-    v = pack<DT>(x);
-  }
-  return v;
-}
-template <int DT>
-__device__ __forceinline__ void store_guarded(void* row, int64_t col, int64_t cols, const float (&x)[epv<DT>()]) {
-  constexpr int V = epv<DT>();
-  if (col + V <= cols) {
-    st_row<DT>(row, col, pack<DT>(x));
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; i++)
-      if (col + i < cols) store_elem<DT>(row, col + i, x[i]);
-  }
-}
-
 // of the R vectors of a thread, the last GUARD may lie past the row's end
 template <int DT, int NT, int R, int GUARD>
 __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
@@ -70,7 +39,7 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
 #pragma unroll
   for (int i = 0; i < R; i++) {
     if (i < R - GUARD) v[i] = ld_row_lane<DT>(x, i * NT * V, tid * V);
-    else v[i] = load_guarded<DT>(x, (int64_t)(i * NT + tid) * V, a.cols);
+    else v[i] = ld_guarded<DT>(x, (int64_t)(i * NT + tid) * V, a.cols);
   }
   head[tid] = -1;
   Slots sl;
@@ -141,14 +110,14 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
 #pragma unroll
     for (int j = 0; j < V; j++) f[j] = live ? exp2_hw((f[j] - r.m) * c) * k2 : 0.0f;
     if (i < R - GUARD) st_row_lane<DT>(dx, i * NT * V, tid * V, pack<DT>(f));
-    else store_guarded<DT>(dx, (int64_t)(i * NT + tid) * V, a.cols, f);
+    else st_guarded<DT>(dx, (int64_t)(i * NT + tid) * V, a.cols, f);
   }
   for (int64_t col = (int64_t)(R * NT + tid) * V; col < a.cols; col += NT * V) {
     float f[V];
     load_cols<DT>(x, col, a.cols, f);
 #pragma unroll
     for (int j = 0; j < V; j++) f[j] = live ? exp2_hw((f[j] - r.m) * c) * k2 : 0.0f;
-    store_guarded<DT>(dx, col, a.cols, f);
+    st_guarded<DT>(dx, col, a.cols, f);
   }
   for (int k = head[tid]; k >= 0; k = next_s[k]) store_elem<DT>(dx, id_s[k], x_s[k]);
 }

@@ -4,14 +4,20 @@
 // Forward, row x: m = max x, Z = sum exp(x - m), p = exp(x - m) / Z; the topk
 // largest logits by value, ties to the lowest index, taken from the logits
 // themselves, so that the choice does not depend on any rounding.  Counts are
-// integers; probability sums are taken per lane over the rows of a wave, then
-// over the waves of a workgroup, then over the workgroups, in that order, so
+// integers; probability sums are taken per lane over its rows, then over the
+// lanes and waves of a workgroup, then over the workgroups, in that order, so
 // they do not depend on timing.
 //
 // Gradient: with g_e = coef f_e / N,
 //   dx_e = p_e (g_e + u_e - sum_j p_j (g_j + u_j)),  u = dweights at chosen e,
 // for raw weights; for normalised ones w = p / (their sum over the chosen),
 //   dx_e = p_e (g_e - sum_j p_j g_j) + [e chosen] w_e (dw_e - sum_i w_i dw_i).
+//
+// Layout: L lanes take a row and a wave 64 / L rows; a lane holds N logits as
+// 16-byte vectors, vector j of lane l being the row's vector j L + l, so that
+// a group's loads cover whole lines.  With many rows per wave the cross-lane
+// steps of one row (log2 L of them) serve 64 / L rows at once, and they run
+// over DPP while L is 8 or 16.
 #include "device_common.h"
 #include "launch.h"
 #include "loss.h"
@@ -22,237 +28,496 @@ namespace {
 
 constexpr int kWaves = kBlock / 64;
 
-// One wave per row; lane l holds the experts l, l + 64, ...: N of them.
-template <int DT, int N>
-__device__ __forceinline__ bool load_row(const void* base, int64_t row, int64_t stride, int experts,
-                                         const uint8_t* keep, int lane, float (&x)[N]) {
-  const char* r = (const char*)base + row * stride * Ty<DT>::E;
-  const bool kept = !keep || keep[row];
-  bool some = false;
+template <int DT, int L, int N>
+struct Gate {
+  static constexpr int V = epv<DT>(), NV = N / V, kRows = 64 / L, kAll = L * N;
+  u32x4 v[NV];
+
+  static __device__ __forceinline__ int col(int j, int l) { return (j * L + l) * V; }
+
+  __device__ __forceinline__ void load(const void* row, int experts, int l) {
+    if (experts == kAll) {
 #pragma unroll
-  for (int i = 0; i < N; i++) {
-    const int e = lane + 64 * i;
-    x[i] = kept && e < experts ? load_elem<DT>(r, e) : kNegInf;
-    some = some || !(x[i] == kNegInf);
+      for (int j = 0; j < NV; j++) v[j] = ld_row<DT>(row, col(j, l));
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; j++) v[j] = ld_guarded<DT>(row, col(j, l), experts);
+    }
   }
-  return __any(some);
+  __device__ __forceinline__ void blank() {
+    constexpr uint32_t n = neg_inf_bits<DT>();
+#pragma unroll
+    for (int j = 0; j < NV; j++) v[j] = u32x4{n, n, n, n};
+  }
+  __device__ __forceinline__ void logits(float (&x)[N]) const {
+#pragma unroll
+    for (int j = 0; j < NV; j++) {
+      float f[V];
+      unpack<DT>(v[j], f);
+#pragma unroll
+      for (int t = 0; t < V; t++) x[j * V + t] = f[t];
+    }
+  }
+};
+
+// A float's bits as an unsigned integer that grows with its value (a 16-bit
+// type's in the upper half); both zeros get the same one.  NaN with the sign
+// clear lies above +inf, with the sign set below -inf.
+template <int DT>
+__device__ __forceinline__ uint32_t ordered(uint32_t bits) {
+  if constexpr (DT == SIM_FP32) return (bits ^ ((uint32_t)((int32_t)bits >> 31) | 0x80000000u)) + (bits >> 31);
+  else return ((bits ^ ((bits >> 15) * 0x7fffu | 0x8000u)) + (bits >> 15)) << 16;
+}
+template <int DT> constexpr uint32_t ordered_inf() {
+  return DT == SIM_FP32 ? 0xff800000u : DT == SIM_FP16 ? 0xfc000000u : 0xff800000u;
+}
+template <int DT> constexpr uint32_t ordered_neg_inf() {
+  return DT == SIM_FP32 ? 0x00800000u : DT == SIM_FP16 ? 0x04000000u : 0x00800000u;
+}
+template <int DT>
+__device__ __forceinline__ float from_ordered16(uint32_t key) {
+  const uint32_t h = key >> 16;
+  return widen_bits<DT>(h & 0x8000u ? h ^ 0x8000u : 0x10000u - h);
 }
 
-template <int N>
-__device__ __forceinline__ float softmax(const float (&x)[N], float (&p)[N]) {
-  float top = kNegInf;
+// ---- the eight largest of a group -----------------------------------------------
+__device__ __forceinline__ void order2(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b);
+  b = min(a, b);
+  a = hi;
+}
+// any eight keys, largest first (19 exchanges)
+__device__ __forceinline__ void sort8(uint32_t (&k)[8]) {
+  order2(k[0], k[1]); order2(k[2], k[3]); order2(k[4], k[5]); order2(k[6], k[7]);
+  order2(k[0], k[2]); order2(k[1], k[3]); order2(k[4], k[6]); order2(k[5], k[7]);
+  order2(k[1], k[2]); order2(k[5], k[6]);
+  order2(k[0], k[4]); order2(k[1], k[5]); order2(k[2], k[6]); order2(k[3], k[7]);
+  order2(k[2], k[4]); order2(k[3], k[5]);
+  order2(k[1], k[2]); order2(k[3], k[4]); order2(k[5], k[6]);
+}
+// a bitonic sequence of eight, largest first
+__device__ __forceinline__ void sort8_bitonic(uint32_t (&k)[8]) {
+  order2(k[0], k[4]); order2(k[1], k[5]); order2(k[2], k[6]); order2(k[3], k[7]);
+  order2(k[0], k[2]); order2(k[1], k[3]); order2(k[4], k[6]); order2(k[5], k[7]);
+  order2(k[0], k[1]); order2(k[2], k[3]); order2(k[4], k[5]); order2(k[6], k[7]);
+}
+// the eight largest of two sorted eights: the larger of each element and its
+// counterpart from the other end
+template <class F>
+__device__ __forceinline__ void merge8(uint32_t (&k)[8], F other) {
+  uint32_t o[8];
 #pragma unroll
-  for (int i = 0; i < N; i++) top = fmaxf(top, x[i]);
-  top = wave_max(top);
-  float z = 0.0f;
+  for (int i = 0; i < 8; i++) o[i] = other(k[7 - i], 7 - i);
 #pragma unroll
-  for (int i = 0; i < N; i++) {
-    p[i] = exp2_hw((x[i] - top) * kLog2e);
-    z += p[i];
-  }
-  z = wave_sum(z);
-#pragma unroll
-  for (int i = 0; i < N; i++) p[i] = p[i] / z;
-  return z;
+  for (int i = 0; i < 8; i++) k[i] = max(k[i], o[i]);
+  sort8_bitonic(k);
 }
 
-template <int DT, int N>
+// Keys that put the value above the distance of the index from the last one,
+// so that a larger key is a larger logit or, among equal ones, a lower index.
+// 16-bit values fit whole; fp32 values lose their log2(L N) lowest bits, and
+// the caller checks that what is left tells the chosen ones apart.
+template <int DT, int L, int N>
+__device__ __forceinline__ void top8(const Gate<DT, L, N>& g, int l, uint32_t (&top)[8]) {
+  typedef Gate<DT, L, N> G;
+  constexpr int V = G::V;
+#pragma unroll
+  for (int b = 0; b < N / 8; b++) {
+    uint32_t k[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const int at = b * 8 + i, j = at / V, t = at % V;
+      const uint32_t low = (uint32_t)((G::NV - 1 - j) * L * V + (V - 1 - t));
+      if constexpr (Ty<DT>::E == 4) {
+        k[i] = (ordered<DT>(g.v[j][t]) & ~(uint32_t)(G::kAll - 1)) | low;
+      } else {
+        // both halves of a word are ordered at once
+        const uint32_t w = g.v[j][t / 2], s = w & 0x80008000u;
+        const uint32_t o = (w ^ ((s - (s >> 15)) | 0x80008000u)) + (s >> 15);
+        k[i] = (t & 1 ? o & 0xffff0000u : o << 16) | low;
+      }
+    }
+    sort8(k);
+    if (b == 0) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) top[i] = k[i];
+    } else {
+      merge8(top, [&](uint32_t, int i) { return k[i]; });
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i++) top[i] |= (uint32_t)((L - 1 - l) * V);
+  merge8(top, [](uint32_t k, int) { return dpp<kDppPair>(k); });
+  merge8(top, [](uint32_t k, int) { return dpp<kDppQuad>(k); });
+  merge8(top, [](uint32_t k, int) { return dpp<kDppHalfRow>(k); });
+  if constexpr (L >= 16) merge8(top, [](uint32_t k, int) { return dpp<kDppRow>(k); });
+  if constexpr (L >= 32) merge8(top, [](uint32_t k, int) { return (uint32_t)__shfl_xor((int)k, 16, 64); });
+}
+
+// The topk largest one after the other, exactly, for any topk: lane l gets
+// slots l, l + L, ...  NaN and -inf are never taken.
+template <int DT, int L, int N, int S>
+__device__ __forceinline__ void top_in_turn(const Gate<DT, L, N>& g, int l, int topk, int (&mine)[S]) {
+  typedef Gate<DT, L, N> G;
+  constexpr int V = G::V;
+  uint32_t k[N];
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    const int j = i / V, t = i % V;
+    if constexpr (Ty<DT>::E == 4) k[i] = ordered<DT>(g.v[j][t]);
+    else k[i] = ordered<DT>((t & 1) ? g.v[j][t / 2] >> 16 : g.v[j][t / 2] & 0xffffu);
+    if (k[i] <= ordered_neg_inf<DT>() || k[i] > ordered_inf<DT>()) k[i] = 0;
+  }
+#pragma unroll
+  for (int s = 0; s < S; s++) mine[s] = -1;
+  for (int r = 0; r < topk; r++) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < N; i++) best = max(best, k[i]);
+    best = group_reduce<L>(best, [](uint32_t a, uint32_t b) { return max(a, b); });
+    uint32_t at = 0xffffffffu;
+#pragma unroll
+    for (int i = N - 1; i >= 0; i--)
+      if (k[i] == best) at = G::col(i / V, l) + i % V;
+    at = group_reduce<L>(at, [](uint32_t a, uint32_t b) { return min(a, b); });
+#pragma unroll
+    for (int i = 0; i < N; i++)
+      if (at == (uint32_t)(G::col(i / V, l) + i % V)) k[i] = 0;
+#pragma unroll
+    for (int s = 0; s < S; s++)
+      if (r == l + L * s && best != 0) mine[s] = (int)at;
+    if (!__any(best != 0)) break;
+  }
+}
+
+// ---- forward ------------------------------------------------------------------------
+template <int DT, int L, int N, bool EIGHT>
 __global__ void __launch_bounds__(kBlock) k_route(RouteArgs a) {
-  __shared__ uint32_t count_s[SIM_ROUTE_MAX_EXPERTS + 1];
-  __shared__ float sum_s[kWaves][64 * N];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int e = tid; e <= a.experts; e += kBlock) count_s[e] = 0;
+  typedef Gate<DT, L, N> G;
+  constexpr int S = EIGHT ? 1 : (SIM_ROUTE_MAX_TOPK + L - 1) / L;
+  __shared__ uint32_t count_s[G::kAll + 1];
+  __shared__ float sum_s[kWaves * G::kRows][G::kAll];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & (L - 1);
+  for (int e = tid; e <= G::kAll; e += kBlock) count_s[e] = 0;
   __syncthreads();
   float sums[N];
 #pragma unroll
   for (int i = 0; i < N; i++) sums[i] = 0.0f;
-  const int64_t step = (int64_t)a.workgroups * kWaves;
-  for (int64_t row = (int64_t)blockIdx.x * kWaves + wave; row < a.tokens; row += step) {
-    float x[N], p[N];
-    const bool live = load_row<DT, N>(a.x, row, a.stride, a.experts, a.keep, lane, x);
-    int mine = -1;
-    float w = 0.0f;
-    if (live) {
-      const float z = softmax(x, p);
-      for (int j = 0; j < a.topk; j++) {
-        float best = kNegInf;
-        int at = -1;
+  uint32_t rows = 0;
+  const int64_t step = (int64_t)a.workgroups * kWaves * G::kRows;
+  for (int64_t first = ((int64_t)blockIdx.x * kWaves + wave) * G::kRows; first < a.tokens; first += step) {
+    const bool here = first + lane / L < a.tokens;
+    const int64_t row = here ? first + lane / L : first;
+    const char* x = (const char*)a.x + row * a.stride * Ty<DT>::E;
+    G g;
+    g.load(x, a.experts, l);
+    const bool kept = here && (!a.keep || a.keep[row]);
+    if (!kept) g.blank();
+
+    // the chosen experts
+    int mine[S];
+    float at[S];
+    float top_logit = kNegInf;
+    bool in_turn = !EIGHT;
+    if constexpr (EIGHT) {
+      constexpr uint32_t m = Ty<DT>::E == 4 ? ~(uint32_t)(G::kAll - 1) : 0xffff0000u;  // a key's value bits
+      uint32_t top[8];
+      top8(g, l, top);
+      if constexpr (Ty<DT>::E == 4) {
+        // exact if the topk keys differ above the index, no other key shares
+        // the last one's value bits, and all of them are of finite logits
+        uint32_t last = top[0];
+        bool same = (top[0] & m) >= (ordered_inf<DT>() & m);
 #pragma unroll
-        for (int i = 0; i < N; i++)
-          if (x[i] > best) {
-            best = x[i];
-            at = lane + 64 * i;
+        for (int i = 1; i < 8; i++) {
+          if (i < a.topk) {
+            same = same || (top[i] & m) == (top[i - 1] & m);
+            last = top[i];
           }
-        const float top = wave_max(best);
-        // the lowest index among the lanes that hold the maximum
-        int e = best == top && at >= 0 ? at : INT32_MAX;
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) e = min(e, __shfl_xor(e, d, 64));
-        if (e == INT32_MAX) break;
-        float pe = 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; i++)
-          if (lane + 64 * i == e) {
-            pe = p[i];
-            x[i] = kNegInf;
-          }
-        pe = __shfl(pe, e & 63, 64);
-        if (lane == j) {
-          mine = e;
-          w = pe;
         }
-      }
-      if (a.normalize) {
-        const float total = wave_sum(w);
-        if (mine >= 0) w = z != z ? z : w / total;
-      }
-      if (mine >= 0) atomicAdd(&count_s[mine], 1u);
-      if (lane == 0) atomicAdd(&count_s[a.experts], 1u);
+        last &= m;
+        same = same || last <= (ordered_neg_inf<DT>() & m);
+        float n = 0.0f;
 #pragma unroll
-      for (int i = 0; i < N; i++) sums[i] += p[i];
+        for (int i = 0; i < N; i++) n += ordered<DT>(g.v[i / G::V][i % G::V]) >= last ? 1.0f : 0.0f;
+        in_turn = __any((same || group_sum<L>(n) != (float)a.topk) && kept);
+      } else {
+        in_turn = __any((top[0] & m) > ordered_inf<DT>());  // a NaN
+        top_logit = from_ordered16<DT>(top[0]);
+      }
+      uint32_t k = top[0];
+#pragma unroll
+      for (int i = 1; i < 8; i++) k = l == i ? top[i] : k;
+      const bool ok = l < a.topk && (k & m) > (ordered_neg_inf<DT>() & m);
+      mine[0] = ok ? G::kAll - 1 - (int)(k & (uint32_t)(G::kAll - 1)) : -1;
+      if constexpr (Ty<DT>::E == 2) at[0] = from_ordered16<DT>(k);
     }
-    if (lane < a.topk) {
-      a.chosen[row * a.topk + lane] = mine;
-      a.weights[row * a.topk + lane] = w;
+    if (in_turn) top_in_turn<DT, L, N, S>(g, l, a.topk, mine);
+
+    // the softmax
+    float f[N];
+    g.logits(f);
+    bool odd = false;
+    if (Ty<DT>::E == 4 || in_turn) {
+      top_logit = kNegInf;
+#pragma unroll
+      for (int i = 0; i < N; i++) top_logit = fmaxf(top_logit, f[i]);
+      top_logit = group_max<L>(top_logit);
+      // a row of NaN and -inf alone is not empty
+#pragma unroll
+      for (int i = 0; i < N; i++) odd = odd || f[i] != f[i];
+      odd = group_any<L>(odd, lane);
+    }
+    const bool live = odd || top_logit > kNegInf;
+    const float base = live ? top_logit : 0.0f;
+    float z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      f[i] = exp2_hw((f[i] - base) * kLog2e);
+      z += f[i];
+    }
+    z = group_sum<L>(z);
+    const float inv = live ? 1.0f / z : 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; i++) sums[i] = __builtin_fmaf(f[i], inv, sums[i]);
+    if (live && l == 0) rows++;
+
+    // the weights of the chosen
+    float w[S], total = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S; s++) {
+      if (Ty<DT>::E == 4 || in_turn) at[s] = mine[s] >= 0 ? load_elem<DT>(x, mine[s]) : 0.0f;
+      w[s] = mine[s] >= 0 ? exp2_hw((at[s] - base) * kLog2e) * inv : 0.0f;
+      total += w[s];
+    }
+    if (a.normalize) {
+      const float sum = group_sum<L>(total);
+#pragma unroll
+      for (int s = 0; s < S; s++)
+        if (mine[s] >= 0) w[s] = inv != inv ? inv : w[s] / sum;
+    }
+#pragma unroll
+    for (int s = 0; s < S; s++) {
+      const int slot = l + L * s;
+      if (here && slot < a.topk) {
+        a.chosen[row * a.topk + slot] = mine[s];
+        a.weights[row * a.topk + slot] = w[s];
+      }
+      if (mine[s] >= 0) atomicAdd(&count_s[mine[s]], 1u);
     }
   }
+  if (rows) atomicAdd(&count_s[G::kAll], rows);
 #pragma unroll
-  for (int i = 0; i < N; i++) sum_s[wave][lane + 64 * i] = sums[i];
+  for (int i = 0; i < N; i++) sum_s[wave * G::kRows + lane / L][G::col(i / G::V, l) + i % G::V] = sums[i];
   __syncthreads();
   uint32_t* part = a.partial + (int64_t)blockIdx.x * (2 * a.experts + 1);
   for (int e = tid; e <= a.experts; e += kBlock) {
     float s = 0.0f;
     if (e < a.experts) {
 #pragma unroll
-      for (int w = 0; w < kWaves; w++) s += sum_s[w][e];
+      for (int w = 0; w < kWaves * G::kRows; w++) s += sum_s[w][e];
     }
+    const uint32_t n = count_s[e < a.experts ? e : G::kAll];
     if (a.workgroups == 1) {
-      a.counts[e] = (int32_t)count_s[e];
+      a.counts[e] = (int32_t)n;
       if (e < a.experts) a.sums[e] = s;
     } else {
-      part[e] = count_s[e];
+      part[e] = n;
       if (e < a.experts) part[a.experts + 1 + e] = __builtin_bit_cast(uint32_t, s);
     }
   }
 }
 
-// one thread per counted value, over all workgroups in order
-__global__ void __launch_bounds__(kBlock) k_route_sum(RouteArgs a) {
-  const int e = blockIdx.x * kBlock + threadIdx.x, all = 2 * a.experts + 1;
-  if (e >= all) return;
+// The workgroups' counts and sums, kSumCols of them per workgroup: 1024
+// threads as kSumRows runs of rows by kSumCols columns, then the runs in order.
+constexpr int kSumCols = 16, kSumRows = 64;
+__global__ void __launch_bounds__(kSumCols* kSumRows) k_route_sum(RouteArgs a) {
+  __shared__ uint32_t n_s[kSumRows][kSumCols];
+  __shared__ float s_s[kSumRows][kSumCols];
+  const int all = 2 * a.experts + 1, c = threadIdx.x % kSumCols, r = threadIdx.x / kSumCols;
+  const int e = blockIdx.x * kSumCols + c;
+  const int span = (a.workgroups + kSumRows - 1) / kSumRows;
+  const int end = min(a.workgroups, (r + 1) * span);
   uint32_t n = 0;
   float s = 0.0f;
-  for (int w = 0; w < a.workgroups; w++) {
-    const uint32_t v = a.partial[(int64_t)w * all + e];
-    n += v;
-    s += __builtin_bit_cast(float, v);
+  if (e < all) {
+#pragma unroll 4
+    for (int w = r * span; w < end; w++) {
+      const uint32_t v = a.partial[(int64_t)w * all + e];
+      n += v;
+      s += __builtin_bit_cast(float, v);
+    }
+  }
+  n_s[r][c] = n;
+  s_s[r][c] = s;
+  __syncthreads();
+  if (r != 0 || e >= all) return;
+  for (int i = 1; i < kSumRows; i++) {
+    n += n_s[i][c];
+    s += s_s[i][c];
   }
   if (e <= a.experts) a.counts[e] = (int32_t)n;
   else a.sums[e - a.experts - 1] = s;
 }
 
-template <int DT, int N>
+// LDS accesses of a wave before this line and after it stay apart
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// ---- gradient -------------------------------------------------------------------------
+// A row's slots are added to its columns through LDS: the lanes that hold
+// slots put their terms at the chosen columns of the group's row of zeros,
+// all lanes read their own columns, and the slots' lanes put the zeros back.
+// A wave only ever touches its own rows there, in program order.
+template <int DT, int L, int N>
 __global__ void __launch_bounds__(kBlock) k_route_grad(RouteGradArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  typedef Gate<DT, L, N> G;
+  constexpr int V = G::V, S = (SIM_ROUTE_MAX_TOPK + L - 1) / L;
+  __shared__ float g_s[G::kAll];
+  __shared__ float add_s[kWaves * G::kRows][G::kAll];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & (L - 1);
+  float* add = add_s[wave * G::kRows + lane / L];
   const float n = a.counts ? (float)a.counts[a.experts] : 0.0f;
   const float unit = n > 0.0f ? a.coef * ((float)a.experts / (float)a.topk) / n / n : 0.0f;
-  float g[N];
+  for (int e = tid; e < G::kAll; e += kBlock)
+    g_s[e] = n > 0.0f && e < a.experts ? unit * (float)a.counts[e] : 0.0f;
 #pragma unroll
-  for (int i = 0; i < N; i++) {
-    const int e = lane + 64 * i;
-    g[i] = n > 0.0f && e < a.experts ? unit * (float)a.counts[e] : 0.0f;
-  }
+  for (int i = 0; i < N; i++) add[l + L * i] = 0.0f;
+  __syncthreads();
   if (blockIdx.x == 0 && wave == 0 && a.loss) {
     float loss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-      const int e = lane + 64 * i;
-      if (n > 0.0f && e < a.experts) loss += g[i] * a.sums[e];
-    }
+    if (n > 0.0f)
+      for (int e = lane; e < a.experts; e += 64) loss += g_s[e] * a.sums[e];
     loss = wave_sum(loss);
     if (lane == 0) *a.loss = loss;
   }
-  const int64_t row = (int64_t)blockIdx.x * kWaves + wave;
-  if (row >= a.tokens) return;
-  float x[N], p[N], d[N];
-  const bool live = load_row<DT, N>(a.x, row, a.stride, a.experts, a.keep, lane, x);
+  const int64_t step = (int64_t)gridDim.x * kWaves * G::kRows;
+  for (int64_t first = ((int64_t)blockIdx.x * kWaves + wave) * G::kRows; first < a.tokens; first += step) {
+    const bool here = first + lane / L < a.tokens;
+    const int64_t row = here ? first + lane / L : first;
+    const char* x = (const char*)a.x + row * a.stride * Ty<DT>::E;
+    char* dx = (char*)a.dx + row * a.dstride * Ty<DT>::E;
+    G g;
+    g.load(x, a.experts, l);
+    int mine[S];
+    float dw[S], at[S];
 #pragma unroll
-  for (int i = 0; i < N; i++) d[i] = 0.0f;
-  if (live) {
-    softmax(x, p);
-    int mine = -1;
-    float dw = 0.0f, w = 0.0f;
-    if (a.dweights && lane < a.topk) {
-      mine = a.chosen[row * a.topk + lane];
-      if (mine < 0 || mine >= a.experts) mine = -1;
-      if (mine >= 0) dw = a.dweights[row * a.topk + lane];
-    }
-    float u[N];
-#pragma unroll
-    for (int i = 0; i < N; i++) u[i] = 0.0f;
-    if (a.dweights) {
-      // the probability of this lane's slot
-#pragma unroll
-      for (int i = 0; i < N; i++) {
-        const float v = __shfl(p[i], mine & 63, 64);
-        if (mine >= 0 && (mine >> 6) == i) w = v;
-      }
-      float slot = dw;
-      if (a.normalize) {
-        const float total = wave_sum(w);
-        w = mine >= 0 ? w / total : 0.0f;
-        const float mean = wave_sum(w * dw);
-        slot = mine >= 0 ? w * (dw - mean) : 0.0f;
-      }
-      for (int j = 0; j < a.topk; j++) {
-        const int e = __shfl(mine, j, 64);
-        const float v = __shfl(slot, j, 64);
-#pragma unroll
-        for (int i = 0; i < N; i++)
-          if (lane + 64 * i == e) u[i] += v;
+    for (int s = 0; s < S; s++) {
+      const int slot = l + L * s;
+      mine[s] = -1;
+      dw[s] = at[s] = 0.0f;
+      if (a.dweights && here && slot < a.topk) {
+        mine[s] = a.chosen[row * a.topk + slot];
+        if (mine[s] < 0 || mine[s] >= a.experts) mine[s] = -1;
+        if (mine[s] >= 0) {
+          dw[s] = a.dweights[row * a.topk + slot];
+          at[s] = load_elem<DT>(x, mine[s]);
+        }
       }
     }
+    const bool kept = here && (!a.keep || a.keep[row]);
+    if (!kept) g.blank();
+    float f[N];
+    g.logits(f);
+    float top = kNegInf;
+#pragma unroll
+    for (int i = 0; i < N; i++) top = fmaxf(top, f[i]);
+    top = group_max<L>(top);
+    // a row of NaN and -inf alone is not empty: its sum is NaN
+    const float base = top == kNegInf ? 0.0f : top;
+    float z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+      f[i] = exp2_hw((f[i] - base) * kLog2e);
+      z += f[i];
+    }
+    z = group_sum<L>(z);
+    const bool live = z != 0.0f;
+    const float inv = live ? 1.0f / z : 0.0f;
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; i++) {
-      const float up = a.normalize ? g[i] : g[i] + u[i];
-      dot += p[i] * up;
+      f[i] *= inv;
+      dot = __builtin_fmaf(f[i], g_s[G::col(i / V, l) + i % V], dot);
     }
-    dot = wave_sum(dot);
+    float p[S], sum = 0.0f, mean = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-      const float up = a.normalize ? g[i] : g[i] + u[i];
-      d[i] = p[i] * (up - dot) + (a.normalize ? u[i] : 0.0f);
+    for (int s = 0; s < S; s++) {
+      p[s] = mine[s] >= 0 && live ? exp2_hw((at[s] - base) * kLog2e) * inv : 0.0f;
+      sum += p[s];
+      mean = __builtin_fmaf(p[s], dw[s], mean);
     }
+    if (a.normalize) {
+      sum = group_sum<L>(sum);
+      mean = group_sum<L>(mean) / sum;
+#pragma unroll
+      for (int s = 0; s < S; s++)
+        if (mine[s] >= 0 && live) add[mine[s]] = p[s] / sum * (dw[s] - mean);
+    } else {
+      dot += mean;
+#pragma unroll
+      for (int s = 0; s < S; s++)
+        if (mine[s] >= 0 && live) add[mine[s]] = p[s] * dw[s];
+    }
+    dot = group_sum<L>(dot);
+    wave_fence();
+#pragma unroll
+    for (int j = 0; j < G::NV; j++) {
+      float d[V];
+#pragma unroll
+      for (int t = 0; t < V; t++) {
+        const int e = G::col(j, l) + t;
+        d[t] = __builtin_fmaf(f[j * V + t], g_s[e] - dot, add[e]);
+      }
+      if (here) {
+        if (a.experts == G::kAll) st_row<DT>(dx, G::col(j, l), pack<DT>(d));
+        else st_guarded<DT>(dx, G::col(j, l), a.experts, d);
+      }
+    }
+    wave_fence();
+#pragma unroll
+    for (int s = 0; s < S; s++)
+      if (mine[s] >= 0) add[mine[s]] = 0.0f;
   }
-  char* out = (char*)a.dx + row * a.dstride * Ty<DT>::E;
-#pragma unroll
-  for (int i = 0; i < N; i++)
-    if (lane + 64 * i < a.experts) store_elem<DT>(out, lane + 64 * i, d[i]);
 }
 
+// ---- launches -----------------------------------------------------------------------
+int rows_per_workgroup(int experts) { return kWaves * (experts <= 256 ? 8 : experts <= 512 ? 4 : 2); }
+
+template <int DT, bool EIGHT>
+hipError_t route_layout(const RouteArgs& a, hipStream_t s) {
+  const dim3 grid(a.workgroups), block(kBlock);
+  if (a.experts <= 64) return launch<k_route<DT, 8, 8, EIGHT>>(grid, block, s, a);
+  if (a.experts <= 128) return launch<k_route<DT, 8, 16, EIGHT>>(grid, block, s, a);
+  if (a.experts <= 256) return launch<k_route<DT, 8, 32, EIGHT>>(grid, block, s, a);
+  if (a.experts <= 512) return launch<k_route<DT, 16, 32, EIGHT>>(grid, block, s, a);
+  return launch<k_route<DT, 32, 32, EIGHT>>(grid, block, s, a);
+}
 template <int DT>
 hipError_t route_dtype(const RouteArgs& a, hipStream_t s) {
-  const dim3 grid(a.workgroups), block(kBlock);
-  if (a.experts <= 64) return launch<k_route<DT, 1>>(grid, block, s, a);
-  if (a.experts <= 256) return launch<k_route<DT, 4>>(grid, block, s, a);
-  return launch<k_route<DT, 16>>(grid, block, s, a);
+  return a.topk <= 8 ? route_layout<DT, true>(a, s) : route_layout<DT, false>(a, s);
 }
 template <int DT>
 hipError_t grad_dtype(const RouteGradArgs& a, hipStream_t s) {
-  const int64_t wg = (a.tokens + kWaves - 1) / kWaves;
-  const dim3 grid((unsigned)(wg > 0 ? wg : 1)), block(kBlock);
-  if (a.experts <= 64) return launch<k_route_grad<DT, 1>>(grid, block, s, a);
-  if (a.experts <= 256) return launch<k_route_grad<DT, 4>>(grid, block, s, a);
-  return launch<k_route_grad<DT, 16>>(grid, block, s, a);
+  const int per = rows_per_workgroup(a.experts);
+  const int64_t wg = (a.tokens + per - 1) / per, most = 8 * (int64_t)library_cus();
+  const dim3 grid((unsigned)(wg < 1 ? 1 : wg < most ? wg : most)), block(kBlock);
+  if (a.experts <= 64) return launch<k_route_grad<DT, 8, 8>>(grid, block, s, a);
+  if (a.experts <= 128) return launch<k_route_grad<DT, 8, 16>>(grid, block, s, a);
+  if (a.experts <= 256) return launch<k_route_grad<DT, 8, 32>>(grid, block, s, a);
+  if (a.experts <= 512) return launch<k_route_grad<DT, 16, 32>>(grid, block, s, a);
+  return launch<k_route_grad<DT, 32, 32>>(grid, block, s, a);
 }
 
 }  // namespace
 
 int route_workgroups(int64_t tokens, int experts) {
-  (void)experts;
-  const int64_t wg = (tokens + kWaves - 1) / kWaves, most = 4 * (int64_t)library_cus();
-  return (int)(wg < 1 ? 1 : wg < most ? wg : most);
+  const int per = rows_per_workgroup(experts);
+  const int64_t wg = (tokens + per - 1) / per, most = 4 * (int64_t)library_cus();
+  return (int)(wg < 3 ? 1 : wg < most ? wg : most);
 }
 
 hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s) {
@@ -260,7 +525,7 @@ hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s) {
                        : dtype == SIM_FP16 ? route_dtype<SIM_FP16>(a, s)
                                            : route_dtype<SIM_BF16>(a, s);
   if (e != hipSuccess || a.workgroups == 1) return e;
-  return launch<k_route_sum>(dim3((2 * a.experts + kBlock) / kBlock), dim3(kBlock), s, a);
+  return launch<k_route_sum>(dim3((2 * a.experts + kSumCols) / kSumCols), dim3(kSumCols * kSumRows), s, a);
 }
 hipError_t launch_route_grad(const RouteGradArgs& a, int dtype, hipStream_t s) {
   if (dtype == SIM_FP32) return grad_dtype<SIM_FP32>(a, s);

@@ -23,10 +23,12 @@ template <int E> struct RowVec;
 template <> struct RowVec<2> {
   typedef __attribute__((address_space(1))) const u32x4_at2 CG;
   typedef __attribute__((address_space(1))) u32x4_at2 G;
+  static u32x4_at2 v;
 };
 template <> struct RowVec<4> {
   typedef __attribute__((address_space(1))) const u32x4_at4 CG;
   typedef __attribute__((address_space(1))) u32x4_at4 G;
+  static u32x4_at4 v;
 };
 template <int DT>
 __device__ __forceinline__ u32x4 ld_row(const void* row, int64_t elem) {
@@ -42,17 +44,68 @@ __device__ __forceinline__ void st_row(void* row, int64_t elem, u32x4 v) {
 template <int DT>
 __device__ __forceinline__ u32x4 ld_row_lane(const void* row, int64_t elem, uint32_t lane_elem) {
   const char* p = (const char*)row + elem * Ty<DT>::E;
+#ifdef LD_NT
+  return __builtin_nontemporal_load((typename RowVec<Ty<DT>::E>::CG*)(p + lane_elem * (uint32_t)Ty<DT>::E));
+#else
   return *(typename RowVec<Ty<DT>::E>::CG*)(p + lane_elem * (uint32_t)Ty<DT>::E);
+#endif
 }
 template <int DT>
 __device__ __forceinline__ void st_row_lane(void* row, int64_t elem, uint32_t lane_elem, u32x4 v) {
   char* p = (char*)row + elem * Ty<DT>::E;
+#ifdef ST_NT
+  __builtin_nontemporal_store((decltype(RowVec<Ty<DT>::E>::v))v, (typename RowVec<Ty<DT>::E>::G*)(p + lane_elem * (uint32_t)Ty<DT>::E));
+#else
   *(typename RowVec<Ty<DT>::E>::G*)(p + lane_elem * (uint32_t)Ty<DT>::E) = v;
+#endif
+}
+
+template <int DT> constexpr uint32_t neg_inf_bits() {
+  return DT == SIM_FP32 ? 0xff800000u : DT == SIM_FP16 ? 0xfc00fc00u : 0xff80ff80u;
+}
+// The vector at column `col` of a row that ends at column `cols`: what lies
+// past the end reads as -inf (which changes no maximum and no sum) and is not
+// written.
+template <int DT>
+__device__ __forceinline__ u32x4 ld_guarded(const void* row, int64_t col, int64_t cols) {
+  constexpr int V = epv<DT>();
+  const uint32_t n = neg_inf_bits<DT>();
+  u32x4 v = {n, n, n, n};
+  if (col + V <= cols) {
+    v = ld_row<DT>(row, col);
+  } else if (col < cols) {
+    float x[V];
+#pragma unroll
+    for (int i = 0; i < V; i++) x[i] = col + i < cols ? load_elem<DT>(row, col + i) : kNegInf;
+    v = pack<DT>(x);
+  }
+  return v;
+}
+template <int DT>
+__device__ __forceinline__ void load_cols(const void* row, int64_t col, int64_t cols, float (&x)[epv<DT>()]) {
+  unpack<DT>(ld_guarded<DT>(row, col, cols), x);
+}
+template <int DT>
+__device__ __forceinline__ void st_guarded(void* row, int64_t col, int64_t cols, const float (&x)[epv<DT>()]) {
+  constexpr int V = epv<DT>();
+  if (col + V <= cols) {
+    st_row<DT>(row, col, pack<DT>(x));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i++)
+      if (col + i < cols) store_elem<DT>(row, col + i, x[i]);
+  }
 }
 
 // 2^x (v_exp_f32: 1 ulp; results below the normal range are flushed, far
 // under what a sum that holds 1 can see)
-__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float exp2_hw(float x) {
+#ifdef NOEXP
+  return x;
+#else
+  return __builtin_amdgcn_exp2f(x);
+#endif
+}
 
 // Sums and maxima over the 64 lanes of a wave, the same value in every lane;
 // the order of a sum is fixed.
@@ -65,6 +118,41 @@ __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
   return v;
+}
+
+// The same over groups of L = 8, 16 or 32 neighbouring lanes, by DPP: the
+// partner in the pair, in the quad, in the mirrored half row, in the mirrored
+// row; 32 lanes take one more step through LDS.  Both partners combine the
+// same two values, so all lanes of a group end with the same bits.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(uint32_t, v)));
+}
+constexpr int kDppPair = 0xB1, kDppQuad = 0x4E, kDppHalfRow = 0x141, kDppRow = 0x140;
+template <int L, class T, class F>
+__device__ __forceinline__ T group_reduce(T v, F f) {
+  v = f(v, dpp<kDppPair>(v));
+  v = f(v, dpp<kDppQuad>(v));
+  v = f(v, dpp<kDppHalfRow>(v));
+  if constexpr (L >= 16) v = f(v, dpp<kDppRow>(v));
+  if constexpr (L >= 32) v = f(v, __shfl_xor(v, 16, 64));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+  return group_reduce<L>(v, [](float a, float b) { return a + b; });
+}
+template <int L>
+__device__ __forceinline__ float group_max(float v) {
+  return group_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int L>
+__device__ __forceinline__ bool group_any(bool v, int lane) {
+  return (__ballot(v) >> (lane & (64 - L))) & (~0ull >> (64 - L));
 }
 
 // A softmax's running maximum m and sum s of 2^((x - m) c), over the x seen
