@@ -79,8 +79,17 @@ int check_distill(int64_t rows, int64_t cols, int64_t stride, int dtype, int64_t
   return rows > kMaxGrid ? SIM_ERR_INVALID_ARG : SIM_OK;
 }
 
+// Least columns per workgroup where a row is split.  A shard's parts need one
+// more launch to merge splits, so a row's statistics are split no finer than
+// 32 KiB (one chunk of loads); a gradient and a step's two launches, which
+// need none, split down to 8 KiB.
+int64_t stats_least(int dtype) { return (32 << 10) / size_of(dtype); }
+int64_t grad_least(int dtype) { return (8 << 10) / size_of(dtype); }
+
 int64_t distill_work_bytes(int64_t rows, int64_t cols, int dtype) {
-  return (int64_t)distill_splits(rows, cols, dtype) * 4 * rows * 4;
+  const int64_t step = distill_whole_rows(rows, cols, dtype) ? 0 : distill_splits(rows, cols, grad_least(dtype));
+  const int64_t parts = distill_splits(rows, cols, stats_least(dtype));
+  return std::max<int64_t>(step, parts > 1 ? parts : 0) * 4 * rows * 4;
 }
 
 int check_work(const void* work, size_t have, int64_t need) {
@@ -200,7 +209,7 @@ int sim_distill_step(const void* logits, int64_t row_stride, int dtype, int64_t 
   a.dstride = drow_stride;
   a.loss = loss;
   a.parts = (float*)work;
-  a.splits = distill_splits(rows, vocab, dtype);
+  a.splits = distill_splits(rows, vocab, grad_least(dtype));
   a.span = distill_span(vocab, a.splits);
   if ((int64_t)a.splits * rows > kMaxGrid) return SIM_ERR_INVALID_ARG;
   const hipStream_t s = (hipStream_t)stream;
@@ -242,7 +251,7 @@ int sim_distill_parts(const void* logits, int64_t row_stride, int dtype, int64_t
   a.teacher_dtype = teacher_dtype;
   a.topk = topk;
   a.tau = temperature;
-  a.splits = distill_splits(rows, columns, dtype);
+  a.splits = distill_splits(rows, columns, stats_least(dtype));
   a.span = distill_span(columns, a.splits);
   if ((int64_t)a.splits * rows > kMaxGrid) return SIM_ERR_INVALID_ARG;
   a.parts = a.splits > 1 ? (float*)work : parts;
@@ -315,7 +324,7 @@ int sim_distill_grad(const void* logits, int64_t row_stride, int dtype, int64_t 
   a.dx = dlogits;
   a.dstride = drow_stride;
   a.norm = const_cast<float*>(norm);
-  a.splits = distill_splits(rows, columns, dtype);
+  a.splits = distill_splits(rows, columns, grad_least(dtype));
   a.span = distill_span(columns, a.splits);
   if ((int64_t)a.splits * rows > kMaxGrid) return SIM_ERR_INVALID_ARG;
   return hip_status(launch_distill_grad(a, dtype, (hipStream_t)stream));

@@ -36,9 +36,10 @@ __device__ __forceinline__ Slots load_slots(const DistillArgs& a, int64_t row, i
     z[i] = kNegInf;
     if (k < a.topk) {
       const int id = a.ids[row * a.topk + k];
+      const float zk = teacher_at(a.teacher, a.teacher_dtype, row * a.topk + k);  // in flight with the id
       if (id >= 0 && id < a.vocab) {
         s.id[i] = id;
-        z[i] = teacher_at(a.teacher, a.teacher_dtype, row * a.topk + k);
+        z[i] = zk;
       }
     }
     some = some || !(z[i] == kNegInf);
@@ -72,6 +73,67 @@ __device__ __forceinline__ void* row_at(const void* base, int64_t row, int64_t s
 // part (m, s, a, d) `part` of row `row`
 __device__ __forceinline__ int64_t part_index(int64_t part, int which, int64_t rows, int64_t row) {
   return (part * 4 + which) * rows + row;
+}
+
+// A row's slots as the threads of a workgroup of NT use them.  Slot k hangs on
+// the thread that holds its column (list head[thread], then next[k]); after
+// its vectors a thread writes the full values of its slots' columns.  Its own
+// stores to one address stay in order, so no barrier is needed in between,
+// and slots with the same id write the same value.
+template <int NT>
+struct SlotLists {
+  int head[NT];
+  int next[SIM_DISTILL_MAX_TOPK], id[SIM_DISTILL_MAX_TOPK];
+  float q[SIM_DISTILL_MAX_TOPK], x[SIM_DISTILL_MAX_TOPK];  // x: the slot's logit, then its probability
+  int live;
+};
+// Wave 0, before anything is written (the gradient may lie on the logits):
+// the slots and the logits of those in the columns [lo, hi) of `x`.
+template <int DT, int NT>
+__device__ __forceinline__ void gather_slots(const DistillArgs& a, SlotLists<NT>& s, const Slots& sl, const void* x,
+                                             int64_t lo, int64_t hi, int lane) {
+#pragma unroll
+  for (int i = 0; i < kSlotsPerLane; i++) {
+    const int k = lane + 64 * i;
+    if (k >= a.topk) continue;
+    const int64_t col = (int64_t)sl.id[i] - a.first;
+    s.id[k] = sl.id[i];
+    s.q[k] = sl.q[i];
+    if (sl.id[i] >= 0 && col >= lo && col < hi) s.x[k] = load_elem<DT>(x, col);
+  }
+  if (lane == 0) s.live = sl.live;
+}
+// Wave 0, once the row's maximum m and sum are known: each slot's probability,
+// and its place in its thread's list.
+template <int DT, int NT>
+__device__ __forceinline__ void hang_slots(const DistillArgs& a, SlotLists<NT>& s, const Slots& sl, int64_t lo,
+                                           int64_t hi, float m, float sum, float c, int lane) {
+#pragma unroll
+  for (int i = 0; i < kSlotsPerLane; i++) {
+    const int k = lane + 64 * i;
+    const int64_t col = (int64_t)sl.id[i] - a.first;
+    if (!sl.live || sl.id[i] < 0 || col < lo || col >= hi) continue;
+    s.x[k] = exp2_hw((s.x[k] - m) * c) / sum;
+    s.next[k] = atomicExch(&s.head[((col - lo) / epv<DT>()) % NT], k);
+  }
+}
+// Each slot's column gets up (p - the sum of q over the slots with its id).
+// Slots with one id hang on one thread, so it sees in its own list, whose
+// order depends on timing, whether there are others; then it adds them in
+// the order of the slots.
+template <int DT, int NT>
+__device__ __forceinline__ void write_slots(const DistillArgs& a, const SlotLists<NT>& s, void* dx, float up, int tid) {
+  for (int k = s.head[tid]; k >= 0; k = s.next[k]) {
+    float q = s.q[k];
+    bool more = false;
+    for (int j = s.head[tid]; j >= 0; j = s.next[j]) more = more || (j != k && s.id[j] == s.id[k]);
+    if (more) {
+      q = 0.0f;
+      for (int j = 0; j < a.topk; j++)
+        if (s.id[j] == s.id[k]) q += s.q[j];
+    }
+    store_elem<DT>(dx, (int64_t)s.id[k] - a.first, up * (s.x[k] - q));
+  }
 }
 
 // The parts of a row as one, in the order of the columns.

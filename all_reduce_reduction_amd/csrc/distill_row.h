@@ -9,10 +9,7 @@
 // NT * R vectors is read a second time for its gradient.
 //
 // While the row's loads are in flight, wave 0 reads the slots and their own
-// logits (before anything is written: the gradient may lie on the logits) and
-// hangs each slot on the thread that holds its column.  A thread writes its
-// vectors and then the full values of its slots' columns: its own stores to
-// one address stay in order, so no barrier is needed behind the stores.
+// logits.
 #pragma once
 
 #include "distill_device.h"
@@ -23,12 +20,10 @@ namespace simar {
 // of the R vectors of a thread, the last GUARD may lie past the row's end
 template <int DT, int NT, int R, int GUARD>
 __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
-  constexpr int V = epv<DT>(), W = NT / 64;
-  __shared__ int head[NT];
-  __shared__ int next_s[SIM_DISTILL_MAX_TOPK], id_s[SIM_DISTILL_MAX_TOPK];
-  __shared__ float q_s[SIM_DISTILL_MAX_TOPK], x_s[SIM_DISTILL_MAX_TOPK];
+  constexpr int V = epv<DT>(), W = NT / 64, PAIR = R % 2 ? 1 : 2;
+  constexpr bool STREAM = NT < 1024;
+  __shared__ SlotLists<NT> slots;
   __shared__ float m_s[W], s_s[W];
-  __shared__ int live_s;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x;
   const void* x = row_at(a.x, row, a.stride, Ty<DT>::E);
@@ -38,29 +33,21 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
   u32x4 v[R];
 #pragma unroll
   for (int i = 0; i < R; i++) {
-    if (i < R - GUARD) v[i] = ld_row_lane<DT>(x, i * NT * V, tid * V);
+    if (i < R - GUARD) v[i] = ld_row_lane<DT, STREAM>(x, i * NT * V, tid * V);
     else v[i] = ld_guarded<DT>(x, (int64_t)(i * NT + tid) * V, a.cols);
   }
-  head[tid] = -1;
+  slots.head[tid] = -1;
   Slots sl;
   if (wave == 0) {
     sl = load_slots(a, row, lane);
-#pragma unroll
-    for (int i = 0; i < kSlotsPerLane; i++) {
-      const int k = lane + 64 * i;
-      if (k < a.topk) {
-        id_s[k] = sl.id[i];
-        q_s[k] = sl.q[i];
-        if (sl.id[i] >= 0) x_s[k] = load_elem<DT>(x, sl.id[i]);
-      }
-    }
-    if (lane == 0) live_s = sl.live;
+    gather_slots<DT>(a, slots, sl, x, 0, a.cols, lane);
   }
   Running r{kNegInf, 0.0f};
 #pragma unroll
-  for (int i = 0; i < R; i++) {
-    float f[V];
-    unpack<DT>(v[i], f);
+  for (int i = 0; i < R; i += PAIR) {
+    float f[PAIR * V];
+#pragma unroll
+    for (int j = 0; j < PAIR; j++) unpack<DT>(v[i + j], f + j * V);
     running_add(r, f, c);
   }
   for (int64_t col = (int64_t)(R * NT + tid) * V; col < a.cols; col += NT * V) {
@@ -77,26 +64,18 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
   r.m = lane < W ? m_s[lane] : kNegInf;
   r.s = lane < W ? s_s[lane] : 0.0f;
   r = wave_running(r, c);
-  const bool live = live_s;
+  const bool live = slots.live;
   if (wave == 0) {
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < kSlotsPerLane; i++) {
-      const int k = lane + 64 * i;
-      if (sl.id[i] < 0) continue;
-      const float at = x_s[k];
-      if (!(sl.q[i] == 0.0f)) dot += at == kNegInf ? sl.q[i] * kNegInf : sl.q[i] * ((at - r.m) / a.tau);
-      // the slots with this id, in their order
-      float q = 0.0f;
-      for (int j = 0; j < a.topk; j++)
-        if (id_s[j] == sl.id[i]) q += q_s[j];
-      if (live) {
-        x_s[k] = up * (exp2_hw((at - r.m) * c) / r.s - q);
-        next_s[k] = atomicExch(&head[(sl.id[i] / V) % NT], k);
-      }
+      if (sl.id[i] < 0 || sl.q[i] == 0.0f) continue;
+      const float at = slots.x[lane + 64 * i];
+      dot += at == kNegInf ? sl.q[i] * kNegInf : sl.q[i] * ((at - r.m) / a.tau);
     }
     dot = wave_sum(dot);
     if (lane == 0) a.loss[row] = live ? sl.entropy + __logf(r.s) - dot : 0.0f;
+    hang_slots<DT>(a, slots, sl, 0, a.cols, r.m, r.s, c, lane);
   }
   const float k2 = live ? up / r.s : 0.0f;
   __syncthreads();
@@ -109,7 +88,7 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
     unpack<DT>(v[i], f);
 #pragma unroll
     for (int j = 0; j < V; j++) f[j] = live ? exp2_hw((f[j] - r.m) * c) * k2 : 0.0f;
-    if (i < R - GUARD) st_row_lane<DT>(dx, i * NT * V, tid * V, pack<DT>(f));
+    if (i < R - GUARD) st_row_lane<DT, STREAM>(dx, i * NT * V, tid * V, pack<DT>(f));
     else st_guarded<DT>(dx, (int64_t)(i * NT + tid) * V, a.cols, f);
   }
   for (int64_t col = (int64_t)(R * NT + tid) * V; col < a.cols; col += NT * V) {
@@ -119,7 +98,7 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
     for (int j = 0; j < V; j++) f[j] = live ? exp2_hw((f[j] - r.m) * c) * k2 : 0.0f;
     st_guarded<DT>(dx, col, a.cols, f);
   }
-  for (int k = head[tid]; k >= 0; k = next_s[k]) store_elem<DT>(dx, id_s[k], x_s[k]);
+  write_slots<DT>(a, slots, dx, up, tid);
 }
 
 // The workgroup and the vectors per thread for a row of n vectors: the

@@ -16,15 +16,31 @@
 namespace simar {
 namespace {
 
+// A workgroup's columns come in chunks of kHeld vectors per thread, whose loads
+// are all in flight together.
+constexpr int kHeld = 8;
+template <int DT>
+__device__ __forceinline__ void load_chunk(const void* x, int64_t col, int64_t hi, int tid, u32x4 (&v)[kHeld]) {
+  constexpr int V = epv<DT>();
+  const bool whole = col + kHeld * kBlock * V <= hi;
+#pragma unroll
+  for (int i = 0; i < kHeld; i++) {
+    if (whole) v[i] = ld_row_lane<DT, true>(x, col + i * kBlock * V, tid * V);
+    else v[i] = ld_guarded<DT>(x, col + (i * kBlock + tid) * V, hi);
+  }
+}
+
 template <int DT>
 __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
   constexpr int V = epv<DT>(), W = kBlock / 64;
-  __shared__ Running run[W];
+  __shared__ float m_s[W], s_s[W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
   const int64_t lo = split * a.span, hi = min(a.cols, lo + a.span);
   const void* x = row_at(a.x, row, a.stride, Ty<DT>::E);
   const float c = kLog2e / a.tau;
+  u32x4 v[kHeld];
+  load_chunk<DT>(x, lo, hi, tid, v);
   Slots sl;
   float at[kSlotsPerLane];
   if (wave == 0) {
@@ -38,18 +54,28 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
     }
   }
   Running r{kNegInf, 0.0f};
-  for (int64_t col = lo + (int64_t)tid * V; col < hi; col += kBlock * V) {
-    float v[V];
-    load_cols<DT>(x, col, hi, v);
-    running_add(r, v, c);
+  for (int64_t col = lo;;) {
+#pragma unroll
+    for (int i = 0; i < kHeld; i += 2) {
+      float f[2 * V];
+      unpack<DT>(v[i], f);
+      unpack<DT>(v[i + 1], f + V);
+      running_add(r, f, c);
+    }
+    col += kHeld * kBlock * V;
+    if (col >= hi) break;
+    load_chunk<DT>(x, col, hi, tid, v);
   }
   r = wave_running(r, c);
-  if (lane == 0) run[wave] = r;
+  if (lane == 0) {
+    m_s[wave] = r.m;
+    s_s[wave] = r.s;
+  }
   __syncthreads();
   if (wave == 0) {
-    r = run[0];
-#pragma unroll
-    for (int w = 1; w < W; w++) r = running_join(r, run[w], c);
+    r.m = lane < W ? m_s[lane] : kNegInf;
+    r.s = lane < W ? s_s[lane] : 0.0f;
+    r = wave_running(r, c);
     float mass = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < kSlotsPerLane; i++) {
@@ -93,22 +119,21 @@ __global__ void __launch_bounds__(kBlock) k_distill_merge(DistillArgs a, float* 
   out[3 * a.rows + row] = t.d;
 }
 
-// The gradient of a run of columns.  First the slots' own logits are read
-// (the gradient may lie on the logits), then every column gets scale * p,
-// and last each slot's column its full value; slots with one id each write
-// the same one.
+// The gradient of a run of columns, from the row's joined parts or its norm.
 template <int DT>
 __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
   constexpr int V = epv<DT>();
-  __shared__ int id_s[SIM_DISTILL_MAX_TOPK];
-  __shared__ float q_s[SIM_DISTILL_MAX_TOPK];
-  __shared__ int live_s;
+  __shared__ SlotLists<kBlock> slots;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
   const int64_t lo = split * a.span, hi = min(a.cols, lo + a.span);
   const void* x = row_at(a.x, row, a.stride, Ty<DT>::E);
   void* dx = row_at(a.dx, row, a.dstride, Ty<DT>::E);
   const float c = kLog2e / a.tau;
+  const float up = (a.row_scale ? a.row_scale[row] : 1.0f) * (a.coef / a.tau);
+  u32x4 v[kHeld];
+  load_chunk<DT>(x, lo, hi, tid, v);
+  slots.head[tid] = -1;
   Part t{};
   if (a.norm) {
     t.m = a.norm[row];
@@ -116,56 +141,33 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
   } else {
     t = join_parts(a.parts, a.splits, a.rows, row, a.tau);
   }
+  __syncthreads();
   if (wave == 0) {
     const Slots sl = load_slots(a, row, lane);
-#pragma unroll
-    for (int i = 0; i < kSlotsPerLane; i++)
-      if (lane + 64 * i < a.topk) {
-        id_s[lane + 64 * i] = sl.id[i];
-        q_s[lane + 64 * i] = sl.q[i];
-      }
-    if (lane == 0) {
-      live_s = sl.live;
-      if (a.loss && split == 0) a.loss[row] = loss_of(sl, t);
-    }
+    gather_slots<DT>(a, slots, sl, x, lo, hi, lane);
+    wave_fence();
+    if (lane == 0 && a.loss && split == 0) a.loss[row] = loss_of(sl, t);
+    hang_slots<DT>(a, slots, sl, lo, hi, t.m, t.s, c, lane);
   }
   __syncthreads();
-  const bool live = live_s;
-  const float scale = live ? (a.row_scale ? a.row_scale[row] : 1.0f) * (a.coef / a.tau) : 0.0f;
-  const float inv = live ? scale / t.s : 0.0f;
-  int64_t own = -1;
-  float value = 0.0f;
-  if (tid < a.topk && live) {
-    const int64_t col = (int64_t)id_s[tid] - a.first;
-    if (id_s[tid] >= 0 && col >= lo && col < hi) {
-      own = col;
-      float q = 0.0f;
-      for (int k = 0; k < a.topk; k++)
-        if (id_s[k] == id_s[tid]) q += q_s[k];
-      value = scale * (exp2_hw((load_elem<DT>(x, col) - t.m) * c) / t.s - q);
+  const bool live = slots.live;
+  const float k2 = live ? up / t.s : 0.0f;
+  for (int64_t col = lo;;) {
+    const bool whole = col + kHeld * kBlock * V <= hi;
+#pragma unroll
+    for (int i = 0; i < kHeld; i++) {
+      float f[V];
+      unpack<DT>(v[i], f);
+#pragma unroll
+      for (int j = 0; j < V; j++) f[j] = live ? exp2_hw((f[j] - t.m) * c) * k2 : 0.0f;
+      if (whole) st_row_lane<DT, true>(dx, col + i * kBlock * V, tid * V, pack<DT>(f));
+      else st_guarded<DT>(dx, col + (i * kBlock + tid) * V, hi, f);
     }
+    col += kHeld * kBlock * V;
+    if (col >= hi) break;
+    load_chunk<DT>(x, col, hi, tid, v);
   }
-  __syncthreads();
-  for (int64_t col = lo + (int64_t)tid * V; col < hi; col += kBlock * V) {
-    float v[V];
-    if (live) {
-      load_cols<DT>(x, col, hi, v);
-#pragma unroll
-      for (int i = 0; i < V; i++) v[i] = exp2_hw((v[i] - t.m) * c) * inv;
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; i++) v[i] = 0.0f;
-    }
-    if (col + V <= hi) {
-      st_row<DT>(dx, col, pack<DT>(v));
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; i++)
-        if (col + i < hi) store_elem<DT>(dx, col + i, v[i]);
-    }
-  }
-  __syncthreads();
-  if (own >= 0) store_elem<DT>(dx, own, value);
+  write_slots<DT>(a, slots, dx, up, tid);
 }
 
 }  // namespace
@@ -173,12 +175,16 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
 bool distill_whole_rows(int64_t rows, int64_t cols, int dtype) {
   (void)cols;
   (void)dtype;
+#ifdef FORCE_WHOLE
+  return FORCE_WHOLE;
+#endif
   return rows >= library_cus();
 }
-int distill_splits(int64_t rows, int64_t cols, int dtype) {
-  (void)dtype;
-  const int64_t most = (cols + kBlock * 8 - 1) / (kBlock * 8);
-  const int64_t want = rows > 0 ? (2 * (int64_t)library_cus() + rows - 1) / rows : 1;
+// Workgroups per row: enough for four per compute unit, each with at least
+// `least` columns.
+int distill_splits(int64_t rows, int64_t cols, int64_t least) {
+  const int64_t most = (cols + least - 1) / least;
+  const int64_t want = rows > 0 ? (4 * (int64_t)library_cus() + rows - 1) / rows : 1;
   return (int)(want < most ? want : most);
 }
 int64_t distill_span(int64_t cols, int splits) {

@@ -151,7 +151,11 @@ __device__ __forceinline__ void top8(const Gate<DT, L, N>& g, int l, uint32_t (&
   merge8(top, [](uint32_t k, int) { return dpp<kDppQuad>(k); });
   merge8(top, [](uint32_t k, int) { return dpp<kDppHalfRow>(k); });
   if constexpr (L >= 16) merge8(top, [](uint32_t k, int) { return dpp<kDppRow>(k); });
-  if constexpr (L >= 32) merge8(top, [](uint32_t k, int) { return (uint32_t)__shfl_xor((int)k, 16, 64); });
+  if constexpr (L >= 32) {
+    // every lane keeps its own row's eight and takes the other row's
+    const bool odd = (__lane_id() & 16) != 0;
+    merge8(top, [odd](uint32_t k, int) { return across_rows(k, [odd](uint32_t e, uint32_t o) { return odd ? e : o; }); });
+  }
 }
 
 // The topk largest one after the other, exactly, for any topk: lane l gets
@@ -358,13 +362,6 @@ __global__ void __launch_bounds__(kSumCols* kSumRows) k_route_sum(RouteArgs a) {
   }
   if (e <= a.experts) a.counts[e] = (int32_t)n;
   else a.sums[e - a.experts - 1] = s;
-}
-
-// LDS accesses of a wave before this line and after it stay apart
-__device__ __forceinline__ void wave_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // ---- gradient -------------------------------------------------------------------------

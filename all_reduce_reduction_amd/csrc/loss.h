@@ -73,7 +73,7 @@ int route_workgroups(int64_t tokens, int experts);
 hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s);
 hipError_t launch_route_grad(const RouteGradArgs& a, int dtype, hipStream_t s);
 
-int distill_splits(int64_t rows, int64_t cols, int dtype);
+int distill_splits(int64_t rows, int64_t cols, int64_t least);
 int64_t distill_span(int64_t cols, int splits);
 hipError_t launch_distill_stats(const DistillArgs& a, int dtype, hipStream_t s);
 hipError_t launch_distill_join(const DistillArgs& a, float* loss, float* norm, hipStream_t s);

@@ -21,14 +21,14 @@ typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_at4 __attribute__((ext_vector_type(4), aligned(4)));
 template <int E> struct RowVec;
 template <> struct RowVec<2> {
+  typedef u32x4_at2 V;
   typedef __attribute__((address_space(1))) const u32x4_at2 CG;
   typedef __attribute__((address_space(1))) u32x4_at2 G;
-  static u32x4_at2 v;
 };
 template <> struct RowVec<4> {
+  typedef u32x4_at4 V;
   typedef __attribute__((address_space(1))) const u32x4_at4 CG;
   typedef __attribute__((address_space(1))) u32x4_at4 G;
-  static u32x4_at4 v;
 };
 template <int DT>
 __device__ __forceinline__ u32x4 ld_row(const void* row, int64_t elem) {
@@ -40,24 +40,20 @@ __device__ __forceinline__ void st_row(void* row, int64_t elem, u32x4 v) {
 }
 
 // The same with a workgroup-uniform element offset (kept in scalar registers)
-// and a lane's own, which has 32 bits.
-template <int DT>
+// and a lane's own, which has 32 bits; NT: streaming (nontemporal).
+template <int DT, bool NT>
 __device__ __forceinline__ u32x4 ld_row_lane(const void* row, int64_t elem, uint32_t lane_elem) {
   const char* p = (const char*)row + elem * Ty<DT>::E;
-#ifdef LD_NT
-  return __builtin_nontemporal_load((typename RowVec<Ty<DT>::E>::CG*)(p + lane_elem * (uint32_t)Ty<DT>::E));
-#else
-  return *(typename RowVec<Ty<DT>::E>::CG*)(p + lane_elem * (uint32_t)Ty<DT>::E);
-#endif
+  typename RowVec<Ty<DT>::E>::CG* q = (typename RowVec<Ty<DT>::E>::CG*)(p + lane_elem * (uint32_t)Ty<DT>::E);
+  if constexpr (NT) return __builtin_nontemporal_load(q);
+  else return *q;
 }
-template <int DT>
+template <int DT, bool NT>
 __device__ __forceinline__ void st_row_lane(void* row, int64_t elem, uint32_t lane_elem, u32x4 v) {
   char* p = (char*)row + elem * Ty<DT>::E;
-#ifdef ST_NT
-  __builtin_nontemporal_store((decltype(RowVec<Ty<DT>::E>::v))v, (typename RowVec<Ty<DT>::E>::G*)(p + lane_elem * (uint32_t)Ty<DT>::E));
-#else
-  *(typename RowVec<Ty<DT>::E>::G*)(p + lane_elem * (uint32_t)Ty<DT>::E) = v;
-#endif
+  typename RowVec<Ty<DT>::E>::G* q = (typename RowVec<Ty<DT>::E>::G*)(p + lane_elem * (uint32_t)Ty<DT>::E);
+  if constexpr (NT) __builtin_nontemporal_store((typename RowVec<Ty<DT>::E>::V)v, q);
+  else *q = v;
 }
 
 template <int DT> constexpr uint32_t neg_inf_bits() {
@@ -99,31 +95,14 @@ __device__ __forceinline__ void st_guarded(void* row, int64_t col, int64_t cols,
 
 // 2^x (v_exp_f32: 1 ulp; results below the normal range are flushed, far
 // under what a sum that holds 1 can see)
-__device__ __forceinline__ float exp2_hw(float x) {
-#ifdef NOEXP
-  return x;
-#else
-  return __builtin_amdgcn_exp2f(x);
-#endif
-}
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Sums and maxima over the 64 lanes of a wave, the same value in every lane;
-// the order of a sum is fixed.
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
-  return v;
-}
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-  return v;
-}
-
-// The same over groups of L = 8, 16 or 32 neighbouring lanes, by DPP: the
-// partner in the pair, in the quad, in the mirrored half row, in the mirrored
-// row; 32 lanes take one more step through LDS.  Both partners combine the
-// same two values, so all lanes of a group end with the same bits.
+// Reductions over groups of L = 8, 16, 32 or 64 neighbouring lanes without
+// LDS: with the partner in the pair, in the quad, in the mirrored half row and
+// in the mirrored row by DPP, then between the two rows of 16 of a half wave
+// and between the half waves by lane swaps.  Both partners combine the same
+// two values, so all lanes of a group end with the same bits, and the order of
+// a sum is fixed.
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
@@ -133,13 +112,29 @@ __device__ __forceinline__ float dpp(float v) {
   return __builtin_bit_cast(float, dpp<CTRL>(__builtin_bit_cast(uint32_t, v)));
 }
 constexpr int kDppPair = 0xB1, kDppQuad = 0x4E, kDppHalfRow = 0x141, kDppRow = 0x140;
+// (the even rows' value, the odd rows' value) of each pair of rows
+template <class T, class F>
+__device__ __forceinline__ T across_rows(T v, F f) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  const uint32_t lo = r[0], hi = r[1];
+  return f(__builtin_bit_cast(T, lo), __builtin_bit_cast(T, hi));
+}
+template <class T, class F>
+__device__ __forceinline__ T across_halves(T v, F f) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  const uint32_t lo = r[0], hi = r[1];
+  return f(__builtin_bit_cast(T, lo), __builtin_bit_cast(T, hi));
+}
 template <int L, class T, class F>
 __device__ __forceinline__ T group_reduce(T v, F f) {
   v = f(v, dpp<kDppPair>(v));
   v = f(v, dpp<kDppQuad>(v));
   v = f(v, dpp<kDppHalfRow>(v));
   if constexpr (L >= 16) v = f(v, dpp<kDppRow>(v));
-  if constexpr (L >= 32) v = f(v, __shfl_xor(v, 16, 64));
+  if constexpr (L >= 32) v = across_rows(v, f);
+  if constexpr (L >= 64) v = across_halves(v, f);
   return v;
 }
 template <int L>
@@ -150,9 +145,18 @@ template <int L>
 __device__ __forceinline__ float group_max(float v) {
   return group_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
 }
+__device__ __forceinline__ float wave_sum(float v) { return group_sum<64>(v); }
+__device__ __forceinline__ float wave_max(float v) { return group_max<64>(v); }
 template <int L>
 __device__ __forceinline__ bool group_any(bool v, int lane) {
   return (__ballot(v) >> (lane & (64 - L))) & (~0ull >> (64 - L));
+}
+
+// LDS accesses of a wave before this line and after it stay apart
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // A softmax's running maximum m and sum s of 2^((x - m) c), over the x seen
