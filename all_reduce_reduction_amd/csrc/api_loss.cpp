@@ -63,8 +63,8 @@ int check_route(int64_t tokens, int experts, int topk, int dtype) {
   return tokens < 0 || tokens > kMaxGrid ? SIM_ERR_INVALID_ARG : SIM_OK;
 }
 
-int64_t route_work_bytes(int64_t tokens, int experts) {
-  const int64_t wg = route_workgroups(tokens, experts);
+int64_t route_work_bytes(int64_t tokens, int experts, int dtype) {
+  const int64_t wg = route_workgroups(tokens, experts, dtype);
   return wg > 1 ? wg * (2 * (int64_t)experts + 1) * 4 : 0;
 }
 
@@ -111,7 +111,7 @@ int sim_route_work(int64_t tokens, int experts, int topk, int dtype, size_t* byt
   const int rc = check_route(tokens, experts, topk, dtype);
   if (rc) return rc;
   if (!bytes) return SIM_ERR_INVALID_ARG;
-  *bytes = (size_t)route_work_bytes(tokens, experts);
+  *bytes = (size_t)route_work_bytes(tokens, experts, dtype);
   return SIM_OK;
 }
 
@@ -123,7 +123,7 @@ int sim_route(const void* logits, int64_t row_stride, int dtype, const uint8_t* 
   if (rc) return rc;
   if (!rows_fit(tokens, experts, row_stride)) return SIM_ERR_INVALID_ARG;
   if (!counts || !prob_sums || (tokens > 0 && (!logits || !chosen || !weights))) return SIM_ERR_INVALID_ARG;
-  const int64_t need = route_work_bytes(tokens, experts);
+  const int64_t need = route_work_bytes(tokens, experts, dtype);
   if ((rc = check_work(work, work_bytes, need))) return rc;
   const Array all[] = {rows_of(logits, tokens, experts, row_stride, dtype, false),
                        {keep, tokens, 1, false},
@@ -135,7 +135,7 @@ int sim_route(const void* logits, int64_t row_stride, int dtype, const uint8_t* 
   if ((rc = check_arrays(all, -1, -1, false))) return rc;
   if ((rc = library_device())) return rc;
   const RouteArgs a{logits, row_stride, keep, tokens, experts, topk, normalize != 0, chosen, weights, counts, prob_sums,
-                    (uint32_t*)work, route_workgroups(tokens, experts)};
+                    (uint32_t*)work, route_workgroups(tokens, experts, dtype)};
   return hip_status(launch_route(a, dtype, (hipStream_t)stream));
 }
 

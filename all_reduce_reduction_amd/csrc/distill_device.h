@@ -140,17 +140,32 @@ __device__ __forceinline__ void write_slots(const DistillArgs& a, const SlotList
 struct Part {
   float m, s, a, d;
 };
-__device__ __forceinline__ Part join_parts(const float* parts, int n, int64_t rows, int64_t row, float tau) {
+__device__ __forceinline__ Part join_two(const Part& p, const Part& q, float tau, float c) {
+  Part t;
+  t.m = fmaxf(p.m, q.m);
+  t.s = p.s * rebase(p.m, t.m, c) + q.s * rebase(q.m, t.m, c);
+  t.a = p.a + q.a;
+  // (a part without slots moves nothing, wherever its own maximum is)
+  const float dp = p.a == 0.0f || p.m == t.m ? 0.0f : p.a * ((p.m - t.m) / tau);
+  const float dq = q.a == 0.0f || q.m == t.m ? 0.0f : q.a * ((q.m - t.m) / tau);
+  t.d = (p.d + dp) + (q.d + dq);
+  return t;
+}
+// A whole wave joins a row's n parts: lane k takes parts k, k + 64, ..., so
+// that all loads are in flight together.
+__device__ __forceinline__ Part join_parts(const float* parts, int n, int64_t rows, int64_t row, float tau, int lane) {
   const float c = kLog2e / tau;
   Part t{kNegInf, 0.0f, 0.0f, 0.0f};
-  for (int k = 0; k < n; k++) t.m = fmaxf(t.m, parts[part_index(k, 0, rows, row)]);
-  for (int k = 0; k < n; k++) {
-    const float m = parts[part_index(k, 0, rows, row)], mass = parts[part_index(k, 2, rows, row)];
-    t.s += parts[part_index(k, 1, rows, row)] * rebase(m, t.m, c);
-    if (mass == 0.0f) continue;
-    t.a += mass;
-    t.d += parts[part_index(k, 3, rows, row)] + (m == t.m ? 0.0f : mass * ((m - t.m) / tau));
+  for (int k = lane; k < n; k += 64) {
+    const Part p{parts[part_index(k, 0, rows, row)], parts[part_index(k, 1, rows, row)],
+                 parts[part_index(k, 2, rows, row)], parts[part_index(k, 3, rows, row)]};
+    t = join_two(t, p, tau, c);
   }
+  const float top = wave_max(t.m);
+  t = join_two(t, Part{top, 0.0f, 0.0f, 0.0f}, tau, c);
+  t.s = wave_sum(t.s);
+  t.a = wave_sum(t.a);
+  t.d = wave_sum(t.d);
   return t;
 }
 __device__ __forceinline__ float loss_of(const Slots& s, const Part& t) {

@@ -26,7 +26,7 @@ __device__ __forceinline__ void load_chunk(const void* x, int64_t col, int64_t h
 #pragma unroll
   for (int i = 0; i < kHeld; i++) {
     if (whole) v[i] = ld_row_lane<DT, true>(x, col + i * kBlock * V, tid * V);
-    else v[i] = ld_guarded<DT>(x, col + (i * kBlock + tid) * V, hi);
+    else if (col + i * kBlock * V < hi) v[i] = ld_guarded<DT>(x, col + (i * kBlock + tid) * V, hi);
   }
 }
 
@@ -56,10 +56,10 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
   Running r{kNegInf, 0.0f};
   for (int64_t col = lo;;) {
 #pragma unroll
-    for (int i = 0; i < kHeld; i += 2) {
-      float f[2 * V];
+    for (int i = 0; i < kHeld; i++) {
+      if (col + i * kBlock * V >= hi) continue;
+      float f[V];
       unpack<DT>(v[i], f);
-      unpack<DT>(v[i + 1], f + V);
       running_add(r, f, c);
     }
     col += kHeld * kBlock * V;
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_join(DistillArgs a, float* l
   if (row >= a.rows) return;
   const int lane = threadIdx.x & 63;
   const Slots s = load_slots(a, row, lane);
-  const Part t = join_parts(a.parts, a.splits, a.rows, row, a.tau);
+  const Part t = join_parts(a.parts, a.splits, a.rows, row, a.tau, lane);
   if (lane == 0) {
     loss[row] = loss_of(s, t);
     norm[row] = t.m;
@@ -108,11 +108,13 @@ __global__ void __launch_bounds__(kBlock) k_distill_join(DistillArgs a, float* l
   }
 }
 
-// one thread per row
+// one wave per row
 __global__ void __launch_bounds__(kBlock) k_distill_merge(DistillArgs a, float* out) {
-  const int64_t row = (int64_t)blockIdx.x * kBlock + threadIdx.x;
+  const int64_t row = (int64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
   if (row >= a.rows) return;
-  const Part t = join_parts(a.parts, a.splits, a.rows, row, a.tau);
+  const int lane = threadIdx.x & 63;
+  const Part t = join_parts(a.parts, a.splits, a.rows, row, a.tau, lane);
+  if (lane != 0) return;
   out[row] = t.m;
   out[a.rows + row] = t.s;
   out[2 * a.rows + row] = t.a;
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
     t.m = a.norm[row];
     t.s = a.norm[a.rows + row];
   } else {
-    t = join_parts(a.parts, a.splits, a.rows, row, a.tau);
+    t = join_parts(a.parts, a.splits, a.rows, row, a.tau, lane);
   }
   __syncthreads();
   if (wave == 0) {
@@ -156,6 +158,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
     const bool whole = col + kHeld * kBlock * V <= hi;
 #pragma unroll
     for (int i = 0; i < kHeld; i++) {
+      if (col + i * kBlock * V >= hi) continue;
       float f[V];
       unpack<DT>(v[i], f);
 #pragma unroll
@@ -173,18 +176,17 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
 }  // namespace
 
 bool distill_whole_rows(int64_t rows, int64_t cols, int dtype) {
-  (void)cols;
-  (void)dtype;
 #ifdef FORCE_WHOLE
   return FORCE_WHOLE;
 #endif
-  return rows >= library_cus();
+  const int v = dtype == SIM_FP32 ? 4 : 8;
+  return (cols + v - 1) / v <= 16 * 1024 || rows >= library_cus() / 2;
 }
-// Workgroups per row: enough for four per compute unit, each with at least
+// Workgroups per row: enough for two per compute unit, each with at least
 // `least` columns.
 int distill_splits(int64_t rows, int64_t cols, int64_t least) {
   const int64_t most = (cols + least - 1) / least;
-  const int64_t want = rows > 0 ? (4 * (int64_t)library_cus() + rows - 1) / rows : 1;
+  const int64_t want = rows > 0 ? (2 * (int64_t)library_cus() + rows - 1) / rows : 1;
   return (int)(want < most ? want : most);
 }
 int64_t distill_span(int64_t cols, int splits) {
@@ -211,7 +213,7 @@ hipError_t launch_distill_join(const DistillArgs& a, float* loss, float* norm, h
   return launch<k_distill_join>(dim3((unsigned)((a.rows + 3) / 4)), dim3(kBlock), s, a, loss, norm);
 }
 hipError_t launch_distill_merge(const DistillArgs& a, float* out, hipStream_t s) {
-  return launch<k_distill_merge>(dim3((unsigned)((a.rows + kBlock - 1) / kBlock)), dim3(kBlock), s, a, out);
+  return launch<k_distill_merge>(dim3((unsigned)((a.rows + 3) / 4)), dim3(kBlock), s, a, out);
 }
 
 }  // namespace simar

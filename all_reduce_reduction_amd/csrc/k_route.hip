@@ -49,6 +49,12 @@ struct Gate {
 #pragma unroll
     for (int j = 0; j < NV; j++) v[j] = u32x4{n, n, n, n};
   }
+  // What is made of the vectors after this is made after it: values kept from
+  // one use to the next would take more registers than making them again.
+  __device__ __forceinline__ void renew() {
+#pragma unroll
+    for (int j = 0; j < NV; j++) asm volatile("" : "+v"(v[j]));
+  }
   __device__ __forceinline__ void logits(float (&x)[N]) const {
 #pragma unroll
     for (int j = 0; j < NV; j++) {
@@ -65,14 +71,18 @@ struct Gate {
 // clear lies above +inf, with the sign set below -inf.
 template <int DT>
 __device__ __forceinline__ uint32_t ordered(uint32_t bits) {
-  if constexpr (DT == SIM_FP32) return (bits ^ ((uint32_t)((int32_t)bits >> 31) | 0x80000000u)) + (bits >> 31);
-  else return ((bits ^ ((bits >> 15) * 0x7fffu | 0x8000u)) + (bits >> 15)) << 16;
+  if constexpr (DT == SIM_FP32) {
+    // -0 + 0 is +0, and every other value stays
+    const uint32_t b = __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, bits) + 0.0f);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  }
+  return ((bits ^ ((bits >> 15) * 0x7fffu | 0x8000u)) + (bits >> 15)) << 16;
 }
 template <int DT> constexpr uint32_t ordered_inf() {
   return DT == SIM_FP32 ? 0xff800000u : DT == SIM_FP16 ? 0xfc000000u : 0xff800000u;
 }
 template <int DT> constexpr uint32_t ordered_neg_inf() {
-  return DT == SIM_FP32 ? 0x00800000u : DT == SIM_FP16 ? 0x04000000u : 0x00800000u;
+  return DT == SIM_FP32 ? 0x007fffffu : DT == SIM_FP16 ? 0x04000000u : 0x00800000u;
 }
 template <int DT>
 __device__ __forceinline__ float from_ordered16(uint32_t key) {
@@ -116,11 +126,13 @@ __device__ __forceinline__ void merge8(uint32_t (&k)[8], F other) {
 // Keys that put the value above the distance of the index from the last one,
 // so that a larger key is a larger logit or, among equal ones, a lower index.
 // 16-bit values fit whole; fp32 values lose their log2(L N) lowest bits, and
-// the caller checks that what is left tells the chosen ones apart.
+// the caller checks that what is left tells the chosen ones apart.  Only keys
+// below `limit` take part (0: all do).
 template <int DT, int L, int N>
-__device__ __forceinline__ void top8(const Gate<DT, L, N>& g, int l, uint32_t (&top)[8]) {
+__device__ __forceinline__ void top8(const Gate<DT, L, N>& g, int l, uint32_t limit, uint32_t (&top)[8]) {
   typedef Gate<DT, L, N> G;
   constexpr int V = G::V;
+  const uint32_t mine = (uint32_t)((L - 1 - l) * V);
 #pragma unroll
   for (int b = 0; b < N / 8; b++) {
     uint32_t k[8];
@@ -137,6 +149,10 @@ __device__ __forceinline__ void top8(const Gate<DT, L, N>& g, int l, uint32_t (&
         k[i] = (t & 1 ? o & 0xffff0000u : o << 16) | low;
       }
     }
+    if (limit != 0) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) k[i] = (k[i] | mine) < limit ? k[i] : 0;
+    }
     sort8(k);
     if (b == 0) {
 #pragma unroll
@@ -144,17 +160,24 @@ __device__ __forceinline__ void top8(const Gate<DT, L, N>& g, int l, uint32_t (&
     } else {
       merge8(top, [&](uint32_t, int i) { return k[i]; });
     }
+    // one eight after the other: interleaved, their keys would take the
+    // registers of two more waves
+    __builtin_amdgcn_sched_barrier(0);
   }
 #pragma unroll
-  for (int i = 0; i < 8; i++) top[i] |= (uint32_t)((L - 1 - l) * V);
+  for (int i = 0; i < 8; i++) top[i] |= mine;
   merge8(top, [](uint32_t k, int) { return dpp<kDppPair>(k); });
   merge8(top, [](uint32_t k, int) { return dpp<kDppQuad>(k); });
   merge8(top, [](uint32_t k, int) { return dpp<kDppHalfRow>(k); });
   if constexpr (L >= 16) merge8(top, [](uint32_t k, int) { return dpp<kDppRow>(k); });
+  // every lane keeps its own row's (half's) eight and takes the other's
   if constexpr (L >= 32) {
-    // every lane keeps its own row's eight and takes the other row's
     const bool odd = (__lane_id() & 16) != 0;
     merge8(top, [odd](uint32_t k, int) { return across_rows(k, [odd](uint32_t e, uint32_t o) { return odd ? e : o; }); });
+  }
+  if constexpr (L >= 64) {
+    const bool up = (__lane_id() & 32) != 0;
+    merge8(top, [up](uint32_t k, int) { return across_halves(k, [up](uint32_t e, uint32_t o) { return up ? e : o; }); });
   }
 }
 
@@ -179,14 +202,16 @@ __device__ __forceinline__ void top_in_turn(const Gate<DT, L, N>& g, int l, int 
 #pragma unroll
     for (int i = 0; i < N; i++) best = max(best, k[i]);
     best = group_reduce<L>(best, [](uint32_t a, uint32_t b) { return max(a, b); });
-    uint32_t at = 0xffffffffu;
+    // columns relative to the lane's first, which are constants
+    uint32_t at = 0x40000000u;
 #pragma unroll
     for (int i = N - 1; i >= 0; i--)
-      if (k[i] == best) at = G::col(i / V, l) + i % V;
-    at = group_reduce<L>(at, [](uint32_t a, uint32_t b) { return min(a, b); });
+      if (k[i] == best) at = G::col(i / V, 0) + i % V;
+    at = group_reduce<L>(at + l * V, [](uint32_t a, uint32_t b) { return min(a, b); });
+    const uint32_t own = at - l * V;
 #pragma unroll
     for (int i = 0; i < N; i++)
-      if (at == (uint32_t)(G::col(i / V, l) + i % V)) k[i] = 0;
+      if (own == (uint32_t)(G::col(i / V, 0) + i % V)) k[i] = 0;
 #pragma unroll
     for (int s = 0; s < S; s++)
       if (r == l + L * s && best != 0) mine[s] = (int)at;
@@ -195,10 +220,12 @@ __device__ __forceinline__ void top_in_turn(const Gate<DT, L, N>& g, int l, int 
 }
 
 // ---- forward ------------------------------------------------------------------------
-template <int DT, int L, int N, bool EIGHT>
-__global__ void __launch_bounds__(kBlock) k_route(RouteArgs a) {
+// Up to eight chosen experts come from one pass of the exchange networks; each
+// further eight from another one below the last key.  MANY: topk > 8.
+template <int DT, int L, int N, bool MANY>
+__global__ void __launch_bounds__(kBlock, N == 32 ? 3 : 4) k_route(RouteArgs a) {
   typedef Gate<DT, L, N> G;
-  constexpr int S = EIGHT ? 1 : (SIM_ROUTE_MAX_TOPK + L - 1) / L;
+  constexpr int S = MANY ? (SIM_ROUTE_MAX_TOPK + L - 1) / L : 1;
   __shared__ uint32_t count_s[G::kAll + 1];
   __shared__ float sum_s[kWaves * G::kRows][G::kAll];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & (L - 1);
@@ -219,44 +246,70 @@ __global__ void __launch_bounds__(kBlock) k_route(RouteArgs a) {
     if (!kept) g.blank();
 
     // the chosen experts
+    constexpr uint32_t m = Ty<DT>::E == 4 ? ~(uint32_t)(G::kAll - 1) : 0xffff0000u;  // a key's value bits
     int mine[S];
     float at[S];
+#pragma unroll
+    for (int s = 0; s < S; s++) {
+      mine[s] = -1;
+      at[s] = 0.0f;
+    }
     float top_logit = kNegInf;
-    bool in_turn = !EIGHT;
-    if constexpr (EIGHT) {
-      constexpr uint32_t m = Ty<DT>::E == 4 ? ~(uint32_t)(G::kAll - 1) : 0xffff0000u;  // a key's value bits
+    uint32_t last = 0;
+    bool odd_key = false;
+    for (int done = 0; done < a.topk; done += 8) {
       uint32_t top[8];
-      top8(g, l, top);
+      if (MANY) g.renew();
+      top8(g, l, last, top);
       if constexpr (Ty<DT>::E == 4) {
         // exact if the topk keys differ above the index, no other key shares
         // the last one's value bits, and all of them are of finite logits
-        uint32_t last = top[0];
-        bool same = (top[0] & m) >= (ordered_inf<DT>() & m);
+        if (done == 0) odd_key = (top[0] & m) >= (ordered_inf<DT>() & m);
+        else odd_key = odd_key || (top[0] & m) == (last & m);
+        last = top[0];
 #pragma unroll
         for (int i = 1; i < 8; i++) {
-          if (i < a.topk) {
-            same = same || (top[i] & m) == (top[i - 1] & m);
+          if (done + i < a.topk) {
+            odd_key = odd_key || (top[i] & m) == (top[i - 1] & m);
             last = top[i];
           }
         }
-        last &= m;
-        same = same || last <= (ordered_neg_inf<DT>() & m);
-        float n = 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; i++) n += ordered<DT>(g.v[i / G::V][i % G::V]) >= last ? 1.0f : 0.0f;
-        in_turn = __any((same || group_sum<L>(n) != (float)a.topk) && kept);
       } else {
-        in_turn = __any((top[0] & m) > ordered_inf<DT>());  // a NaN
-        top_logit = from_ordered16<DT>(top[0]);
+        if (done == 0) {
+          odd_key = (top[0] & m) > ordered_inf<DT>();  // a NaN
+          top_logit = from_ordered16<DT>(top[0]);
+        }
+        last = top[7];
       }
+      // slot done + i goes to lane (done + i) mod L
+      const int i0 = MANY ? (l - done) & (L - 1) : l;
       uint32_t k = top[0];
 #pragma unroll
-      for (int i = 1; i < 8; i++) k = l == i ? top[i] : k;
-      const bool ok = l < a.topk && (k & m) > (ordered_neg_inf<DT>() & m);
-      mine[0] = ok ? G::kAll - 1 - (int)(k & (uint32_t)(G::kAll - 1)) : -1;
-      if constexpr (Ty<DT>::E == 2) at[0] = from_ordered16<DT>(k);
+      for (int i = 1; i < 8; i++) k = i0 == i ? top[i] : k;
+      const bool ok = i0 < 8 && done + i0 < a.topk && (k & m) > (ordered_neg_inf<DT>() & m);
+#pragma unroll
+      for (int s = 0; s < S; s++) {
+        if (!MANY || (ok && (done + i0) / L == s)) {
+          mine[s] = ok ? G::kAll - 1 - (int)(k & (uint32_t)(G::kAll - 1)) : -1;
+          if constexpr (Ty<DT>::E == 2) at[s] = from_ordered16<DT>(k);
+        }
+      }
+      if (!MANY) break;
     }
-    if (in_turn) top_in_turn<DT, L, N, S>(g, l, a.topk, mine);
+    g.renew();
+    if constexpr (Ty<DT>::E == 4) {
+      odd_key = odd_key || (last & m) <= (ordered_neg_inf<DT>() & m);
+      float n = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; i++) n += ordered<DT>(g.v[i / G::V][i % G::V]) >= (last & m) ? 1.0f : 0.0f;
+      odd_key = odd_key || group_sum<L>(n) != (float)a.topk;
+    }
+    const bool in_turn = __any(odd_key && kept);
+    if (in_turn) {
+      g.renew();
+      top_in_turn<DT, L, N, S>(g, l, a.topk, mine);
+    }
+    g.renew();
 
     // the softmax
     float f[N];
@@ -340,12 +393,12 @@ __global__ void __launch_bounds__(kSumCols* kSumRows) k_route_sum(RouteArgs a) {
   __shared__ float s_s[kSumRows][kSumCols];
   const int all = 2 * a.experts + 1, c = threadIdx.x % kSumCols, r = threadIdx.x / kSumCols;
   const int e = blockIdx.x * kSumCols + c;
-  const int span = (a.workgroups + kSumRows - 1) / kSumRows;
+  const int span = (a.workgroups + kSumRows - 1) / kSumRows;  // at most 16
   const int end = min(a.workgroups, (r + 1) * span);
   uint32_t n = 0;
   float s = 0.0f;
   if (e < all) {
-#pragma unroll 4
+#pragma unroll 8
     for (int w = r * span; w < end; w++) {
       const uint32_t v = a.partial[(int64_t)w * all + e];
       n += v;
@@ -482,39 +535,44 @@ __global__ void __launch_bounds__(kBlock) k_route_grad(RouteGradArgs a) {
 }
 
 // ---- launches -----------------------------------------------------------------------
-int rows_per_workgroup(int experts) { return kWaves * (experts <= 256 ? 8 : experts <= 512 ? 4 : 2); }
+// Workgroups that share the rows evenly, at most `most` of them.
+int64_t even_workgroups(int64_t tokens, int per, int64_t most) {
+  const int64_t n = (tokens + per - 1) / per, turns = (n + most - 1) / most;
+  return n < 1 ? 1 : (n + turns - 1) / turns;
+}
 
-template <int DT, bool EIGHT>
+template <int DT, bool MANY>
 hipError_t route_layout(const RouteArgs& a, hipStream_t s) {
+  constexpr int N = Ty<DT>::E == 2 ? 32 : 16;
   const dim3 grid(a.workgroups), block(kBlock);
-  if (a.experts <= 64) return launch<k_route<DT, 8, 8, EIGHT>>(grid, block, s, a);
-  if (a.experts <= 128) return launch<k_route<DT, 8, 16, EIGHT>>(grid, block, s, a);
-  if (a.experts <= 256) return launch<k_route<DT, 8, 32, EIGHT>>(grid, block, s, a);
-  if (a.experts <= 512) return launch<k_route<DT, 16, 32, EIGHT>>(grid, block, s, a);
-  return launch<k_route<DT, 32, 32, EIGHT>>(grid, block, s, a);
+  if (a.experts <= 64) return launch<k_route<DT, 8, 8, MANY>>(grid, block, s, a);
+  if (a.experts <= 128) return launch<k_route<DT, 8, 16, MANY>>(grid, block, s, a);
+  if (a.experts <= 256) return launch<k_route<DT, 256 / N, N, MANY>>(grid, block, s, a);
+  if (a.experts <= 512) return launch<k_route<DT, 512 / N, N, MANY>>(grid, block, s, a);
+  return launch<k_route<DT, 1024 / N, N, MANY>>(grid, block, s, a);
 }
 template <int DT>
 hipError_t route_dtype(const RouteArgs& a, hipStream_t s) {
-  return a.topk <= 8 ? route_layout<DT, true>(a, s) : route_layout<DT, false>(a, s);
+  return a.topk <= 8 ? route_layout<DT, false>(a, s) : route_layout<DT, true>(a, s);
 }
 template <int DT>
 hipError_t grad_dtype(const RouteGradArgs& a, hipStream_t s) {
-  const int per = rows_per_workgroup(a.experts);
-  const int64_t wg = (a.tokens + per - 1) / per, most = 8 * (int64_t)library_cus();
-  const dim3 grid((unsigned)(wg < 1 ? 1 : wg < most ? wg : most)), block(kBlock);
+  const int rows = a.experts <= 128 ? 8 : a.experts <= 256 ? 4 : a.experts <= 512 ? 2 : 1;
+  const dim3 grid((unsigned)even_workgroups(a.tokens, kWaves * rows, 4 * (int64_t)library_cus())), block(kBlock);
   if (a.experts <= 64) return launch<k_route_grad<DT, 8, 8>>(grid, block, s, a);
   if (a.experts <= 128) return launch<k_route_grad<DT, 8, 16>>(grid, block, s, a);
-  if (a.experts <= 256) return launch<k_route_grad<DT, 8, 32>>(grid, block, s, a);
-  if (a.experts <= 512) return launch<k_route_grad<DT, 16, 32>>(grid, block, s, a);
-  return launch<k_route_grad<DT, 32, 32>>(grid, block, s, a);
+  if (a.experts <= 256) return launch<k_route_grad<DT, 16, 16>>(grid, block, s, a);
+  if (a.experts <= 512) return launch<k_route_grad<DT, 32, 16>>(grid, block, s, a);
+  return launch<k_route_grad<DT, 64, 16>>(grid, block, s, a);
 }
 
 }  // namespace
 
-int route_workgroups(int64_t tokens, int experts) {
-  const int per = rows_per_workgroup(experts);
-  const int64_t wg = (tokens + per - 1) / per, most = 4 * (int64_t)library_cus();
-  return (int)(wg < 3 ? 1 : wg < most ? wg : most);
+int route_workgroups(int64_t tokens, int experts, int dtype) {
+  const int n = dtype == SIM_FP32 ? 16 : 32;
+  const int rows = experts <= 128 ? 8 : 64 * n / (experts <= 256 ? 256 : experts <= 512 ? 512 : 1024);
+  const int64_t wg = even_workgroups(tokens, kWaves * rows, (n == 32 && experts > 128 ? 2 : 4) * (int64_t)library_cus());
+  return (int)(wg < 3 ? 1 : wg);
 }
 
 hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s) {

@@ -69,7 +69,7 @@ struct DistillArgs {
   int64_t span;       // columns per workgroup
 };
 
-int route_workgroups(int64_t tokens, int experts);
+int route_workgroups(int64_t tokens, int experts, int dtype);
 hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s);
 hipError_t launch_route_grad(const RouteGradArgs& a, int dtype, hipStream_t s);
 
