@@ -4,7 +4,6 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <cmath>
 
 #include "loss.h"
 
@@ -73,7 +72,7 @@ int check_distill(int64_t rows, int64_t cols, int64_t stride, int dtype, int64_t
                   int topk, float tau) {
   if (!float_dtype(dtype) || !float_dtype(tdtype)) return SIM_ERR_INVALID_ARG;
   if (topk < 1 || topk > SIM_DISTILL_MAX_TOPK) return SIM_ERR_INVALID_ARG;
-  if (!(tau > 0.0f) || !std::isfinite(tau)) return SIM_ERR_INVALID_ARG;
+  if (!(tau >= 1e-20f && tau <= 1e20f)) return SIM_ERR_INVALID_ARG;
   if (!rows_fit(rows, cols, stride)) return SIM_ERR_INVALID_ARG;
   if (vocab < 1 || vocab > INT32_MAX || first < 0 || first > vocab - cols) return SIM_ERR_INVALID_ARG;
   return rows > kMaxGrid ? SIM_ERR_INVALID_ARG : SIM_OK;

@@ -51,15 +51,16 @@ __device__ __forceinline__ Slots load_slots(const DistillArgs& a, int64_t row, i
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < kSlotsPerLane; i++) {
-    s.q[i] = z[i] == kNegInf ? 0.0f : exp2_hw((z[i] - top) * c);
+    s.q[i] = z[i] == kNegInf ? 0.0f : exp2_hw((z[i] - top) * c + 32.0f);  // (32: see Against)
     sum += s.q[i];
   }
   sum = wave_sum(sum);
-  const float log_sum = __logf(sum), inv = 1.0f / sum;
+  sum *= 0x1p-32f;
+  const float log_sum = __logf(sum);
   float h = 0.0f;
 #pragma unroll
   for (int i = 0; i < kSlotsPerLane; i++) {
-    s.q[i] = s.live ? s.q[i] * inv : 0.0f;
+    s.q[i] = s.live ? s.q[i] * 0x1p-32f / sum : 0.0f;
     if (!(s.q[i] == 0.0f)) h += s.q[i] * ((z[i] - top) / a.tau - log_sum);
   }
   s.entropy = s.live ? wave_sum(h) : 0.0f;
@@ -103,17 +104,17 @@ __device__ __forceinline__ void gather_slots(const DistillArgs& a, SlotLists<NT>
   }
   if (lane == 0) s.live = sl.live;
 }
-// Wave 0, once the row's maximum m and sum are known: each slot's probability,
-// and its place in its thread's list.
+// Wave 0, once the row's maximum and its sum against `top` are known: each
+// slot's probability, and its place in its thread's list.
 template <int DT, int NT>
 __device__ __forceinline__ void hang_slots(const DistillArgs& a, SlotLists<NT>& s, const Slots& sl, int64_t lo,
-                                           int64_t hi, float m, float sum, float c, int lane) {
+                                           int64_t hi, const Against& top, float sum, int lane) {
 #pragma unroll
   for (int i = 0; i < kSlotsPerLane; i++) {
     const int k = lane + 64 * i;
     const int64_t col = (int64_t)sl.id[i] - a.first;
     if (!sl.live || sl.id[i] < 0 || col < lo || col >= hi) continue;
-    s.x[k] = exp2_hw((s.x[k] - m) * c) / sum;
+    s.x[k] = exp_against(s.x[k], top) / sum;
     s.next[k] = atomicExch(&s.head[((col - lo) / epv<DT>()) % NT], k);
   }
 }

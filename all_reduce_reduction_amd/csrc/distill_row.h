@@ -21,7 +21,10 @@ namespace simar {
 template <int DT, int NT, int R, int GUARD>
 __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
   constexpr int V = epv<DT>(), W = NT / 64, PAIR = R % 2 ? 1 : 2;
-  constexpr bool STREAM = NT < 1024;
+  #ifndef STRM
+#define STRM (NT < 1024)
+#endif
+  constexpr bool STREAM = STRM;
   __shared__ SlotLists<NT> slots;
   __shared__ float m_s[W], s_s[W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -42,20 +45,20 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
     sl = load_slots(a, row, lane);
     gather_slots<DT>(a, slots, sl, x, 0, a.cols, lane);
   }
-  Running r{kNegInf, 0.0f};
+  Scan scan;
 #pragma unroll
   for (int i = 0; i < R; i += PAIR) {
     float f[PAIR * V];
 #pragma unroll
     for (int j = 0; j < PAIR; j++) unpack<DT>(v[i + j], f + j * V);
-    running_add(r, f, c);
+    scan.add(f, c);
   }
   for (int64_t col = (int64_t)(R * NT + tid) * V; col < a.cols; col += NT * V) {
     float f[V];
     load_cols<DT>(x, col, a.cols, f);
-    running_add(r, f, c);
+    scan.add(f, c);
   }
-  r = wave_running(r, c);
+  Running r = wave_running(scan.done(c), c);
   if (lane == 0) {
     m_s[wave] = r.m;
     s_s[wave] = r.s;
@@ -64,7 +67,23 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
   r.m = lane < W ? m_s[lane] : kNegInf;
   r.s = lane < W ? s_s[lane] : 0.0f;
   r = wave_running(r, c);
+  if (__builtin_expect(far(r.m, c), 0)) {
+    float n = 0.0f;
+#pragma unroll 1
+    for (int64_t col = (int64_t)tid * V; col < a.cols; col += NT * V) {
+      float f[V];
+      load_cols<DT>(x, col, a.cols, f);
+      n += count_of(f, r.m);
+    }
+    n = wave_sum(n);
+    __syncthreads();
+    if (lane == 0) s_s[wave] = n;
+    __syncthreads();
+    r.s += wave_sum(lane < W ? s_s[lane] : 0.0f);
+  }
   const bool live = slots.live;
+  const Against top = against(r.m, c);
+  const float sum = r.s * exp2_hw(at_max(r.m, top));  // against top.t
   if (wave == 0) {
     float dot = 0.0f;
 #pragma unroll
@@ -75,10 +94,16 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
     }
     dot = wave_sum(dot);
     if (lane == 0) a.loss[row] = live ? sl.entropy + __logf(r.s) - dot : 0.0f;
-    hang_slots<DT>(a, slots, sl, 0, a.cols, r.m, r.s, c, lane);
+    hang_slots<DT>(a, slots, sl, 0, a.cols, top, sum, lane);
   }
-  const float k2 = live ? up / r.s : 0.0f;
+  const float k2 = up / sum;
   __syncthreads();
+  if (!live) {
+    // (0 * p would keep the NaN of a row that does not count)
+    const float f[V] = {};
+    for (int64_t col = (int64_t)tid * V; col < a.cols; col += NT * V) st_guarded<DT>(dx, col, a.cols, f);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < R; i++) {
     // widened again here: kept from above, the fp32 values would take the
@@ -87,37 +112,38 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
     float f[V];
     unpack<DT>(v[i], f);
 #pragma unroll
-    for (int j = 0; j < V; j++) f[j] = live ? exp2_hw((f[j] - r.m) * c) * k2 : 0.0f;
-    if (i < R - GUARD) st_row_lane<DT, STREAM>(dx, i * NT * V, tid * V, pack<DT>(f));
+    for (int j = 0; j < V; j++) f[j] = exp_against(f[j], top) * k2;
+    if (i < R - GUARD) st_row_lane<DT, STREAM>(dx, i * NT * V, tid * V, pack_rounded<DT>(f));
     else st_guarded<DT>(dx, (int64_t)(i * NT + tid) * V, a.cols, f);
   }
   for (int64_t col = (int64_t)(R * NT + tid) * V; col < a.cols; col += NT * V) {
     float f[V];
     load_cols<DT>(x, col, a.cols, f);
 #pragma unroll
-    for (int j = 0; j < V; j++) f[j] = live ? exp2_hw((f[j] - r.m) * c) * k2 : 0.0f;
+    for (int j = 0; j < V; j++) f[j] = exp_against(f[j], top) * k2;
     st_guarded<DT>(dx, col, a.cols, f);
   }
   write_slots<DT>(a, slots, dx, up, tid);
 }
 
-// The workgroup and the vectors per thread for a row of n vectors: the
-// smallest workgroup that holds it in 16 vectors per thread.  R comes in
-// steps of 2 from 4 on, so the last two vectors of a thread may lie past the
-// row's end.
+// The workgroup and the vectors per thread for a row of n vectors.  Where the
+// rows fill the GPU, the smallest workgroup that holds a row in 16 vectors per
+// thread: more of them share a compute unit, and one's reads run while another
+// computes or writes.  With fewer rows than compute units, the largest that
+// gives each thread a vector or more: there a row's own time counts.  R comes
+// in steps of 2 from 4 on, so the last two vectors of a thread may lie past
+// the row's end.
 template <int DT, int NT, int R>
 hipError_t launch_row_as(const DistillArgs& a, hipStream_t s) {
   constexpr int G = R < 4 ? 1 : 2;
   return launch<k_distill_row<DT, NT, R, G>>(dim3((unsigned)a.rows), dim3(NT), s, a);
 }
-template <int DT, int NT, bool SHORT>
+template <int DT, int NT>
 hipError_t launch_row_with(const DistillArgs& a, int64_t vectors, hipStream_t s) {
   const int r = (int)((vectors + NT - 1) / NT);
-  if constexpr (SHORT) {
-    if (r <= 1) return launch_row_as<DT, NT, 1>(a, s);
-    if (r <= 2) return launch_row_as<DT, NT, 2>(a, s);
-    if (r <= 3) return launch_row_as<DT, NT, 3>(a, s);
-  }
+  if (r <= 1) return launch_row_as<DT, NT, 1>(a, s);
+  if (r <= 2) return launch_row_as<DT, NT, 2>(a, s);
+  if (r <= 3) return launch_row_as<DT, NT, 3>(a, s);
   if (r <= 4) return launch_row_as<DT, NT, 4>(a, s);
   if (r <= 6) return launch_row_as<DT, NT, 6>(a, s);
   if (r <= 8) return launch_row_as<DT, NT, 8>(a, s);
@@ -129,10 +155,20 @@ hipError_t launch_row_with(const DistillArgs& a, int64_t vectors, hipStream_t s)
 template <int DT>
 hipError_t launch_row(const DistillArgs& a, hipStream_t s) {
   const int64_t n = (a.cols + epv<DT>() - 1) / epv<DT>();
-  if (n <= 64 * 16) return launch_row_with<DT, 64, true>(a, n, s);
-  if (n <= 256 * 16) return launch_row_with<DT, 256, false>(a, n, s);
-  if (n <= 512 * 16) return launch_row_with<DT, 512, false>(a, n, s);
-  return launch_row_with<DT, 1024, false>(a, n, s);
+#ifndef FEW
+#define FEW 1
+#endif
+  if (a.rows <= FEW * library_cus()) {
+    if (n > 512) return launch_row_with<DT, 1024>(a, n, s);
+    if (n > 128) return launch_row_with<DT, 256>(a, n, s);
+  }
+#ifndef C64
+#define C64 16
+#endif
+  if (n <= 64 * C64) return launch_row_with<DT, 64>(a, n, s);
+  if (n <= 256 * 16) return launch_row_with<DT, 256>(a, n, s);
+  if (n <= 512 * 16) return launch_row_with<DT, 512>(a, n, s);
+  return launch_row_with<DT, 1024>(a, n, s);
 }
 
 }  // namespace simar

@@ -53,29 +53,42 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
       if (!here) sl.q[i] = 0.0f;
     }
   }
-  Running r{kNegInf, 0.0f};
+  Scan scan;
   for (int64_t col = lo;;) {
 #pragma unroll
     for (int i = 0; i < kHeld; i++) {
       if (col + i * kBlock * V >= hi) continue;
       float f[V];
       unpack<DT>(v[i], f);
-      running_add(r, f, c);
+      scan.add(f, c);
     }
     col += kHeld * kBlock * V;
     if (col >= hi) break;
     load_chunk<DT>(x, col, hi, tid, v);
   }
-  r = wave_running(r, c);
+  Running r = wave_running(scan.done(c), c);
   if (lane == 0) {
     m_s[wave] = r.m;
     s_s[wave] = r.s;
   }
   __syncthreads();
+  r.m = lane < W ? m_s[lane] : kNegInf;
+  r.s = lane < W ? s_s[lane] : 0.0f;
+  r = wave_running(r, c);
+  if (__builtin_expect(far(r.m, c), 0)) {
+    float n = 0.0f;
+    for (int64_t col = lo + (int64_t)tid * V; col < hi; col += kBlock * V) {
+      float f[V];
+      load_cols<DT>(x, col, hi, f);
+      n += count_of(f, r.m);
+    }
+    n = wave_sum(n);
+    __syncthreads();
+    if (lane == 0) s_s[wave] = n;
+    __syncthreads();
+    r.s += wave_sum(lane < W ? s_s[lane] : 0.0f);
+  }
   if (wave == 0) {
-    r.m = lane < W ? m_s[lane] : kNegInf;
-    r.s = lane < W ? s_s[lane] : 0.0f;
-    r = wave_running(r, c);
     float mass = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < kSlotsPerLane; i++) {
@@ -143,17 +156,25 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
   } else {
     t = join_parts(a.parts, a.splits, a.rows, row, a.tau, lane);
   }
+  const Against top = against(t.m, c);
+  const float sum = t.s * exp2_hw(at_max(t.m, top));  // against top.t
   __syncthreads();
   if (wave == 0) {
     const Slots sl = load_slots(a, row, lane);
     gather_slots<DT>(a, slots, sl, x, lo, hi, lane);
     wave_fence();
     if (lane == 0 && a.loss && split == 0) a.loss[row] = loss_of(sl, t);
-    hang_slots<DT>(a, slots, sl, lo, hi, t.m, t.s, c, lane);
+    hang_slots<DT>(a, slots, sl, lo, hi, top, sum, lane);
   }
   __syncthreads();
   const bool live = slots.live;
-  const float k2 = live ? up / t.s : 0.0f;
+  if (!live) {
+    // (0 * p would keep the NaN of a row that does not count)
+    const float f[V] = {};
+    for (int64_t col = lo + (int64_t)tid * V; col < hi; col += kBlock * V) st_guarded<DT>(dx, col, hi, f);
+    return;
+  }
+  const float k2 = up / sum;
   for (int64_t col = lo;;) {
     const bool whole = col + kHeld * kBlock * V <= hi;
 #pragma unroll
@@ -162,8 +183,8 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
       float f[V];
       unpack<DT>(v[i], f);
 #pragma unroll
-      for (int j = 0; j < V; j++) f[j] = live ? exp2_hw((f[j] - t.m) * c) * k2 : 0.0f;
-      if (whole) st_row_lane<DT, true>(dx, col + i * kBlock * V, tid * V, pack<DT>(f));
+      for (int j = 0; j < V; j++) f[j] = exp_against(f[j], top) * k2;
+      if (whole) st_row_lane<DT, true>(dx, col + i * kBlock * V, tid * V, pack_rounded<DT>(f));
       else st_guarded<DT>(dx, col + (i * kBlock + tid) * V, hi, f);
     }
     col += kHeld * kBlock * V;

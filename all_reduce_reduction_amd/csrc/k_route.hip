@@ -326,11 +326,11 @@ __global__ void __launch_bounds__(kBlock, N == 32 ? 3 : 4) k_route(RouteArgs a) 
       odd = group_any<L>(odd, lane);
     }
     const bool live = odd || top_logit > kNegInf;
-    const float base = live ? top_logit : 0.0f;
+    const Against base = against(top_logit, kLog2e);
     float z = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; i++) {
-      f[i] = exp2_hw((f[i] - base) * kLog2e);
+      f[i] = exp_against(f[i], base);
       z += f[i];
     }
     z = group_sum<L>(z);
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kBlock, N == 32 ? 3 : 4) k_route(RouteArgs a) 
 #pragma unroll
     for (int s = 0; s < S; s++) {
       if (Ty<DT>::E == 4 || in_turn) at[s] = mine[s] >= 0 ? load_elem<DT>(x, mine[s]) : 0.0f;
-      w[s] = mine[s] >= 0 ? exp2_hw((at[s] - base) * kLog2e) * inv : 0.0f;
+      w[s] = mine[s] >= 0 ? exp_against(at[s], base) * inv : 0.0f;
       total += w[s];
     }
     if (a.normalize) {
@@ -477,11 +477,11 @@ __global__ void __launch_bounds__(kBlock) k_route_grad(RouteGradArgs a) {
     for (int i = 0; i < N; i++) top = fmaxf(top, f[i]);
     top = group_max<L>(top);
     // a row of NaN and -inf alone is not empty: its sum is NaN
-    const float base = top == kNegInf ? 0.0f : top;
+    const Against base = against(top, kLog2e);
     float z = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; i++) {
-      f[i] = exp2_hw((f[i] - base) * kLog2e);
+      f[i] = exp_against(f[i], base);
       z += f[i];
     }
     z = group_sum<L>(z);
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(kBlock) k_route_grad(RouteGradArgs a) {
     float p[S], sum = 0.0f, mean = 0.0f;
 #pragma unroll
     for (int s = 0; s < S; s++) {
-      p[s] = mine[s] >= 0 && live ? exp2_hw((at[s] - base) * kLog2e) * inv : 0.0f;
+      p[s] = mine[s] >= 0 && live ? exp_against(at[s], base) * inv : 0.0f;
       sum += p[s];
       mean = __builtin_fmaf(p[s], dw[s], mean);
     }
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kBlock) k_route_grad(RouteGradArgs a) {
         d[t] = __builtin_fmaf(f[j * V + t], g_s[e] - dot, add[e]);
       }
       if (here) {
-        if (a.experts == G::kAll) st_row<DT>(dx, G::col(j, l), pack<DT>(d));
+        if (a.experts == G::kAll) st_row<DT>(dx, G::col(j, l), pack_rounded<DT>(d));
         else st_guarded<DT>(dx, G::col(j, l), a.experts, d);
       }
     }

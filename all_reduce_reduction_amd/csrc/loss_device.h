@@ -56,6 +56,26 @@ __device__ __forceinline__ void st_row_lane(void* row, int64_t elem, uint32_t la
   else *q = v;
 }
 
+// fp32 values rounded to storage, two at a time.
+template <int DT>
+__device__ __forceinline__ u32x4 pack_rounded(const float (&f)[epv<DT>()]) {
+  if constexpr (Ty<DT>::E == 4) {
+    return pack<DT>(f);
+  } else {
+    typedef float F2 __attribute__((ext_vector_type(2)));
+    typedef _Float16 H2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 B2 __attribute__((ext_vector_type(2)));
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const F2 p = {f[2 * i], f[2 * i + 1]};
+      if constexpr (DT == SIM_FP16) v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, H2));
+      else v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, B2));
+    }
+    return v;
+  }
+}
+
 template <int DT> constexpr uint32_t neg_inf_bits() {
   return DT == SIM_FP32 ? 0xff800000u : DT == SIM_FP16 ? 0xfc00fc00u : 0xff80ff80u;
 }
@@ -85,7 +105,7 @@ template <int DT>
 __device__ __forceinline__ void st_guarded(void* row, int64_t col, int64_t cols, const float (&x)[epv<DT>()]) {
   constexpr int V = epv<DT>();
   if (col + V <= cols) {
-    st_row<DT>(row, col, pack<DT>(x));
+    st_row<DT>(row, col, pack_rounded<DT>(x));
   } else {
 #pragma unroll
     for (int i = 0; i < V; i++)
@@ -159,27 +179,46 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Exponentials against a maximum m as one multiply-add: 2^(x c - t) with
+// t = m c - 32, so that what lies up to 2^-158 below the maximum is still a
+// normal number (the hardware's 2^x flushes others).  t's own rounding is no
+// error of the sums, which are taken against t, not m; at_max() is the exact
+// distance m c - t (at most 96, as |m c| stays below 2^31) for what has to be
+// taken against m.  Where a finite m has |m c| >= 2^31 (far()), c is cut to a
+// power of two, which makes t = m c exact: neighbouring floats lie 128 / c
+// apart there or more, so the result is 1 at m and 0 below it with either.
+// For m = -inf, t is 0 (2^-inf is 0); for +inf the results are NaN.  c lies
+// below 2^67.
+constexpr float kFar = 2147483648.0f;
+__device__ __forceinline__ bool far(float m, float c) { return fabsf(m) < __builtin_inff() && !(fabsf(m * c) < kFar); }
+struct Against {
+  float c, t;
+};
+__device__ __forceinline__ Against against(float m, float c) {
+  Against r{c, m == kNegInf ? 0.0f : m * c - 32.0f};
+  if (__builtin_expect(far(m, c), 0)) {
+    r.c = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, c) & 0xff800000u);
+    if (fabsf(m) >= 0x1p60f) r.c = fminf(r.c, 1.0f);
+    r.t = m * r.c;
+  }
+  return r;
+}
+__device__ __forceinline__ float exp_against(float x, const Against& r) {
+  return exp2_hw(__builtin_fmaf(x, r.c, -r.t));
+}
+__device__ __forceinline__ float at_max(float m, const Against& r) {
+  return m == kNegInf ? 0.0f : __builtin_fmaf(m, r.c, -r.t);
+}
+
 // A softmax's running maximum m and sum s of 2^((x - m) c), over the x seen
-// so far (m = -inf, s = 0 for none).  While m is -inf the exponents are
-// taken against 0, where a -inf counts 0.  A NaN never enters m and makes s
-// NaN; so does +inf.
+// so far (m = -inf, s = 0 for none).  A NaN never enters m and makes s NaN;
+// so does +inf.
 struct Running {
   float m, s;
 };
 // factor that brings a sum taken against m over to the maximum top >= m
 __device__ __forceinline__ float rebase(float m, float top, float c) {
   return m == top ? 1.0f : exp2_hw((m - top) * c);
-}
-template <int N>
-__device__ __forceinline__ void running_add(Running& r, const float (&x)[N], float c) {
-  float top = r.m;
-#pragma unroll
-  for (int i = 0; i < N; i++) top = fmaxf(top, x[i]);
-  r.s *= rebase(r.m, top, c);
-  r.m = top;
-  const float at = top == kNegInf ? 0.0f : top;
-#pragma unroll
-  for (int i = 0; i < N; i++) r.s += exp2_hw((x[i] - at) * c);
 }
 __device__ __forceinline__ Running running_join(const Running& a, const Running& b, float c) {
   Running r;
@@ -192,6 +231,35 @@ __device__ __forceinline__ Running wave_running(Running r, float c) {
   r.s = wave_sum(r.s * rebase(r.m, top, c));
   r.m = top;
   return r;
+}
+// One thread's sum on its way, taken against t = m c.  A maximum that is -inf
+// or far() leaves the sum 0: below zero that is what it is worth against any
+// other maximum, and a row whose own maximum is far() is counted again.
+struct Scan {
+  float m = kNegInf, s = 0.0f, t = -kFar;
+  template <int N>
+  __device__ __forceinline__ void add(const float (&x)[N], float c) {
+#pragma unroll
+    for (int i = 0; i < N; i++) m = fmaxf(m, x[i]);
+    float next = fmaxf(m * c, -kFar);
+    next = next < kFar ? next : __builtin_inff();
+    s *= exp2_hw(fminf(t - next, 0.0f));
+    t = next;
+#pragma unroll
+    for (int i = 0; i < N; i++) s += exp2_hw(__builtin_fmaf(x[i], c, -t));
+  }
+  // against m; a NaN stays one
+  __device__ __forceinline__ Running done(float c) const {
+    return Running{m, s * (fabsf(m * c) < kFar ? exp2_hw(-__builtin_fmaf(m, c, -t)) : 0.0f)};
+  }
+};
+// how many of the values are the maximum, in a row where it is far()
+template <int N>
+__device__ __forceinline__ float count_of(const float (&x)[N], float m) {
+  float n = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; i++) n += x[i] == m ? 1.0f : 0.0f;
+  return n;
 }
 
 }  // namespace simar

@@ -512,7 +512,7 @@ int sim_route_grad(const void* logits, int64_t row_stride, int dtype, const uint
  * row_scale (may be NULL: all 1) is the upstream gradient of loss[t]; neither
  * it nor coef scales loss.  A row with no slot, or with teacher logits of
  * -inf in all of them, has loss 0 and a zero gradient whatever its logits
- * hold (its logits are not read).  Otherwise a NaN, a +inf or a row of -inf
+ * hold.  temperature lies in [1e-20, 1e20].  Otherwise a NaN, a +inf or a row of -inf
  * alone makes that row's loss and gradient NaN; an id whose own logit is -inf
  * makes the loss +inf.
  *

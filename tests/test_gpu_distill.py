@@ -101,6 +101,27 @@ def test_empty_rows_and_special_values(lib, dtype, t):
     assert torch.isinf(loss[9]) and torch.isnan(loss[[6, 7, 8, 10]]).all()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("t", [5, 600])
+def test_logits_at_the_ends_of_the_type(lib, dtype, t):
+    """Rows whose logits are all so large that logit / temperature overflows, beside ordinary ones."""
+    v, k = 2100, 7
+    x, ids, z, _ = case(t, v, k, dtype, torch.float32, 78, holes=False)
+    low, high = torch.finfo(dtype).min, torch.finfo(dtype).max
+    x[0] = low                    # masked everywhere: the softmax is even
+    x[1] = high
+    x[2, :v - 50] = low           # masked by the type's lowest value, ordinary elsewhere
+    x[3, 40:] = low
+    x[3, :40] = -INF
+    x[4, 100] = high
+    ids[2, 0] = v - 1
+    for tau in (1.0, 0.25, 1e-3):
+        loss, d = step(lib, x, ids, z, tau)
+        check(x, ids, z, tau, None, 1.0, loss, d, f"tau {tau}")
+        loss, d, _ = shards(lib, x, ids, z, tau, None, 1.0, 2)
+        check(x, ids, z, tau, None, 1.0, loss, d, f"shards, tau {tau}")
+
+
 def test_repeated_ids_add_up(lib):
     x, ids, z, _ = case(40, 500, 16, torch.float32, torch.float32, 5, holes=False)
     ids[:, 8:] = ids[:, :8]
