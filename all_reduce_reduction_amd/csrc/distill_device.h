@@ -31,6 +31,7 @@ __device__ __forceinline__ Slots load_slots(const DistillArgs& a, int64_t row, i
   bool some = false;
 #pragma unroll
   for (int i = 0; i < kSlotsPerLane; i++) {
+    if (64 * i >= a.topk) break;
     const int k = lane + 64 * i;
     s.id[i] = -1;
     z[i] = kNegInf;
@@ -51,16 +52,18 @@ __device__ __forceinline__ Slots load_slots(const DistillArgs& a, int64_t row, i
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < kSlotsPerLane; i++) {
-    s.q[i] = z[i] == kNegInf ? 0.0f : exp2_hw((z[i] - top) * c + 32.0f);  // (32: see Against)
+    if (64 * i >= a.topk) break;
+    s.q[i] = z[i] == kNegInf ? 0.0f : exp2_hw((z[i] - top) * c + 8.0f);  // (8: see Against)
     sum += s.q[i];
   }
   sum = wave_sum(sum);
-  sum *= 0x1p-32f;
+  sum *= 0x1p-8f;
   const float log_sum = __logf(sum);
   float h = 0.0f;
 #pragma unroll
   for (int i = 0; i < kSlotsPerLane; i++) {
-    s.q[i] = s.live ? s.q[i] * 0x1p-32f / sum : 0.0f;
+    if (64 * i >= a.topk) break;
+    s.q[i] = s.live ? s.q[i] * 0x1p-8f / sum : 0.0f;
     if (!(s.q[i] == 0.0f)) h += s.q[i] * ((z[i] - top) / a.tau - log_sum);
   }
   s.entropy = s.live ? wave_sum(h) : 0.0f;
@@ -95,6 +98,7 @@ __device__ __forceinline__ void gather_slots(const DistillArgs& a, SlotLists<NT>
                                              int64_t lo, int64_t hi, int lane) {
 #pragma unroll
   for (int i = 0; i < kSlotsPerLane; i++) {
+    if (64 * i >= a.topk) break;
     const int k = lane + 64 * i;
     if (k >= a.topk) continue;
     const int64_t col = (int64_t)sl.id[i] - a.first;
@@ -111,6 +115,7 @@ __device__ __forceinline__ void hang_slots(const DistillArgs& a, SlotLists<NT>& 
                                            int64_t hi, const Against& top, float sum, int lane) {
 #pragma unroll
   for (int i = 0; i < kSlotsPerLane; i++) {
+    if (64 * i >= a.topk) break;
     const int k = lane + 64 * i;
     const int64_t col = (int64_t)sl.id[i] - a.first;
     if (!sl.live || sl.id[i] < 0 || col < lo || col >= hi) continue;

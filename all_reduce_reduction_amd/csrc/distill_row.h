@@ -18,14 +18,10 @@
 namespace simar {
 
 // of the R vectors of a thread, the last GUARD may lie past the row's end
-template <int DT, int NT, int R, int GUARD>
+template <int DT, int NT, int R, int GUARD, bool STREAM>
 __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
   constexpr int V = epv<DT>(), W = NT / 64, PAIR = R % 2 ? 1 : 2;
-  #ifndef STRM
-#define STRM (NT < 1024)
-#endif
-  constexpr bool STREAM = STRM;
-  __shared__ SlotLists<NT> slots;
+    __shared__ SlotLists<NT> slots;
   __shared__ float m_s[W], s_s[W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x;
@@ -88,6 +84,7 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < kSlotsPerLane; i++) {
+      if (64 * i >= a.topk) break;
       if (sl.id[i] < 0 || sl.q[i] == 0.0f) continue;
       const float at = slots.x[lane + 64 * i];
       dot += at == kNegInf ? sl.q[i] * kNegInf : sl.q[i] * ((at - r.m) / a.tau);
@@ -126,49 +123,48 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
   write_slots<DT>(a, slots, dx, up, tid);
 }
 
-// The workgroup and the vectors per thread for a row of n vectors.  Where the
-// rows fill the GPU, the smallest workgroup that holds a row in 16 vectors per
-// thread: more of them share a compute unit, and one's reads run while another
-// computes or writes.  With fewer rows than compute units, the largest that
-// gives each thread a vector or more: there a row's own time counts.  R comes
-// in steps of 2 from 4 on, so the last two vectors of a thread may lie past
-// the row's end.
-template <int DT, int NT, int R>
+// The workgroup, the vectors per thread (R, in steps of 2 from 4 on, so that
+// the last two of a thread may lie past the row's end) and the cache policy
+// for a row of n vectors, measured on MI355X (us, bf16):
+//   - fewer rows than compute units: the largest workgroup, as a row's own time
+//     counts (256 rows x 32,768: 1024 threads 11.8, 256 threads 18.3);
+//   - rows of up to 32 KiB, any number: cached accesses, small workgroups
+//     (32,768 x 8,192: 193, streaming 264);
+//   - longer rows, less than 512 MiB of them: streaming accesses and the
+//     smallest workgroup that holds a row in 16 vectors per thread, so that
+//     several share a compute unit and one reads while another computes or
+//     writes (2,048 x 65,536: 93, cached 107, 1024 threads 104);
+//   - 512 MiB and more, which the 256 MiB memory-side cache helps little:
+//     cached accesses and one workgroup per compute unit, whose reads and
+//     writes come in long runs (16,384 x 32,768: 407, cached in small
+//     workgroups 444, streaming in them 494).
+template <int DT, int NT, int R, bool STREAM>
 hipError_t launch_row_as(const DistillArgs& a, hipStream_t s) {
   constexpr int G = R < 4 ? 1 : 2;
-  return launch<k_distill_row<DT, NT, R, G>>(dim3((unsigned)a.rows), dim3(NT), s, a);
+  return launch<k_distill_row<DT, NT, R, G, STREAM>>(dim3((unsigned)a.rows), dim3(NT), s, a);
 }
-template <int DT, int NT>
+// the smallest R of LEAST, ..., MOST that holds the row (MOST where none does)
+template <int DT, int NT, bool STREAM, int LEAST, int MOST>
 hipError_t launch_row_with(const DistillArgs& a, int64_t vectors, hipStream_t s) {
-  const int r = (int)((vectors + NT - 1) / NT);
-  if (r <= 1) return launch_row_as<DT, NT, 1>(a, s);
-  if (r <= 2) return launch_row_as<DT, NT, 2>(a, s);
-  if (r <= 3) return launch_row_as<DT, NT, 3>(a, s);
-  if (r <= 4) return launch_row_as<DT, NT, 4>(a, s);
-  if (r <= 6) return launch_row_as<DT, NT, 6>(a, s);
-  if (r <= 8) return launch_row_as<DT, NT, 8>(a, s);
-  if (r <= 10) return launch_row_as<DT, NT, 10>(a, s);
-  if (r <= 12) return launch_row_as<DT, NT, 12>(a, s);
-  if (r <= 14) return launch_row_as<DT, NT, 14>(a, s);
-  return launch_row_as<DT, NT, 16>(a, s);
+  if constexpr (LEAST < MOST) {
+    constexpr int NEXT = LEAST < 4 ? LEAST + 1 : LEAST + 2;
+    if (vectors > (int64_t)NT * LEAST) return launch_row_with<DT, NT, STREAM, NEXT, MOST>(a, vectors, s);
+  }
+  return launch_row_as<DT, NT, LEAST, STREAM>(a, s);
 }
 template <int DT>
 hipError_t launch_row(const DistillArgs& a, hipStream_t s) {
   const int64_t n = (a.cols + epv<DT>() - 1) / epv<DT>();
-#ifndef FEW
-#define FEW 1
-#endif
-  if (a.rows <= FEW * library_cus()) {
-    if (n > 512) return launch_row_with<DT, 1024>(a, n, s);
-    if (n > 128) return launch_row_with<DT, 256>(a, n, s);
+  const bool few = a.rows <= library_cus();
+  if (n <= 2048) {
+    if (few && n > 512) return launch_row_with<DT, 1024, false, 1, 2>(a, n, s);
+    if (!few && n <= 256) return launch_row_with<DT, 64, false, 1, 4>(a, n, s);
+    return launch_row_with<DT, 256, false, 1, 8>(a, n, s);
   }
-#ifndef C64
-#define C64 16
-#endif
-  if (n <= 64 * C64) return launch_row_with<DT, 64>(a, n, s);
-  if (n <= 256 * 16) return launch_row_with<DT, 256>(a, n, s);
-  if (n <= 512 * 16) return launch_row_with<DT, 512>(a, n, s);
-  return launch_row_with<DT, 1024>(a, n, s);
+  if (!few && a.rows * a.cols * Ty<DT>::E >= ((int64_t)512 << 20))
+    return launch_row_with<DT, 1024, false, 3, 16>(a, n, s);
+  if (few || n > 8192) return launch_row_with<DT, 1024, true, 3, 16>(a, n, s);
+  return n <= 4096 ? launch_row_with<DT, 256, true, 10, 16>(a, n, s) : launch_row_with<DT, 512, true, 10, 16>(a, n, s);
 }
 
 }  // namespace simar

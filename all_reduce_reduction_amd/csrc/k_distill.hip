@@ -47,6 +47,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
     sl = load_slots(a, row, lane);
 #pragma unroll
     for (int i = 0; i < kSlotsPerLane; i++) {
+      if (64 * i >= a.topk) break;
       const int64_t col = (int64_t)sl.id[i] - a.first;
       const bool here = sl.id[i] >= 0 && col >= lo && col < hi;
       at[i] = here ? load_elem<DT>(x, col) : 0.0f;
@@ -92,6 +93,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
     float mass = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < kSlotsPerLane; i++) {
+      if (64 * i >= a.topk) break;
       if (sl.q[i] == 0.0f) continue;
       mass += sl.q[i];
       dot += at[i] == kNegInf ? sl.q[i] * kNegInf : sl.q[i] * ((at[i] - r.m) / a.tau);

@@ -180,11 +180,12 @@ __device__ __forceinline__ void wave_fence() {
 }
 
 // Exponentials against a maximum m as one multiply-add: 2^(x c - t) with
-// t = m c - 32, so that what lies up to 2^-158 below the maximum is still a
-// normal number (the hardware's 2^x flushes others).  t's own rounding is no
-// error of the sums, which are taken against t, not m; at_max() is the exact
-// distance m c - t (at most 96, as |m c| stays below 2^31) for what has to be
-// taken against m.  Where a finite m has |m c| >= 2^31 (far()), c is cut to a
+// t = m c - 8, so that what lies up to 2^-134 below the maximum is still a
+// normal number (the hardware's 2^x flushes others; a larger distance would
+// cost the exponents near the maximum their last bits).  t's own rounding is
+// no error of the sums, which are taken against t, not m; at_max() is the
+// exact distance m c - t (at most 72, as |m c| stays below 2^31) for what has
+// to be taken against m.  Where a finite m has |m c| >= 2^31 (far()), c is cut to a
 // power of two, which makes t = m c exact: neighbouring floats lie 128 / c
 // apart there or more, so the result is 1 at m and 0 below it with either.
 // For m = -inf, t is 0 (2^-inf is 0); for +inf the results are NaN.  c lies
@@ -195,7 +196,7 @@ struct Against {
   float c, t;
 };
 __device__ __forceinline__ Against against(float m, float c) {
-  Against r{c, m == kNegInf ? 0.0f : m * c - 32.0f};
+  Against r{c, m == kNegInf ? 0.0f : m * c - 8.0f};
   if (__builtin_expect(far(m, c), 0)) {
     r.c = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, c) & 0xff800000u);
     if (fabsf(m) >= 0x1p60f) r.c = fminf(r.c, 1.0f);
