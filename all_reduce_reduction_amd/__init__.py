@@ -13,6 +13,7 @@ and pass their pointers and the current HIP stream to the library.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import List, Optional, Sequence
 
@@ -145,12 +146,16 @@ CALIBRATION = os.path.join(_HERE, "calib", "mi355x.json")
 
 # ---- the C functions, one to one ------------------------------------------------
 def sim_init(device: int = 0, p_max: int = MAX_RANKS, max_bytes_per_rank: int = 0) -> None:
+    sim_route_work.cache_clear()
+    sim_distill_work.cache_clear()
     _check(lib.sim_init(device, p_max, max_bytes_per_rank), "sim_init")
     if not os.environ.get("SIM_CALIB") and os.path.exists(CALIBRATION):
         sim_model_load(CALIBRATION)
 
 
 def sim_finalize() -> None:
+    sim_route_work.cache_clear()
+    sim_distill_work.cache_clear()
     _check(lib.sim_finalize(), "sim_finalize")
 
 
@@ -248,8 +253,9 @@ def sim_copy_streams(src_ptrs, dst_ptrs, k: int, nbytes: int, workgroups: int = 
                                 stream or None)
 
 
+@functools.lru_cache(maxsize=1024)
 def sim_route_work(tokens: int, experts: int, topk: int, dtype) -> int:
-    """Workspace bytes of sim_route."""
+    """Workspace bytes of sim_route (they follow from these sizes and the device that sim_init chose)."""
     n = ctypes.c_size_t(0)
     _check(lib.sim_route_work(tokens, experts, topk, _code(DTYPES, dtype, "dtype"), ctypes.byref(n)),
            "sim_route_work")
@@ -269,6 +275,7 @@ def sim_route_grad(logits, row_stride, dtype, keep, tokens, experts, topk, norma
                               stream or None)
 
 
+@functools.lru_cache(maxsize=1024)
 def sim_distill_work(rows: int, columns: int, dtype) -> int:
     """Workspace bytes of sim_distill_step (columns: the vocabulary) and sim_distill_parts."""
     n = ctypes.c_size_t(0)
@@ -446,6 +453,29 @@ _raw_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", N
 _TORCH_CODE = {} if torch is None else {torch.float32: 1, torch.float16: 2, torch.bfloat16: 3}
 if torch is not None:
     _F32, _I32, _MASK = (torch.float32,), (torch.int32,), (torch.bool, torch.uint8)
+    _FLOATS = tuple(_TORCH_CODE)
+
+_ENTRIES = ("route", "route_grad", "distill_step", "distill_parts", "distill_join", "distill_grad")
+
+
+def _vec_py(t, what, dtypes, device, *shape):
+    """Pointer of a contiguous device tensor of the given shape and one of the given dtypes (None: None)."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous tensor {shape!r} of one of {dtypes!r} on {device}")
+    return t.data_ptr()
+
+
+if hasattr(_pycall, "bind"):
+    # arguments converted and tensors checked in C: of a small call's 7.3 us on the host, ctypes and the same checks
+    # in Python took about 2
+    for _name in _ENTRIES:
+        _pycall.bind(_name, ctypes.cast(lib["sim_" + _name], ctypes.c_void_p).value)
+    _entry, _vec = _pycall, _pycall.pointer
+else:
+    import types as _types
+    _entry, _vec = _types.SimpleNamespace(**{n: getattr(lib, "sim_" + n) for n in _ENTRIES}), _vec_py
 
 
 def _code_of(t) -> int:
@@ -455,27 +485,17 @@ def _code_of(t) -> int:
     return c
 
 
-def _rows(t, what, cols=None, like=None):
+def _rows(t, what, like=None):
     """(pointer, row stride) of a 2-D device tensor whose rows are contiguous."""
     if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{what} must be a 2-D device tensor")
     n, c = t.shape
     st = t.stride()
-    if c > 1 and st[1] != 1:
+    if st[1] != 1 and c > 1:
         raise ValueError(f"{what}'s rows must be contiguous")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
-        raise ValueError(f"{what} must have the logits' shape and dtype")
+    if like is not None and (t.dtype is not like.dtype or t.shape != like.shape or t.device != like.device):
+        raise ValueError(f"{what} must have the logits' shape, dtype and device")
     return t.data_ptr(), (st[0] if n > 1 else c)
-
-
-def _vec(t, what, shape, dtypes, device):
-    """Pointer of a contiguous device tensor of the given shape and one of the given dtypes (None: None)."""
-    if t is None:
-        return None
-    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{what} must be a contiguous tensor {tuple(shape)} of "
-                         f"{' or '.join(str(d) for d in dtypes)} on {device}")
-    return t.data_ptr()
 
 
 def _on(stream, device):
@@ -508,14 +528,13 @@ def route(logits, topk: int, keep=None, normalize: bool = True, out=None, stream
     if out is None:
         out = (torch.empty((n, topk), dtype=torch.int32, device=dev), torch.empty((n, topk), device=dev),
                torch.empty(e + 1, dtype=torch.int32, device=dev), torch.empty(e, device=dev))
-    nb = ctypes.c_size_t(0)
-    _check(lib.sim_route_work(n, e, topk, dt, ctypes.byref(nb)), "sim_route_work")
-    w, wp = _work(nb.value, dev, stream)
-    _check(lib.sim_route(ptr, ld, dt, _vec(keep, "keep", (n,), _MASK, dev), n, e, topk,
-                         bool(normalize), _vec(out[0], "chosen", (n, topk), _I32, dev),
-                         _vec(out[1], "weights", (n, topk), _F32, dev), _vec(out[2], "counts", (e + 1,), _I32, dev),
-                         _vec(out[3], "prob_sums", (e,), _F32, dev), wp, nb.value, _on(stream, dev)),
-           "sim_route")
+    chosen, weights, counts, sums = out
+    nb = sim_route_work(n, e, topk, dt)
+    w, wp = _work(nb, dev, stream)
+    _check(_entry.route(ptr, ld, dt, _vec(keep, "keep", _MASK, dev, n), n, e, topk, bool(normalize),
+                        _vec(chosen, "chosen", _I32, dev, n, topk), _vec(weights, "weights", _F32, dev, n, topk),
+                        _vec(counts, "counts", _I32, dev, e + 1), _vec(sums, "prob_sums", _F32, dev, e), wp, nb,
+                        _on(stream, dev)), "sim_route")
     return out
 
 
@@ -530,25 +549,23 @@ def route_grad(logits, chosen, dweights=None, counts=None, prob_sums=None, coef:
     topk = chosen.shape[1]
     if out is None:
         out = (torch.empty(1, device=dev), torch.empty((n, e), dtype=logits.dtype, device=dev))
-    dptr, dld = _rows(out[1], "dlogits", like=logits)
-    _check(lib.sim_route_grad(ptr, ld, _code_of(logits),
-                              _vec(keep, "keep", (n,), _MASK, dev), n, e, topk, bool(normalize),
-                              _vec(chosen, "chosen", (n, topk), _I32, dev),
-                              _vec(dweights, "dweights", (n, topk), _F32, dev),
-                              _vec(counts, "counts", (e + 1,), _I32, dev), _vec(prob_sums, "prob_sums", (e,), _F32, dev),
-                              coef, dptr, dld, _vec(out[0], "loss", (1,), _F32, dev), _on(stream, dev)),
-           "sim_route_grad")
+    loss, dlogits = out
+    dptr, dld = _rows(dlogits, "dlogits", like=logits)
+    _check(_entry.route_grad(ptr, ld, _code_of(logits), _vec(keep, "keep", _MASK, dev, n), n, e, topk,
+                             bool(normalize), _vec(chosen, "chosen", _I32, dev, n, topk),
+                             _vec(dweights, "dweights", _F32, dev, n, topk), _vec(counts, "counts", _I32, dev, e + 1),
+                             _vec(prob_sums, "prob_sums", _F32, dev, e), coef, dptr, dld,
+                             _vec(loss, "loss", _F32, dev, 1), _on(stream, dev)), "sim_route_grad")
     return out
 
 
 def _slots(ids, teacher, rows, device):
     """(ids pointer, teacher pointer, its dtype code, topk)"""
-    shape = ids.shape
-    if len(shape) != 2 or shape[0] != rows:
+    if ids.dim() != 2:
         raise ValueError("ids must be [rows, topk]")
-    return (_vec(ids, "ids", shape, _I32, device),
-            _vec(teacher, "teacher", shape, _TORCH_CODE, device),
-            _code_of(teacher), shape[1])
+    k = ids.shape[1]
+    return (_vec(ids, "ids", _I32, device, rows, k), _vec(teacher, "teacher", _FLOATS, device, rows, k),
+            _code_of(teacher), k)
 
 
 def distill_step(logits, ids, teacher, temperature: float = 1.0, row_scale=None, coef: float = 1.0, out=None,
@@ -561,15 +578,14 @@ def distill_step(logits, ids, teacher, temperature: float = 1.0, row_scale=None,
     dev, dt = logits.device, _code_of(logits)
     if out is None:
         out = (torch.empty(n, device=dev), torch.empty((n, v), dtype=logits.dtype, device=dev))
-    dptr, dld = _rows(out[1], "dlogits", like=logits)
+    loss, dlogits = out
+    dptr, dld = _rows(dlogits, "dlogits", like=logits)
     ip, tp, tdt, k = _slots(ids, teacher, n, dev)
-    nb = ctypes.c_size_t(0)
-    _check(lib.sim_distill_work(n, v, dt, ctypes.byref(nb)), "sim_distill_work")
-    w, wp = _work(nb.value, dev, stream)
-    _check(lib.sim_distill_step(ptr, ld, dt, n, v, ip, tp, tdt, k, temperature,
-                                _vec(row_scale, "row_scale", (n,), _F32, dev), coef, dptr, dld,
-                                _vec(out[0], "loss", (n,), _F32, dev), wp, nb.value, _on(stream, dev)),
-           "sim_distill_step")
+    nb = sim_distill_work(n, v, dt)
+    w, wp = _work(nb, dev, stream)
+    _check(_entry.distill_step(ptr, ld, dt, n, v, ip, tp, tdt, k, temperature,
+                               _vec(row_scale, "row_scale", _F32, dev, n), coef, dptr, dld,
+                               _vec(loss, "loss", _F32, dev, n), wp, nb, _on(stream, dev)), "sim_distill_step")
     return out
 
 
@@ -583,29 +599,28 @@ def distill_parts(logits, ids, teacher, temperature: float = 1.0, first: int = 0
     if out is None:
         out = torch.empty((4, n), device=dev)
     ip, tp, tdt, k = _slots(ids, teacher, n, dev)
-    nb = ctypes.c_size_t(0)
-    _check(lib.sim_distill_work(n, c, dt, ctypes.byref(nb)), "sim_distill_work")
-    w, wp = _work(nb.value, dev, stream)
-    _check(lib.sim_distill_parts(ptr, ld, dt, n, c, first, first + c if vocab is None else vocab, ip, tp, tdt, k,
-                                 temperature, _vec(out, "parts", (4, n), _F32, dev), wp, nb.value,
-                                 _on(stream, dev)), "sim_distill_parts")
+    nb = sim_distill_work(n, c, dt)
+    w, wp = _work(nb, dev, stream)
+    _check(_entry.distill_parts(ptr, ld, dt, n, c, first, first + c if vocab is None else vocab, ip, tp, tdt, k,
+                                temperature, _vec(out, "parts", _F32, dev, 4, n), wp, nb, _on(stream, dev)),
+           "sim_distill_parts")
     return out
 
 
 def distill_join(parts, ids, teacher, temperature: float = 1.0, vocab: Optional[int] = None, out=None, stream=None):
     """Loss of all shards' parts [nparts, 4, rows], as all_gather leaves them: (loss fp32 [rows], norm fp32 [2,
-    rows]).  vocab: the whole vocabulary (ids outside it are empty slots; default: none is, but the negative)."""
-    if parts.dim() != 3 or parts.shape[1] != 4:
-        raise ValueError("parts must be [nparts, 4, rows]")
+    rows]).  vocab: the whole vocabulary (an id outside it is an empty slot; default: only a negative one is)."""
+    if parts.dim() != 3 or not parts.is_cuda:
+        raise ValueError("parts must be a device tensor [nparts, 4, rows]")
     p, _, n = parts.shape
     dev = parts.device
     if out is None:
         out = (torch.empty(n, device=dev), torch.empty((2, n), device=dev))
+    loss, norm = out
     ip, tp, tdt, k = _slots(ids, teacher, n, dev)
-    _check(lib.sim_distill_join(_vec(parts, "parts", (p, 4, n), _F32, dev), p, n,
-                                2 ** 31 - 1 if vocab is None else vocab, ip, tp, tdt, k, temperature,
-                                _vec(out[0], "loss", (n,), _F32, dev), _vec(out[1], "norm", (2, n), _F32, dev),
-                                _on(stream, dev)), "sim_distill_join")
+    _check(_entry.distill_join(_vec(parts, "parts", _F32, dev, p, 4, n), p, n, 2 ** 31 - 1 if vocab is None else vocab,
+                               ip, tp, tdt, k, temperature, _vec(loss, "loss", _F32, dev, n),
+                               _vec(norm, "norm", _F32, dev, 2, n), _on(stream, dev)), "sim_distill_join")
     return out
 
 
@@ -620,8 +635,8 @@ def distill_grad(logits, ids, teacher, norm, temperature: float = 1.0, row_scale
         out = torch.empty((n, c), dtype=logits.dtype, device=dev)
     dptr, dld = _rows(out, "dlogits", like=logits)
     ip, tp, tdt, k = _slots(ids, teacher, n, dev)
-    _check(lib.sim_distill_grad(ptr, ld, _code_of(logits), n, c, first,
-                                first + c if vocab is None else vocab, ip, tp, tdt, k, temperature,
-                                _vec(norm, "norm", (2, n), _F32, dev), _vec(row_scale, "row_scale", (n,), _F32, dev),
-                                coef, dptr, dld, _on(stream, dev)), "sim_distill_grad")
+    _check(_entry.distill_grad(ptr, ld, _code_of(logits), n, c, first, first + c if vocab is None else vocab, ip, tp,
+                               tdt, k, temperature, _vec(norm, "norm", _F32, dev, 2, n),
+                               _vec(row_scale, "row_scale", _F32, dev, n), coef, dptr, dld, _on(stream, dev)),
+           "sim_distill_grad")
     return out

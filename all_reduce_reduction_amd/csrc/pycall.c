@@ -1,4 +1,5 @@
-/* pycall.c -- the Python object behind prepare_allreduce().
+/* pycall.c -- the Python object behind prepare_allreduce(), and the direct
+ * calls behind the routing and loss helpers (further down).
  *
  * prepare_allreduce() marshals the arguments of one sim_allreduce call
  * once; calling the object it returns makes that C call again.  Through
@@ -14,6 +15,7 @@
 #include <Python.h>
 #include <stddef.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "simar.h"
 
@@ -110,12 +112,162 @@ static PyTypeObject PreparedCallType = {
     .tp_call = PreparedCall_call,
 };
 
+/* ---- the routing and loss entry points ------------------------------------
+ * bind(name, address) sets an entry point once; the function of that name
+ * then takes the C function's arguments (pointers as integers or None) and
+ * returns its status. */
+#define ENTRY(name) static __typeof__(sim_##name)* name##_fn
+ENTRY(route);
+ENTRY(route_grad);
+ENTRY(distill_step);
+ENTRY(distill_parts);
+ENTRY(distill_join);
+ENTRY(distill_grad);
+
+static void* as_pointer(PyObject* o) { return o == Py_None ? NULL : PyLong_AsVoidPtr(o); }
+static int as_int(PyObject* o) {
+  const long v = PyLong_AsLong(o);
+  if (v != (int)v && !PyErr_Occurred()) PyErr_SetString(PyExc_OverflowError, "argument does not fit an int");
+  return (int)v;
+}
+#define P(i) as_pointer(a[i])
+#define I(i) as_int(a[i])
+#define L(i) ((int64_t)PyLong_AsLongLong(a[i]))
+#define Z(i) ((size_t)PyLong_AsUnsignedLongLong(a[i]))
+#define F(i) ((float)PyFloat_AsDouble(a[i]))
+
+static int ready(const void* fn, Py_ssize_t n, Py_ssize_t want) {
+  if (!fn) PyErr_SetString(PyExc_RuntimeError, "entry point not bound");
+  else if (n != want) PyErr_Format(PyExc_TypeError, "%zd arguments wanted, %zd given", want, n);
+  else return 1;
+  return 0;
+}
+/* The arguments are converted into locals first, so that a failed conversion
+ * is seen before the call. */
+#define ARGS(...) __VA_ARGS__
+#define WRAP(name, count, DECL, CALL)                                                       \
+  static PyObject* py_##name(PyObject* self, PyObject* const* a, Py_ssize_t n) {            \
+    (void)self;                                                                             \
+    if (!ready((const void*)name##_fn, n, count)) return NULL;                              \
+    DECL if (PyErr_Occurred()) return NULL;                                                 \
+    return PyLong_FromLong(name##_fn(CALL));                                                \
+  }
+
+WRAP(route, 15,
+     void* x = P(0); int64_t ld = L(1); int dt = I(2); void* keep = P(3); int64_t tokens = L(4); int experts = I(5);
+     int topk = I(6); int norm = I(7); void* chosen = P(8); void* w = P(9); void* counts = P(10); void* sums = P(11);
+     void* work = P(12); size_t bytes = Z(13); void* s = P(14);
+     , ARGS(x, ld, dt, keep, tokens, experts, topk, norm, chosen, w, counts, sums, work, bytes, s))
+WRAP(route_grad, 17,
+     void* x = P(0); int64_t ld = L(1); int dt = I(2); void* keep = P(3); int64_t tokens = L(4); int experts = I(5);
+     int topk = I(6); int norm = I(7); void* chosen = P(8); void* dw = P(9); void* counts = P(10); void* sums = P(11);
+     float coef = F(12); void* dx = P(13); int64_t dld = L(14); void* loss = P(15); void* s = P(16);
+     , ARGS(x, ld, dt, keep, tokens, experts, topk, norm, chosen, dw, counts, sums, coef, dx, dld, loss, s))
+WRAP(distill_step, 18,
+     void* x = P(0); int64_t ld = L(1); int dt = I(2); int64_t rows = L(3); int64_t vocab = L(4); void* ids = P(5);
+     void* z = P(6); int zdt = I(7); int topk = I(8); float tau = F(9); void* rs = P(10); float coef = F(11);
+     void* dx = P(12); int64_t dld = L(13); void* loss = P(14); void* work = P(15); size_t bytes = Z(16); void* s = P(17);
+     , ARGS(x, ld, dt, rows, vocab, ids, z, zdt, topk, tau, rs, coef, dx, dld, loss, work, bytes, s))
+WRAP(distill_parts, 16,
+     void* x = P(0); int64_t ld = L(1); int dt = I(2); int64_t rows = L(3); int64_t cols = L(4); int64_t first = L(5);
+     int64_t vocab = L(6); void* ids = P(7); void* z = P(8); int zdt = I(9); int topk = I(10); float tau = F(11);
+     void* parts = P(12); void* work = P(13); size_t bytes = Z(14); void* s = P(15);
+     , ARGS(x, ld, dt, rows, cols, first, vocab, ids, z, zdt, topk, tau, parts, work, bytes, s))
+WRAP(distill_join, 12,
+     void* parts = P(0); int nparts = I(1); int64_t rows = L(2); int64_t vocab = L(3); void* ids = P(4); void* z = P(5);
+     int zdt = I(6); int topk = I(7); float tau = F(8); void* loss = P(9); void* norm = P(10); void* s = P(11);
+     , ARGS(parts, nparts, rows, vocab, ids, z, zdt, topk, tau, loss, norm, s))
+WRAP(distill_grad, 18,
+     void* x = P(0); int64_t ld = L(1); int dt = I(2); int64_t rows = L(3); int64_t cols = L(4); int64_t first = L(5);
+     int64_t vocab = L(6); void* ids = P(7); void* z = P(8); int zdt = I(9); int topk = I(10); float tau = F(11);
+     void* norm = P(12); void* rs = P(13); float coef = F(14); void* dx = P(15); int64_t dld = L(16); void* s = P(17);
+     , ARGS(x, ld, dt, rows, cols, first, vocab, ids, z, zdt, topk, tau, norm, rs, coef, dx, dld, s))
+
+static PyObject* py_bind(PyObject* self, PyObject* args) {
+  (void)self;
+  const char* name;
+  unsigned long long at;
+  if (!PyArg_ParseTuple(args, "sK", &name, &at)) return NULL;
+#define SET(entry) \
+  if (!strcmp(name, #entry)) { entry##_fn = (__typeof__(sim_##entry)*)(uintptr_t)at; Py_RETURN_NONE; }
+  SET(route) SET(route_grad) SET(distill_step) SET(distill_parts) SET(distill_join) SET(distill_grad)
+  PyErr_Format(PyExc_ValueError, "no entry point %s", name);
+  return NULL;
+}
+
+/* pointer(tensor, what, dtypes, device, *shape): the data pointer of a
+ * contiguous tensor of that shape, device and one of those dtypes (None for
+ * None). */
+static PyObject *s_dtype, *s_shape, *s_device, *s_contiguous, *s_data_ptr;
+static PyObject* py_pointer(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n < 4 || !PyTuple_Check(a[2])) {
+    PyErr_SetString(PyExc_TypeError, "pointer(tensor, what, dtypes, device, *shape)");
+    return NULL;
+  }
+  if (a[0] == Py_None) Py_RETURN_NONE;
+  int ok = 0;
+  PyObject* v = PyObject_GetAttr(a[0], s_dtype);
+  if (!v) return NULL;
+  for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(a[2]); i++) ok = ok || PyTuple_GET_ITEM(a[2], i) == v;
+  Py_DECREF(v);
+  if (ok) {
+    if (!(v = PyObject_GetAttr(a[0], s_shape))) return NULL;
+    ok = PyTuple_Check(v) && PyTuple_GET_SIZE(v) == n - 4;
+    for (Py_ssize_t i = 4; ok && i < n; i++)
+      ok = PyLong_AsLongLong(PyTuple_GET_ITEM(v, i - 4)) == PyLong_AsLongLong(a[i]);
+    Py_DECREF(v);
+    if (PyErr_Occurred()) return NULL;
+  }
+  if (ok) {
+    if (!(v = PyObject_GetAttr(a[0], s_device))) return NULL;
+    ok = PyObject_RichCompareBool(v, a[3], Py_EQ);
+    Py_DECREF(v);
+    if (ok < 0) return NULL;
+  }
+  if (ok) {
+    if (!(v = PyObject_CallMethodNoArgs(a[0], s_contiguous))) return NULL;
+    ok = PyObject_IsTrue(v);
+    Py_DECREF(v);
+    if (ok < 0) return NULL;
+  }
+  if (ok) return PyObject_CallMethodNoArgs(a[0], s_data_ptr);
+  PyObject* shape = PyTuple_New(n - 4);
+  if (!shape) return NULL;
+  for (Py_ssize_t i = 4; i < n; i++) {
+    Py_INCREF(a[i]);
+    PyTuple_SET_ITEM(shape, i - 4, a[i]);
+  }
+  PyErr_Format(PyExc_ValueError, "%U must be a contiguous tensor %R of one of %R on %S", a[1], shape, a[2], a[3]);
+  Py_DECREF(shape);
+  return NULL;
+}
+
+#define METHOD(name, f, doc) {name, (PyCFunction)(void (*)(void))f, METH_FASTCALL, doc}
+static PyMethodDef pycall_methods[] = {
+    {"bind", py_bind, METH_VARARGS, "bind(name, address): set an entry point"},
+    METHOD("pointer", py_pointer, "pointer(tensor, what, dtypes, device, *shape): the checked data pointer"),
+    METHOD("route", py_route, "sim_route"),
+    METHOD("route_grad", py_route_grad, "sim_route_grad"),
+    METHOD("distill_step", py_distill_step, "sim_distill_step"),
+    METHOD("distill_parts", py_distill_parts, "sim_distill_parts"),
+    METHOD("distill_join", py_distill_join, "sim_distill_join"),
+    METHOD("distill_grad", py_distill_grad, "sim_distill_grad"),
+    {NULL, NULL, 0, NULL},
+};
+
 static struct PyModuleDef pycall_module = {
-    PyModuleDef_HEAD_INIT, "_pycall", "Prepared C-ABI calls for the Python binding.", -1, NULL,
+    PyModuleDef_HEAD_INIT, "_pycall", "Prepared C-ABI calls for the Python binding.", -1, pycall_methods,
 };
 
 PyMODINIT_FUNC PyInit__pycall(void) {
   if (PyType_Ready(&PreparedCallType) < 0) return NULL;
+  s_dtype = PyUnicode_InternFromString("dtype");
+  s_shape = PyUnicode_InternFromString("shape");
+  s_device = PyUnicode_InternFromString("device");
+  s_contiguous = PyUnicode_InternFromString("is_contiguous");
+  s_data_ptr = PyUnicode_InternFromString("data_ptr");
+  if (!s_dtype || !s_shape || !s_device || !s_contiguous || !s_data_ptr) return NULL;
   PyObject* m = PyModule_Create(&pycall_module);
   if (!m) return NULL;
   Py_INCREF(&PreparedCallType);
