@@ -23,8 +23,30 @@ __device__ __forceinline__ float teacher_at(const void* p, int dtype, int64_t i)
   return dtype == SIM_FP16 ? load_elem<SIM_FP16>(p, i) : load_elem<SIM_BF16>(p, i);
 }
 
+// The slots' ids and logits on their way from memory: a wave asks for them
+// before it asks for anything else and works on them once the rest is in
+// flight.
+struct SlotLoads {
+  int id[kSlotsPerLane];
+  float z[kSlotsPerLane];
+};
+__device__ __forceinline__ SlotLoads ask_slots(const DistillArgs& a, int64_t row, int lane) {
+  SlotLoads s;
+#pragma unroll
+  for (int i = 0; i < kSlotsPerLane; i++) {
+    if (64 * i >= a.topk) break;
+    const int k = lane + 64 * i;
+    s.id[i] = -1;
+    s.z[i] = 0.0f;
+    if (k < a.topk) {
+      s.id[i] = a.ids[row * a.topk + k];
+      s.z[i] = teacher_at(a.teacher, a.teacher_dtype, row * a.topk + k);
+    }
+  }
+  return s;
+}
 // one whole wave calls this
-__device__ __forceinline__ Slots load_slots(const DistillArgs& a, int64_t row, int lane) {
+__device__ __forceinline__ Slots make_slots(const DistillArgs& a, const SlotLoads& in) {
   Slots s;
   float z[kSlotsPerLane];
   float top = kNegInf;
@@ -32,17 +54,9 @@ __device__ __forceinline__ Slots load_slots(const DistillArgs& a, int64_t row, i
 #pragma unroll
   for (int i = 0; i < kSlotsPerLane; i++) {
     if (64 * i >= a.topk) break;
-    const int k = lane + 64 * i;
-    s.id[i] = -1;
-    z[i] = kNegInf;
-    if (k < a.topk) {
-      const int id = a.ids[row * a.topk + k];
-      const float zk = teacher_at(a.teacher, a.teacher_dtype, row * a.topk + k);  // in flight with the id
-      if (id >= 0 && id < a.vocab) {
-        s.id[i] = id;
-        z[i] = zk;
-      }
-    }
+    const bool ok = in.id[i] >= 0 && in.id[i] < a.vocab;
+    s.id[i] = ok ? in.id[i] : -1;
+    z[i] = ok ? in.z[i] : kNegInf;
     some = some || !(z[i] == kNegInf);
     top = fmaxf(top, z[i]);
   }

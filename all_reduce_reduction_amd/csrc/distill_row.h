@@ -8,8 +8,8 @@
 // them hold a row of 256 KiB (131,072 16-bit logits).  What a row has beyond
 // NT * R vectors is read a second time for its gradient.
 //
-// While the row's loads are in flight, wave 0 reads the slots and their own
-// logits.
+// Wave 0 asks for the slots before it asks for its share of the row, and works
+// them out and reads their own logits while the row is in flight.
 #pragma once
 
 #include "distill_device.h"
@@ -17,41 +17,58 @@
 
 namespace simar {
 
-// of the R vectors of a thread, the last GUARD may lie past the row's end
+// of the R vectors of a thread, the last GUARD may lie past the row's end; a
+// row is at least one vector long
 template <int DT, int NT, int R, int GUARD, bool STREAM>
 __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
   constexpr int V = epv<DT>(), W = NT / 64, PAIR = R % 2 ? 1 : 2;
+  static_assert((R - GUARD) % PAIR == 0, "a pair lies wholly before the guarded vectors or among them");
     __shared__ SlotLists<NT> slots;
   __shared__ float m_s[W], s_s[W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x;
+  const uint32_t cols = (uint32_t)a.cols;
   const void* x = row_at(a.x, row, a.stride, Ty<DT>::E);
   void* dx = row_at(a.dx, row, a.dstride, Ty<DT>::E);
   const float c = kLog2e / a.tau;
   const float up = (a.row_scale ? a.row_scale[row] : 1.0f) * (a.coef / a.tau);
+  SlotLoads asked;
+  if (wave == 0) asked = ask_slots(a, row, lane);
   u32x4 v[R];
 #pragma unroll
   for (int i = 0; i < R; i++) {
     if (i < R - GUARD) v[i] = ld_row_lane<DT, STREAM>(x, i * NT * V, tid * V);
-    else v[i] = ld_guarded<DT>(x, (int64_t)(i * NT + tid) * V, a.cols);
+    else v[i] = Tail<DT>(i * NT * V + tid * V, cols).load(x);
   }
   slots.head[tid] = -1;
   Slots sl;
   if (wave == 0) {
-    sl = load_slots(a, row, lane);
+    sl = make_slots(a, asked);
     gather_slots<DT>(a, slots, sl, x, 0, a.cols, lane);
   }
   Scan scan;
 #pragma unroll
   for (int i = 0; i < R; i += PAIR) {
-    float f[PAIR * V];
+    if (i < R - GUARD) {
+      float f[PAIR * V];
 #pragma unroll
-    for (int j = 0; j < PAIR; j++) unpack<DT>(v[i + j], f + j * V);
-    scan.add(f, c);
+      for (int j = 0; j < PAIR; j++) unpack<DT>(v[i + j], f + j * V);
+      scan.add(f, c);
+    } else {
+#pragma unroll
+      for (int j = 0; j < PAIR; j++) {
+        float f[V];
+        unpack<DT>(v[i + j], f);
+        Tail<DT>((i + j) * NT * V + lane_offset(tid * V), cols).mask(f);
+        scan.add(f, c);
+      }
+    }
   }
-  for (int64_t col = (int64_t)(R * NT + tid) * V; col < a.cols; col += NT * V) {
+  for (uint32_t col = (uint32_t)(R * NT + tid) * V; col < cols; col += NT * V) {
+    const Tail<DT> t(col, cols);
     float f[V];
-    load_cols<DT>(x, col, a.cols, f);
+    unpack<DT>(t.load(x), f);
+    t.mask(f);
     scan.add(f, c);
   }
   Running r = wave_running(scan.done(c), c);
@@ -66,9 +83,11 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
   if (__builtin_expect(far(r.m, c), 0)) {
     float n = 0.0f;
 #pragma unroll 1
-    for (int64_t col = (int64_t)tid * V; col < a.cols; col += NT * V) {
+    for (uint32_t col = tid * V; col < cols; col += NT * V) {
+      const Tail<DT> t(col, cols);
       float f[V];
-      load_cols<DT>(x, col, a.cols, f);
+      unpack<DT>(t.load(x), f);
+      t.mask(f);
       n += count_of(f, r.m);
     }
     n = wave_sum(n);
@@ -98,7 +117,7 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
   if (!live) {
     // (0 * p would keep the NaN of a row that does not count)
     const float f[V] = {};
-    for (int64_t col = (int64_t)tid * V; col < a.cols; col += NT * V) st_guarded<DT>(dx, col, a.cols, f);
+    for (uint32_t col = tid * V; col < cols; col += NT * V) Tail<DT>(col, cols).store(dx, f);
     return;
   }
 #pragma unroll
@@ -111,14 +130,15 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
 #pragma unroll
     for (int j = 0; j < V; j++) f[j] = exp_against(f[j], top) * k2;
     if (i < R - GUARD) st_row_lane<DT, STREAM>(dx, i * NT * V, tid * V, pack_rounded<DT>(f));
-    else st_guarded<DT>(dx, (int64_t)(i * NT + tid) * V, a.cols, f);
+    else Tail<DT>(i * NT * V + lane_offset(tid * V), cols).store(dx, f);
   }
-  for (int64_t col = (int64_t)(R * NT + tid) * V; col < a.cols; col += NT * V) {
+  for (uint32_t col = (uint32_t)(R * NT + tid) * V; col < cols; col += NT * V) {
+    const Tail<DT> t(col, cols);
     float f[V];
-    load_cols<DT>(x, col, a.cols, f);
+    unpack<DT>(t.load(x), f);
 #pragma unroll
     for (int j = 0; j < V; j++) f[j] = exp_against(f[j], top) * k2;
-    st_guarded<DT>(dx, col, a.cols, f);
+    t.store(dx, f);
   }
   write_slots<DT>(a, slots, dx, up, tid);
 }
@@ -140,7 +160,7 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
 //     workgroups 444, streaming in them 494).
 template <int DT, int NT, int R, bool STREAM>
 hipError_t launch_row_as(const DistillArgs& a, hipStream_t s) {
-  constexpr int G = R < 4 ? 1 : 2;
+  constexpr int G = R % 2 ? 1 : 2;
   return launch<k_distill_row<DT, NT, R, G, STREAM>>(dim3((unsigned)a.rows), dim3(NT), s, a);
 }
 // the smallest R of LEAST, ..., MOST that holds the row (MOST where none does)

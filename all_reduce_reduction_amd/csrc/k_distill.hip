@@ -10,63 +10,107 @@
 // part: its own maximum m, its sum s against m, the slots' mass a in it and
 // d = sum q (x - m) / tau over them; parts join by rebasing to the largest m,
 // in the order of the columns.  All of it in fp32; a gradient is rounded once.
+#include <type_traits>
+
 #include "distill_device.h"
 #include "launch.h"
 
 namespace simar {
 namespace {
 
-// A workgroup's columns come in chunks of kHeld vectors per thread, whose loads
-// are all in flight together.
+// A workgroup's columns [lo, hi) of a row come in chunks of kHeld vectors per
+// thread, whose loads are all in flight together: whole chunks (WHOLE), then
+// one that ends at hi.  There each vector is the row's last where its own
+// would reach past the row (see Tail), so that no load waits for a branch.
+// TINY: rows shorter than a vector, element by element.
 constexpr int kHeld = 8;
+template <int DT> constexpr uint32_t chunk_cols() { return kHeld * kBlock * epv<DT>(); }
+struct Columns {
+  uint32_t lo, hi, cols;
+};
+__device__ __forceinline__ Columns columns_of(const DistillArgs& a, int64_t split) {
+  const int64_t lo = min(a.cols, split * a.span), hi = min(a.cols, lo + a.span);
+  return {(uint32_t)lo, (uint32_t)hi, (uint32_t)a.cols};
+}
+// (a thread's place is worked out at each use: kept for eight vectors, it
+// takes 40 registers)
 template <int DT>
-__device__ __forceinline__ void load_chunk(const void* x, int64_t col, int64_t hi, int tid, u32x4 (&v)[kHeld]) {
+__device__ __forceinline__ Tail<DT> tail(uint32_t col, int i, int tid, const Columns& r) {
   constexpr int V = epv<DT>();
-  const bool whole = col + kHeld * kBlock * V <= hi;
+  return Tail<DT>(col + i * kBlock * V + lane_offset(tid * V), r.hi, r.cols);
+}
+template <int DT, bool WHOLE, bool TINY>
+__device__ __forceinline__ void load_chunk(const void* x, uint32_t col, int tid, const Columns& r,
+                                           u32x4 (&v)[kHeld]) {
+  constexpr int V = epv<DT>();
 #pragma unroll
   for (int i = 0; i < kHeld; i++) {
-    if (whole) v[i] = ld_row_lane<DT, true>(x, col + i * kBlock * V, tid * V);
-    else if (col + i * kBlock * V < hi) v[i] = ld_guarded<DT>(x, col + (i * kBlock + tid) * V, hi);
+    if constexpr (TINY) v[i] = ld_guarded<DT>(x, (i * kBlock + tid) * V, r.cols);
+    else if constexpr (WHOLE) v[i] = ld_row_lane<DT, true>(x, col + i * kBlock * V, tid * V);
+    else v[i] = tail<DT>(col, i, tid, r).load(x);
   }
 }
+// All chunks: load, `first` behind the first loads, use(v, col, whole).
+template <int DT, bool TINY, class First, class Use>
+__device__ __forceinline__ void each_chunk(const void* x, int tid, const Columns& r, First first, Use use) {
+  u32x4 v[kHeld];
+  uint32_t col = r.lo;
+  if (!TINY && col + chunk_cols<DT>() <= r.hi) {
+    load_chunk<DT, true, false>(x, col, tid, r, v);
+    first();
+    use(v, col, std::true_type());
+#pragma unroll 1
+    for (col += chunk_cols<DT>(); col + chunk_cols<DT>() <= r.hi; col += chunk_cols<DT>()) {
+      load_chunk<DT, true, false>(x, col, tid, r, v);
+      use(v, col, std::true_type());
+    }
+    if (col >= r.hi) return;
+    load_chunk<DT, false, TINY>(x, col, tid, r, v);
+  } else {
+    load_chunk<DT, false, TINY>(x, col, tid, r, v);
+    first();
+  }
+  use(v, col, std::false_type());
+}
 
-template <int DT>
+template <int DT, bool TINY>
 __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
   constexpr int V = epv<DT>(), W = kBlock / 64;
   __shared__ float m_s[W], s_s[W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
-  const int64_t lo = split * a.span, hi = min(a.cols, lo + a.span);
+  const Columns range = columns_of(a, split);
   const void* x = row_at(a.x, row, a.stride, Ty<DT>::E);
   const float c = kLog2e / a.tau;
-  u32x4 v[kHeld];
-  load_chunk<DT>(x, lo, hi, tid, v);
+  SlotLoads asked;
+  if (wave == 0) asked = ask_slots(a, row, lane);
   Slots sl;
   float at[kSlotsPerLane];
-  if (wave == 0) {
-    sl = load_slots(a, row, lane);
-#pragma unroll
-    for (int i = 0; i < kSlotsPerLane; i++) {
-      if (64 * i >= a.topk) break;
-      const int64_t col = (int64_t)sl.id[i] - a.first;
-      const bool here = sl.id[i] >= 0 && col >= lo && col < hi;
-      at[i] = here ? load_elem<DT>(x, col) : 0.0f;
-      if (!here) sl.q[i] = 0.0f;
-    }
-  }
   Scan scan;
-  for (int64_t col = lo;;) {
+  each_chunk<DT, TINY>(
+      x, tid, range,
+      [&]() __attribute__((always_inline)) {
+        if (wave != 0) return;
+        sl = make_slots(a, asked);
 #pragma unroll
-    for (int i = 0; i < kHeld; i++) {
-      if (col + i * kBlock * V >= hi) continue;
-      float f[V];
-      unpack<DT>(v[i], f);
-      scan.add(f, c);
-    }
-    col += kHeld * kBlock * V;
-    if (col >= hi) break;
-    load_chunk<DT>(x, col, hi, tid, v);
-  }
+        for (int i = 0; i < kSlotsPerLane; i++) {
+          if (64 * i >= a.topk) break;
+          const int64_t col = (int64_t)sl.id[i] - a.first;
+          const bool here = sl.id[i] >= 0 && col >= range.lo && col < range.hi;
+          at[i] = here ? load_elem<DT>(x, col) : 0.0f;
+          if (!here) sl.q[i] = 0.0f;
+        }
+      },
+      [&](u32x4(&v)[kHeld], uint32_t col, auto whole) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < kHeld; i++) {
+          if (!whole() && col + i * kBlock * V >= range.hi) break;
+          float f[V];
+          unpack<DT>(v[i], f);
+          if (!whole() && !TINY) tail<DT>(col, i, tid, range).mask(f);
+          scan.add(f, c);
+        }
+      });
   Running r = wave_running(scan.done(c), c);
   if (lane == 0) {
     m_s[wave] = r.m;
@@ -77,15 +121,15 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
   r.s = lane < W ? s_s[lane] : 0.0f;
   r = wave_running(r, c);
   if (__builtin_expect(far(r.m, c), 0)) {
-    float n = 0.0f;
-    for (int64_t col = lo + (int64_t)tid * V; col < hi; col += kBlock * V) {
+    float top = 0.0f;
+    for (int64_t col = range.lo + tid * V; col < range.hi; col += kBlock * V) {
       float f[V];
-      load_cols<DT>(x, col, hi, f);
-      n += count_of(f, r.m);
+      load_cols<DT>(x, col, range.hi, f);
+      top += count_of(f, r.m);
     }
-    n = wave_sum(n);
+    top = wave_sum(top);
     __syncthreads();
-    if (lane == 0) s_s[wave] = n;
+    if (lane == 0) s_s[wave] = top;
     __syncthreads();
     r.s += wave_sum(lane < W ? s_s[lane] : 0.0f);
   }
@@ -114,7 +158,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_join(DistillArgs a, float* l
   const int64_t row = (int64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
   if (row >= a.rows) return;
   const int lane = threadIdx.x & 63;
-  const Slots s = load_slots(a, row, lane);
+  const Slots s = make_slots(a, ask_slots(a, row, lane));
   const Part t = join_parts(a.parts, a.splits, a.rows, row, a.tau, lane);
   if (lane == 0) {
     loss[row] = loss_of(s, t);
@@ -137,19 +181,19 @@ __global__ void __launch_bounds__(kBlock) k_distill_merge(DistillArgs a, float* 
 }
 
 // The gradient of a run of columns, from the row's joined parts or its norm.
-template <int DT>
+template <int DT, bool TINY>
 __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
   constexpr int V = epv<DT>();
   __shared__ SlotLists<kBlock> slots;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
-  const int64_t lo = split * a.span, hi = min(a.cols, lo + a.span);
+  const Columns range = columns_of(a, split);
   const void* x = row_at(a.x, row, a.stride, Ty<DT>::E);
   void* dx = row_at(a.dx, row, a.dstride, Ty<DT>::E);
   const float c = kLog2e / a.tau;
   const float up = (a.row_scale ? a.row_scale[row] : 1.0f) * (a.coef / a.tau);
-  u32x4 v[kHeld];
-  load_chunk<DT>(x, lo, hi, tid, v);
+  SlotLoads asked;
+  if (wave == 0) asked = ask_slots(a, row, lane);
   slots.head[tid] = -1;
   Part t{};
   if (a.norm) {
@@ -160,49 +204,44 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
   }
   const Against top = against(t.m, c);
   const float sum = t.s * exp2_hw(at_max(t.m, top));  // against top.t
-  __syncthreads();
-  if (wave == 0) {
-    const Slots sl = load_slots(a, row, lane);
-    gather_slots<DT>(a, slots, sl, x, lo, hi, lane);
-    wave_fence();
-    if (lane == 0 && a.loss && split == 0) a.loss[row] = loss_of(sl, t);
-    hang_slots<DT>(a, slots, sl, lo, hi, top, sum, lane);
-  }
-  __syncthreads();
-  const bool live = slots.live;
-  if (!live) {
-    // (0 * p would keep the NaN of a row that does not count)
-    const float f[V] = {};
-    for (int64_t col = lo + (int64_t)tid * V; col < hi; col += kBlock * V) st_guarded<DT>(dx, col, hi, f);
-    return;
-  }
   const float k2 = up / sum;
-  for (int64_t col = lo;;) {
-    const bool whole = col + kHeld * kBlock * V <= hi;
+  bool live = true;
+  each_chunk<DT, TINY>(
+      x, tid, range,
+      [&]() __attribute__((always_inline)) {
+        __syncthreads();
+        if (wave == 0) {
+          const Slots sl = make_slots(a, asked);
+          gather_slots<DT>(a, slots, sl, x, range.lo, range.hi, lane);
+          wave_fence();
+          if (lane == 0 && a.loss && split == 0) a.loss[row] = loss_of(sl, t);
+          hang_slots<DT>(a, slots, sl, range.lo, range.hi, top, sum, lane);
+        }
+        __syncthreads();
+        live = slots.live;
+      },
+      [&](u32x4(&v)[kHeld], uint32_t col, auto whole) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < kHeld; i++) {
-      if (col + i * kBlock * V >= hi) continue;
-      float f[V];
-      unpack<DT>(v[i], f);
+        for (int i = 0; i < kHeld; i++) {
+          if (!whole() && col + i * kBlock * V >= range.hi) break;
+          float f[V];
+          unpack<DT>(v[i], f);
+          // (0 * p would keep the NaN of a row that does not count)
 #pragma unroll
-      for (int j = 0; j < V; j++) f[j] = exp_against(f[j], top) * k2;
-      if (whole) st_row_lane<DT, true>(dx, col + i * kBlock * V, tid * V, pack_rounded<DT>(f));
-      else st_guarded<DT>(dx, col + (i * kBlock + tid) * V, hi, f);
-    }
-    col += kHeld * kBlock * V;
-    if (col >= hi) break;
-    load_chunk<DT>(x, col, hi, tid, v);
-  }
+          for (int j = 0; j < V; j++) f[j] = live ? exp_against(f[j], top) * k2 : 0.0f;
+          if (whole()) st_row_lane<DT, true>(dx, col + i * kBlock * V, tid * V, pack_rounded<DT>(f));
+          else if (!TINY) tail<DT>(col, i, tid, range).store(dx, f);
+          else st_guarded<DT>(dx, (i * kBlock + tid) * V, range.cols, f);
+        }
+      });
   write_slots<DT>(a, slots, dx, up, tid);
 }
 
 }  // namespace
 
 bool distill_whole_rows(int64_t rows, int64_t cols, int dtype) {
-#ifdef FORCE_WHOLE
-  return FORCE_WHOLE;
-#endif
   const int v = dtype == SIM_FP32 ? 4 : 8;
+  if (cols < v) return false;
   return (cols + v - 1) / v <= 16 * 1024 || rows >= library_cus() / 2;
 }
 // Workgroups per row: enough for two per compute unit, each with at least
@@ -217,11 +256,11 @@ int64_t distill_span(int64_t cols, int splits) {
   return (v + 7) / 8 * 8;
 }
 
-#define BY_DTYPE(K, ...)                                          \
-  switch (dtype) {                                                \
-    case SIM_FP32: return launch<K<SIM_FP32>>(__VA_ARGS__);       \
-    case SIM_FP16: return launch<K<SIM_FP16>>(__VA_ARGS__);       \
-    default: return launch<K<SIM_BF16>>(__VA_ARGS__);             \
+#define BY_DTYPE(K, ...)                                                                              \
+  switch (dtype) {                                                                                    \
+    case SIM_FP32: return a.cols < 4 ? launch<K<SIM_FP32, true>>(__VA_ARGS__) : launch<K<SIM_FP32, false>>(__VA_ARGS__); \
+    case SIM_FP16: return a.cols < 8 ? launch<K<SIM_FP16, true>>(__VA_ARGS__) : launch<K<SIM_FP16, false>>(__VA_ARGS__); \
+    default: return a.cols < 8 ? launch<K<SIM_BF16, true>>(__VA_ARGS__) : launch<K<SIM_BF16, false>>(__VA_ARGS__);       \
   }
 
 hipError_t launch_distill_stats(const DistillArgs& a, int dtype, hipStream_t s) {

@@ -39,10 +39,41 @@ struct Gate {
     if (experts == kAll) {
 #pragma unroll
       for (int j = 0; j < NV; j++) v[j] = ld_row<DT>(row, col(j, l));
+    } else if (experts >= V) {
+      // the row's last vector where a lane's own would reach past the end, its
+      // elements moved to their places and the rest set to -inf: no branch, so
+      // all loads are in flight together
+#pragma unroll
+      for (int j = 0; j < NV; j++) v[j] = Tail<DT>(col(j, l), experts).load(row);
+#pragma unroll
+      for (int j = 0; j < NV; j++) move_down(v[j], Tail<DT>(col(j, l), experts).skip);
     } else {
 #pragma unroll
       for (int j = 0; j < NV; j++) v[j] = ld_guarded<DT>(row, col(j, l), experts);
     }
+  }
+  // element i becomes element i + skip, -inf past the last
+  static __device__ __forceinline__ void move_down(u32x4& w, int skip) {
+    constexpr uint32_t n = neg_inf_bits<DT>();
+    const int words = skip * Ty<DT>::E / 4;
+    u32x4 r = w;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      uint32_t x = n;
+#pragma unroll
+      for (int k = i; k < 4; k++) x = words == k - i ? w[k] : x;
+      r[i] = x;
+    }
+    if constexpr (Ty<DT>::E == 2) {
+      // an odd number of halves: one more half down
+      const u32x4 q = r;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const uint32_t above = i < 3 ? q[i + 1] : n;
+        r[i] = skip & 1 ? q[i] >> 16 | above << 16 : q[i];
+      }
+    }
+    w = r;
   }
   __device__ __forceinline__ void blank() {
     constexpr uint32_t n = neg_inf_bits<DT>();

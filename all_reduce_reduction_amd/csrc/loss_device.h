@@ -113,6 +113,37 @@ __device__ __forceinline__ void st_guarded(void* row, int64_t col, int64_t cols,
   }
 }
 
+// The vector at column `col` of a row of `cols` >= V columns, without a branch:
+// past cols - V it is the row's last vector instead, which other columns'
+// threads have too.  The first `skip` elements are not this thread's; none is
+// from column `hi` on.
+template <int DT>
+struct Tail {
+  uint32_t at;  // (a row has fewer than 2^31 columns)
+  int skip;
+  __device__ __forceinline__ Tail(uint32_t col, uint32_t hi, uint32_t cols) {
+    constexpr uint32_t V = epv<DT>();
+    at = col < cols - V ? col : cols - V;
+    skip = (int)(col < hi ? col - at : V);
+  }
+  __device__ __forceinline__ Tail(uint32_t col, uint32_t cols) : Tail(col, cols, cols) {}
+  __device__ __forceinline__ u32x4 load(const void* row) const { return ld_row<DT>(row, at); }
+  // the others' elements as -inf
+  __device__ __forceinline__ void mask(float (&x)[epv<DT>()]) const {
+#pragma unroll
+    for (int i = 0; i < epv<DT>(); i++) x[i] = i >= skip ? x[i] : kNegInf;
+  }
+  __device__ __forceinline__ void store(void* row, const float (&x)[epv<DT>()]) const {
+    if (skip == 0) {
+      st_row<DT>(row, at, pack_rounded<DT>(x));
+    } else {
+#pragma unroll
+      for (int i = 0; i < epv<DT>(); i++)
+        if (i >= skip) store_elem<DT>(row, (int64_t)at + i, x[i]);
+    }
+  }
+};
+
 // 2^x (v_exp_f32: 1 ulp; results below the normal range are flushed, far
 // under what a sum that holds 1 can see)
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
