@@ -508,13 +508,20 @@ def _on(stream, device):
     return torch.cuda.current_stream(device).cuda_stream or None
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor for the call's stream: memory the allocator hands out for one stream may still be in use there, so
+    it is taken from the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _work(nbytes, device, stream):
-    """A call's scratch: (tensor, pointer); kept from reuse by other streams until the call's work is done."""
+    """A call's scratch: (tensor, pointer)."""
     if nbytes == 0:
         return None, None
-    w = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        w.record_stream(stream)
+    w = _empty(nbytes, torch.uint8, device, stream)
     return w, w.data_ptr()
 
 
@@ -526,8 +533,8 @@ def route(logits, topk: int, keep=None, normalize: bool = True, out=None, stream
     n, e = logits.shape
     dev, dt = logits.device, _code_of(logits)
     if out is None:
-        out = (torch.empty((n, topk), dtype=torch.int32, device=dev), torch.empty((n, topk), device=dev),
-               torch.empty(e + 1, dtype=torch.int32, device=dev), torch.empty(e, device=dev))
+        out = (_empty((n, topk), torch.int32, dev, stream), _empty((n, topk), torch.float32, dev, stream),
+               _empty(e + 1, torch.int32, dev, stream), _empty(e, torch.float32, dev, stream))
     chosen, weights, counts, sums = out
     nb = sim_route_work(n, e, topk, dt)
     w, wp = _work(nb, dev, stream)
@@ -548,7 +555,7 @@ def route_grad(logits, chosen, dweights=None, counts=None, prob_sums=None, coef:
     dev = logits.device
     topk = chosen.shape[1]
     if out is None:
-        out = (torch.empty(1, device=dev), torch.empty((n, e), dtype=logits.dtype, device=dev))
+        out = (_empty(1, torch.float32, dev, stream), _empty((n, e), logits.dtype, dev, stream))
     loss, dlogits = out
     dptr, dld = _rows(dlogits, "dlogits", like=logits)
     _check(_entry.route_grad(ptr, ld, _code_of(logits), _vec(keep, "keep", _MASK, dev, n), n, e, topk,
@@ -577,7 +584,7 @@ def distill_step(logits, ids, teacher, temperature: float = 1.0, row_scale=None,
     n, v = logits.shape
     dev, dt = logits.device, _code_of(logits)
     if out is None:
-        out = (torch.empty(n, device=dev), torch.empty((n, v), dtype=logits.dtype, device=dev))
+        out = (_empty(n, torch.float32, dev, stream), _empty((n, v), logits.dtype, dev, stream))
     loss, dlogits = out
     dptr, dld = _rows(dlogits, "dlogits", like=logits)
     ip, tp, tdt, k = _slots(ids, teacher, n, dev)
@@ -597,7 +604,7 @@ def distill_parts(logits, ids, teacher, temperature: float = 1.0, first: int = 0
     n, c = logits.shape
     dev, dt = logits.device, _code_of(logits)
     if out is None:
-        out = torch.empty((4, n), device=dev)
+        out = _empty((4, n), torch.float32, dev, stream)
     ip, tp, tdt, k = _slots(ids, teacher, n, dev)
     nb = sim_distill_work(n, c, dt)
     w, wp = _work(nb, dev, stream)
@@ -615,7 +622,7 @@ def distill_join(parts, ids, teacher, temperature: float = 1.0, vocab: Optional[
     p, _, n = parts.shape
     dev = parts.device
     if out is None:
-        out = (torch.empty(n, device=dev), torch.empty((2, n), device=dev))
+        out = (_empty(n, torch.float32, dev, stream), _empty((2, n), torch.float32, dev, stream))
     loss, norm = out
     ip, tp, tdt, k = _slots(ids, teacher, n, dev)
     _check(_entry.distill_join(_vec(parts, "parts", _F32, dev, p, 4, n), p, n, 2 ** 31 - 1 if vocab is None else vocab,
@@ -632,7 +639,7 @@ def distill_grad(logits, ids, teacher, norm, temperature: float = 1.0, row_scale
     n, c = logits.shape
     dev = logits.device
     if out is None:
-        out = torch.empty((n, c), dtype=logits.dtype, device=dev)
+        out = _empty((n, c), logits.dtype, dev, stream)
     dptr, dld = _rows(out, "dlogits", like=logits)
     ip, tp, tdt, k = _slots(ids, teacher, n, dev)
     _check(_entry.distill_grad(ptr, ld, _code_of(logits), n, c, first, first + c if vocab is None else vocab, ip, tp,

@@ -25,12 +25,12 @@ __device__ __forceinline__ float teacher_at(const void* p, int dtype, int64_t i)
 
 // The slots' ids and logits on their way from memory: a wave asks for them
 // before it asks for anything else and works on them once the rest is in
-// flight.
+// flight.  `all`: the logits too, not only the ids.
 struct SlotLoads {
   int id[kSlotsPerLane];
   float z[kSlotsPerLane];
 };
-__device__ __forceinline__ SlotLoads ask_slots(const DistillArgs& a, int64_t row, int lane) {
+__device__ __forceinline__ SlotLoads ask_slots(const DistillArgs& a, int64_t row, int lane, bool all) {
   SlotLoads s;
 #pragma unroll
   for (int i = 0; i < kSlotsPerLane; i++) {
@@ -40,10 +40,21 @@ __device__ __forceinline__ SlotLoads ask_slots(const DistillArgs& a, int64_t row
     s.z[i] = 0.0f;
     if (k < a.topk) {
       s.id[i] = a.ids[row * a.topk + k];
-      s.z[i] = teacher_at(a.teacher, a.teacher_dtype, row * a.topk + k);
+      if (all) s.z[i] = teacher_at(a.teacher, a.teacher_dtype, row * a.topk + k);
     }
   }
   return s;
+}
+// Whether the row has a slot at all: a row without one (a prompt's, padding)
+// need not be read.  One whole wave calls this.
+__device__ __forceinline__ bool has_slots(const DistillArgs& a, const SlotLoads& in) {
+  bool some = false;
+#pragma unroll
+  for (int i = 0; i < kSlotsPerLane; i++) {
+    if (64 * i >= a.topk) break;
+    some = some || (in.id[i] >= 0 && in.id[i] < a.vocab);
+  }
+  return __any(some);
 }
 // one whole wave calls this
 __device__ __forceinline__ Slots make_slots(const DistillArgs& a, const SlotLoads& in) {

@@ -32,14 +32,25 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
   void* dx = row_at(a.dx, row, a.dstride, Ty<DT>::E);
   const float c = kLog2e / a.tau;
   const float up = (a.row_scale ? a.row_scale[row] : 1.0f) * (a.coef / a.tau);
-  SlotLoads asked;
-  if (wave == 0) asked = ask_slots(a, row, lane);
+  const SlotLoads asked = ask_slots(a, row, lane, wave == 0);
   u32x4 v[R];
-#pragma unroll
-  for (int i = 0; i < R; i++) {
+  auto load = [&](int i) __attribute__((always_inline)) {
     if (i < R - GUARD) v[i] = ld_row_lane<DT, STREAM>(x, i * NT * V, tid * V);
     else v[i] = Tail<DT>(i * NT * V + tid * V, cols).load(x);
+  };
+  // The first EARLY vectors are asked for before it is known whether the row
+  // has slots, so that this costs no time; the others only if it has.
+  constexpr int EARLY = R < 8 ? R : 4;
+#pragma unroll
+  for (int i = 0; i < EARLY; i++) load(i);
+  if (!has_slots(a, asked)) {
+    const float f[V] = {};
+    for (uint32_t col = tid * V; col < cols; col += NT * V) Tail<DT>(col, cols).store(dx, f);
+    if (tid == 0) a.loss[row] = 0.0f;
+    return;
   }
+#pragma unroll
+  for (int i = EARLY; i < R; i++) load(i);
   slots.head[tid] = -1;
   Slots sl;
   if (wave == 0) {

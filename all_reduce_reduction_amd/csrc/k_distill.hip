@@ -82,8 +82,11 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
   const Columns range = columns_of(a, split);
   const void* x = row_at(a.x, row, a.stride, Ty<DT>::E);
   const float c = kLog2e / a.tau;
-  SlotLoads asked;
-  if (wave == 0) asked = ask_slots(a, row, lane);
+  const SlotLoads asked = ask_slots(a, row, lane, wave == 0);
+  if (a.look_first && !has_slots(a, asked)) {
+    if (tid < 4) a.parts[part_index(split, tid, a.rows, row)] = tid == 0 ? kNegInf : 0.0f;
+    return;
+  }
   Slots sl;
   float at[kSlotsPerLane];
   Scan scan;
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_join(DistillArgs a, float* l
   const int64_t row = (int64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
   if (row >= a.rows) return;
   const int lane = threadIdx.x & 63;
-  const Slots s = make_slots(a, ask_slots(a, row, lane));
+  const Slots s = make_slots(a, ask_slots(a, row, lane, true));
   const Part t = join_parts(a.parts, a.splits, a.rows, row, a.tau, lane);
   if (lane == 0) {
     loss[row] = loss_of(s, t);
@@ -192,8 +195,13 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
   void* dx = row_at(a.dx, row, a.dstride, Ty<DT>::E);
   const float c = kLog2e / a.tau;
   const float up = (a.row_scale ? a.row_scale[row] : 1.0f) * (a.coef / a.tau);
-  SlotLoads asked;
-  if (wave == 0) asked = ask_slots(a, row, lane);
+  const SlotLoads asked = ask_slots(a, row, lane, wave == 0);
+  if (a.look_first && !has_slots(a, asked)) {
+    const float f[V] = {};
+    for (uint32_t col = range.lo + tid * V; col < range.hi; col += kBlock * V) st_guarded<DT>(dx, col, range.hi, f);
+    if (a.loss && split == 0 && tid == 0) a.loss[row] = 0.0f;
+    return;
+  }
   slots.head[tid] = -1;
   Part t{};
   if (a.norm) {
@@ -263,11 +271,21 @@ int64_t distill_span(int64_t cols, int splits) {
     default: return a.cols < 8 ? launch<K<SIM_BF16, true>>(__VA_ARGS__) : launch<K<SIM_BF16, false>>(__VA_ARGS__);       \
   }
 
-hipError_t launch_distill_stats(const DistillArgs& a, int dtype, hipStream_t s) {
+// Whether a workgroup waits for the slots before it reads its columns, to
+// leave out rows without any: where eight or more workgroups share a compute
+// unit, others fill the wait; with fewer it would be part of the call's time.
+DistillArgs with_look(const DistillArgs& in) {
+  DistillArgs a = in;
+  a.look_first = a.rows * a.splits >= 8 * (int64_t)library_cus();
+  return a;
+}
+hipError_t launch_distill_stats(const DistillArgs& in, int dtype, hipStream_t s) {
+  const DistillArgs a = with_look(in);
   const dim3 grid((unsigned)(a.rows * a.splits)), block(kBlock);
   BY_DTYPE(k_distill_stats, grid, block, s, a)
 }
-hipError_t launch_distill_grad(const DistillArgs& a, int dtype, hipStream_t s) {
+hipError_t launch_distill_grad(const DistillArgs& in, int dtype, hipStream_t s) {
+  const DistillArgs a = with_look(in);
   const dim3 grid((unsigned)(a.rows * a.splits)), block(kBlock);
   BY_DTYPE(k_distill_grad, grid, block, s, a)
 }

@@ -67,6 +67,7 @@ struct DistillArgs {
   float* norm;        // [2][rows]
   int splits;         // workgroups per row, each over a run of columns
   int64_t span;       // columns per workgroup
+  int look_first;     // rows without slots are left unread
 };
 
 int route_workgroups(int64_t tokens, int experts, int dtype);

@@ -460,8 +460,8 @@ int sim_verify_custom(int algo, int p, int nchunks, int rounds, int nsteps, cons
  *     least the bytes the matching *_work function says (0: it may be NULL),
  *     4-byte aligned, free for reuse once the call's stream work is done;
  *     too little is SIM_ERR_NOMEM.
- *   - Rows are processed where 0 rows is a no-op apart from the outputs that
- *     do not depend on the row count (zero counts and sums, the loss).
+ *   - 0 rows are a no-op, except that sim_route writes zero counts and sums
+ *     and sim_route_grad writes the loss.
  */
 #define SIM_ROUTE_MAX_EXPERTS 1024
 #define SIM_ROUTE_MAX_TOPK 32
@@ -510,11 +510,12 @@ int sim_route_grad(const void* logits, int64_t row_stride, int dtype, const uint
  *   dlogits[t][v] = coef * row_scale[t] / temperature *
  *                   (p_v - the sum of q_k over the slots with id v)
  * row_scale (may be NULL: all 1) is the upstream gradient of loss[t]; neither
- * it nor coef scales loss.  A row with no slot, or with teacher logits of
- * -inf in all of them, has loss 0 and a zero gradient whatever its logits
- * hold.  temperature lies in [1e-20, 1e20].  Otherwise a NaN, a +inf or a row of -inf
- * alone makes that row's loss and gradient NaN; an id whose own logit is -inf
- * makes the loss +inf.
+ * it nor coef scales loss.  temperature lies in [1e-20, 1e20].  A row with no
+ * slot, or with teacher logits of -inf in all of them, has loss 0 and a zero
+ * gradient whatever its logits hold.  Otherwise a NaN or +inf among a row's
+ * logits, or a row of -inf alone, makes its loss and gradient NaN; a NaN or
+ * +inf among its slots' teacher logits makes its loss, and the gradient of the
+ * slots' columns, NaN; an id whose own logit is -inf makes the loss +inf.
  *
  * sim_distill_step: rows of the whole vocabulary, loss and gradient. */
 int sim_distill_work(int64_t rows, int64_t columns, int dtype, size_t* bytes);
@@ -528,7 +529,8 @@ int sim_distill_step(const void* logits, int64_t row_stride, int dtype, int64_t 
  *   sim_distill_parts  parts[4][rows] of the shard: the largest logit m, the
  *                      sum of exp((x - m)/temperature), the sum of q_k over
  *                      the slots in the shard, and the sum of
- *                      q_k (x[ids_k] - m)/temperature over them
+ *                      q_k (x[ids_k] - m)/temperature over them (a row
+ *                      without slots may be left unread: -inf, 0, 0, 0)
  *   sim_distill_join   parts[nparts][4][rows] of all shards (in rank order,
  *                      as sim_all_gather leaves them) -> loss[rows] and
  *                      norm[2][rows]: the row's largest logit and the sum of
