@@ -133,11 +133,20 @@ __device__ __forceinline__ void gather_slots(const DistillArgs& a, SlotLists<NT>
   }
   if (lane == 0) s.live = sl.live;
 }
+// 1 where a row of 16-bit logits starts in the middle of a word.  Its first
+// column then goes by itself and the vectors start behind it: 16-byte accesses
+// that are not even word-aligned take two passes each (4,096 rows x 50,021
+// bf16, every other one such: 182 us against 157 with 50,022 columns).
+template <int DT>
+__device__ __forceinline__ uint32_t lone_columns(const void* row) {
+  return Ty<DT>::E == 2 ? (uint32_t)((uintptr_t)row >> 1) & 1u : 0u;
+}
 // Wave 0, once the row's maximum and its sum against `top` are known: each
-// slot's probability, and its place in its thread's list.
+// slot's probability, and its place in its thread's list.  `base`: the first
+// vector's column (the column before it is thread 0's).
 template <int DT, int NT>
 __device__ __forceinline__ void hang_slots(const DistillArgs& a, SlotLists<NT>& s, const Slots& sl, int64_t lo,
-                                           int64_t hi, const Against& top, float sum, int lane) {
+                                           int64_t hi, int64_t base, const Against& top, float sum, int lane) {
 #pragma unroll
   for (int i = 0; i < kSlotsPerLane; i++) {
     if (64 * i >= a.topk) break;
@@ -145,7 +154,7 @@ __device__ __forceinline__ void hang_slots(const DistillArgs& a, SlotLists<NT>& 
     const int64_t col = (int64_t)sl.id[i] - a.first;
     if (!sl.live || sl.id[i] < 0 || col < lo || col >= hi) continue;
     s.x[k] = exp_against(s.x[k], top) / sum;
-    s.next[k] = atomicExch(&s.head[((col - lo) / epv<DT>()) % NT], k);
+    s.next[k] = atomicExch(&s.head[col < base ? 0 : (col - base) / epv<DT>() % NT], k);
   }
 }
 // Each slot's column gets up (p - the sum of q over the slots with its id).

@@ -18,18 +18,20 @@
 namespace simar {
 
 // of the R vectors of a thread, the last GUARD may lie past the row's end; a
-// row is at least one vector long
+// row is longer than one vector
 template <int DT, int NT, int R, int GUARD, bool STREAM>
 __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
   constexpr int V = epv<DT>(), W = NT / 64, PAIR = R % 2 ? 1 : 2;
   static_assert((R - GUARD) % PAIR == 0, "a pair lies wholly before the guarded vectors or among them");
-    __shared__ SlotLists<NT> slots;
+  __shared__ SlotLists<NT> slots;
   __shared__ float m_s[W], s_s[W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x;
-  const uint32_t cols = (uint32_t)a.cols;
-  const void* x = row_at(a.x, row, a.stride, Ty<DT>::E);
-  void* dx = row_at(a.dx, row, a.dstride, Ty<DT>::E);
+  const void* row_x = row_at(a.x, row, a.stride, Ty<DT>::E);
+  void* row_dx = row_at(a.dx, row, a.dstride, Ty<DT>::E);
+  const uint32_t lone = lone_columns<DT>(row_x), cols = (uint32_t)a.cols - lone;
+  const void* x = (const char*)row_x + lone * Ty<DT>::E;
+  void* dx = (char*)row_dx + lone * Ty<DT>::E;
   const float c = kLog2e / a.tau;
   const float up = (a.row_scale ? a.row_scale[row] : 1.0f) * (a.coef / a.tau);
   const SlotLoads asked = ask_slots(a, row, lane, wave == 0);
@@ -47,6 +49,7 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
     const float f[V] = {};
     for (uint32_t col = tid * V; col < cols; col += NT * V) Tail<DT>(col, cols).store(dx, f);
     if (tid == 0) a.loss[row] = 0.0f;
+    if (tid == 0 && lone) store_elem<DT>(row_dx, 0, 0.0f);
     return;
   }
 #pragma unroll
@@ -55,9 +58,10 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
   Slots sl;
   if (wave == 0) {
     sl = make_slots(a, asked);
-    gather_slots<DT>(a, slots, sl, x, 0, a.cols, lane);
+    gather_slots<DT>(a, slots, sl, row_x, 0, a.cols, lane);
   }
   Scan scan;
+  const float alone = lone && tid == 0 ? load_elem<DT>(row_x, 0) : kNegInf;
 #pragma unroll
   for (int i = 0; i < R; i += PAIR) {
     if (i < R - GUARD) {
@@ -82,6 +86,7 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
     t.mask(f);
     scan.add(f, c);
   }
+  if (lone) scan.add({alone}, c);
   Running r = wave_running(scan.done(c), c);
   if (lane == 0) {
     m_s[wave] = r.m;
@@ -92,7 +97,7 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
   r.s = lane < W ? s_s[lane] : 0.0f;
   r = wave_running(r, c);
   if (__builtin_expect(far(r.m, c), 0)) {
-    float n = 0.0f;
+    float n = alone == r.m ? 1.0f : 0.0f;
 #pragma unroll 1
     for (uint32_t col = tid * V; col < cols; col += NT * V) {
       const Tail<DT> t(col, cols);
@@ -121,7 +126,7 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
     }
     dot = wave_sum(dot);
     if (lane == 0) a.loss[row] = live ? sl.entropy + __logf(r.s) - dot : 0.0f;
-    hang_slots<DT>(a, slots, sl, 0, a.cols, top, sum, lane);
+    hang_slots<DT>(a, slots, sl, 0, a.cols, lone, top, sum, lane);
   }
   const float k2 = up / sum;
   __syncthreads();
@@ -129,8 +134,10 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
     // (0 * p would keep the NaN of a row that does not count)
     const float f[V] = {};
     for (uint32_t col = tid * V; col < cols; col += NT * V) Tail<DT>(col, cols).store(dx, f);
+    if (tid == 0 && lone) store_elem<DT>(row_dx, 0, 0.0f);
     return;
   }
+  if (tid == 0 && lone) store_elem<DT>(row_dx, 0, exp_against(alone, top) * k2);
 #pragma unroll
   for (int i = 0; i < R; i++) {
     // widened again here: kept from above, the fp32 values would take the
@@ -151,7 +158,7 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
     for (int j = 0; j < V; j++) f[j] = exp_against(f[j], top) * k2;
     t.store(dx, f);
   }
-  write_slots<DT>(a, slots, dx, up, tid);
+  write_slots<DT>(a, slots, row_dx, up, tid);
 }
 
 // The workgroup, the vectors per thread (R, in steps of 2 from 4 on, so that
@@ -172,6 +179,8 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
 template <int DT, int NT, int R, bool STREAM>
 hipError_t launch_row_as(const DistillArgs& a, hipStream_t s) {
   constexpr int G = R % 2 ? 1 : 2;
+  // the kernel reads the first R - G vectors of every thread unchecked
+  if (a.cols <= (int64_t)(R - G) * NT * epv<DT>() || a.cols <= epv<DT>()) return hipErrorInvalidValue;
   return launch<k_distill_row<DT, NT, R, G, STREAM>>(dim3((unsigned)a.rows), dim3(NT), s, a);
 }
 // the smallest R of LEAST, ..., MOST that holds the row (MOST where none does)

@@ -22,15 +22,20 @@ namespace {
 // thread, whose loads are all in flight together: whole chunks (WHOLE), then
 // one that ends at hi.  There each vector is the row's last where its own
 // would reach past the row (see Tail), so that no load waits for a branch.
-// TINY: rows shorter than a vector, element by element.
+// TINY: rows of a vector or less, element by element.
 constexpr int kHeld = 8;
 template <int DT> constexpr uint32_t chunk_cols() { return kHeld * kBlock * epv<DT>(); }
+// `lone`: column 0 by itself before lo, thread 0's (see lone_columns).
 struct Columns {
   uint32_t lo, hi, cols;
+  bool lone;
+  __device__ __forceinline__ int64_t first() const { return lone ? 0 : lo; }
 };
-__device__ __forceinline__ Columns columns_of(const DistillArgs& a, int64_t split) {
-  const int64_t lo = min(a.cols, split * a.span), hi = min(a.cols, lo + a.span);
-  return {(uint32_t)lo, (uint32_t)hi, (uint32_t)a.cols};
+template <int DT, bool TINY>
+__device__ __forceinline__ Columns columns_of(const DistillArgs& a, const void* row, int64_t split) {
+  const int64_t off = TINY ? 0 : lone_columns<DT>(row);
+  const int64_t lo = min(a.cols, split * a.span + off), hi = min(a.cols, (split + 1) * a.span + off);
+  return {(uint32_t)lo, (uint32_t)hi, (uint32_t)a.cols, off != 0 && split == 0};
 }
 // (a thread's place is worked out at each use: kept for eight vectors, it
 // takes 40 registers)
@@ -79,8 +84,8 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
   __shared__ float m_s[W], s_s[W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
-  const Columns range = columns_of(a, split);
   const void* x = row_at(a.x, row, a.stride, Ty<DT>::E);
+  const Columns range = columns_of<DT, TINY>(a, x, split);
   const float c = kLog2e / a.tau;
   const SlotLoads asked = ask_slots(a, row, lane, wave == 0);
   if (a.look_first && !has_slots(a, asked)) {
@@ -90,6 +95,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
   Slots sl;
   float at[kSlotsPerLane];
   Scan scan;
+  const float alone = range.lone && tid == 0 ? load_elem<DT>(x, 0) : kNegInf;
   each_chunk<DT, TINY>(
       x, tid, range,
       [&]() __attribute__((always_inline)) {
@@ -99,7 +105,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
         for (int i = 0; i < kSlotsPerLane; i++) {
           if (64 * i >= a.topk) break;
           const int64_t col = (int64_t)sl.id[i] - a.first;
-          const bool here = sl.id[i] >= 0 && col >= range.lo && col < range.hi;
+          const bool here = sl.id[i] >= 0 && col >= range.first() && col < range.hi;
           at[i] = here ? load_elem<DT>(x, col) : 0.0f;
           if (!here) sl.q[i] = 0.0f;
         }
@@ -114,6 +120,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
           scan.add(f, c);
         }
       });
+  if (range.lone) scan.add({alone}, c);
   Running r = wave_running(scan.done(c), c);
   if (lane == 0) {
     m_s[wave] = r.m;
@@ -124,7 +131,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
   r.s = lane < W ? s_s[lane] : 0.0f;
   r = wave_running(r, c);
   if (__builtin_expect(far(r.m, c), 0)) {
-    float top = 0.0f;
+    float top = alone == r.m ? 1.0f : 0.0f;
     for (int64_t col = range.lo + tid * V; col < range.hi; col += kBlock * V) {
       float f[V];
       load_cols<DT>(x, col, range.hi, f);
@@ -190,8 +197,8 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
   __shared__ SlotLists<kBlock> slots;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
-  const Columns range = columns_of(a, split);
   const void* x = row_at(a.x, row, a.stride, Ty<DT>::E);
+  const Columns range = columns_of<DT, TINY>(a, x, split);
   void* dx = row_at(a.dx, row, a.dstride, Ty<DT>::E);
   const float c = kLog2e / a.tau;
   const float up = (a.row_scale ? a.row_scale[row] : 1.0f) * (a.coef / a.tau);
@@ -199,6 +206,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
   if (a.look_first && !has_slots(a, asked)) {
     const float f[V] = {};
     for (uint32_t col = range.lo + tid * V; col < range.hi; col += kBlock * V) st_guarded<DT>(dx, col, range.hi, f);
+    if (range.lone && tid == 0) store_elem<DT>(dx, 0, 0.0f);
     if (a.loss && split == 0 && tid == 0) a.loss[row] = 0.0f;
     return;
   }
@@ -214,16 +222,17 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
   const float sum = t.s * exp2_hw(at_max(t.m, top));  // against top.t
   const float k2 = up / sum;
   bool live = true;
+  const float alone = range.lone && tid == 0 ? load_elem<DT>(x, 0) : kNegInf;
   each_chunk<DT, TINY>(
       x, tid, range,
       [&]() __attribute__((always_inline)) {
         __syncthreads();
         if (wave == 0) {
           const Slots sl = make_slots(a, asked);
-          gather_slots<DT>(a, slots, sl, x, range.lo, range.hi, lane);
+          gather_slots<DT>(a, slots, sl, x, range.first(), range.hi, lane);
           wave_fence();
           if (lane == 0 && a.loss && split == 0) a.loss[row] = loss_of(sl, t);
-          hang_slots<DT>(a, slots, sl, range.lo, range.hi, top, sum, lane);
+          hang_slots<DT>(a, slots, sl, range.first(), range.hi, range.lo, top, sum, lane);
         }
         __syncthreads();
         live = slots.live;
@@ -242,6 +251,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
           else st_guarded<DT>(dx, (i * kBlock + tid) * V, range.cols, f);
         }
       });
+  if (range.lone && tid == 0) store_elem<DT>(dx, 0, live ? exp_against(alone, top) * k2 : 0.0f);
   write_slots<DT>(a, slots, dx, up, tid);
 }
 
@@ -249,7 +259,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
 
 bool distill_whole_rows(int64_t rows, int64_t cols, int dtype) {
   const int v = dtype == SIM_FP32 ? 4 : 8;
-  if (cols < v) return false;
+  if (cols <= v) return false;
   return (cols + v - 1) / v <= 16 * 1024 || rows >= library_cus() / 2;
 }
 // Workgroups per row: enough for two per compute unit, each with at least
@@ -266,9 +276,9 @@ int64_t distill_span(int64_t cols, int splits) {
 
 #define BY_DTYPE(K, ...)                                                                              \
   switch (dtype) {                                                                                    \
-    case SIM_FP32: return a.cols < 4 ? launch<K<SIM_FP32, true>>(__VA_ARGS__) : launch<K<SIM_FP32, false>>(__VA_ARGS__); \
-    case SIM_FP16: return a.cols < 8 ? launch<K<SIM_FP16, true>>(__VA_ARGS__) : launch<K<SIM_FP16, false>>(__VA_ARGS__); \
-    default: return a.cols < 8 ? launch<K<SIM_BF16, true>>(__VA_ARGS__) : launch<K<SIM_BF16, false>>(__VA_ARGS__);       \
+    case SIM_FP32: return a.cols <= 4 ? launch<K<SIM_FP32, true>>(__VA_ARGS__) : launch<K<SIM_FP32, false>>(__VA_ARGS__); \
+    case SIM_FP16: return a.cols <= 8 ? launch<K<SIM_FP16, true>>(__VA_ARGS__) : launch<K<SIM_FP16, false>>(__VA_ARGS__); \
+    default: return a.cols <= 8 ? launch<K<SIM_BF16, true>>(__VA_ARGS__) : launch<K<SIM_BF16, false>>(__VA_ARGS__);       \
   }
 
 // Whether a workgroup waits for the slots before it reads its columns, to
