@@ -55,22 +55,30 @@ __device__ __forceinline__ void load_chunk(const void* x, uint32_t col, int tid,
     else v[i] = tail<DT>(col, i, tid, r).load(x);
   }
 }
-// All chunks: load, `first` behind the first loads, use(v, col, whole).
+// All chunks: load, `first` behind the first loads, use(v, col, whole).  A
+// last chunk of one vector per thread or less is asked for with the first, so
+// that it costs no wait of its own.
 template <int DT, bool TINY, class First, class Use>
 __device__ __forceinline__ void each_chunk(const void* x, int tid, const Columns& r, First first, Use use) {
-  u32x4 v[kHeld];
+  constexpr uint32_t chunk = chunk_cols<DT>();
   uint32_t col = r.lo;
-  if (!TINY && col + chunk_cols<DT>() <= r.hi) {
+  u32x4 v[kHeld];
+  if (!TINY && col + chunk <= r.hi) {
+    const uint32_t last = r.hi - (r.hi - r.lo) % chunk;
     load_chunk<DT, true, false>(x, col, tid, r, v);
+    u32x4 few[1] = {tail<DT>(last, 0, tid, r).load(x)};
     first();
     use(v, col, std::true_type());
 #pragma unroll 1
-    for (col += chunk_cols<DT>(); col + chunk_cols<DT>() <= r.hi; col += chunk_cols<DT>()) {
+    for (col += chunk; col < last; col += chunk) {
       load_chunk<DT, true, false>(x, col, tid, r, v);
       use(v, col, std::true_type());
     }
-    if (col >= r.hi) return;
-    load_chunk<DT, false, TINY>(x, col, tid, r, v);
+    if (last + kBlock * epv<DT>() >= r.hi) {
+      use(few, last, std::false_type());
+      return;
+    }
+    load_chunk<DT, false, TINY>(x, last, tid, r, v);
   } else {
     load_chunk<DT, false, TINY>(x, col, tid, r, v);
     first();
@@ -110,13 +118,13 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
           if (!here) sl.q[i] = 0.0f;
         }
       },
-      [&](u32x4(&v)[kHeld], uint32_t col, auto whole) __attribute__((always_inline)) {
+      [&](auto& v, uint32_t col, auto whole) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < kHeld; i++) {
+        for (int i = 0; i < (int)(sizeof v / sizeof v[0]); i++) {
           if (!whole() && col + i * kBlock * V >= range.hi) break;
           float f[V];
           unpack<DT>(v[i], f);
-          if (!whole() && !TINY) tail<DT>(col, i, tid, range).mask(f);
+          if (!whole() && !TINY && col + (i + 1) * kBlock * V > range.hi) tail<DT>(col, i, tid, range).mask(f);
           scan.add(f, c);
         }
       });
@@ -237,9 +245,9 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
         __syncthreads();
         live = slots.live;
       },
-      [&](u32x4(&v)[kHeld], uint32_t col, auto whole) __attribute__((always_inline)) {
+      [&](auto& v, uint32_t col, auto whole) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < kHeld; i++) {
+        for (int i = 0; i < (int)(sizeof v / sizeof v[0]); i++) {
           if (!whole() && col + i * kBlock * V >= range.hi) break;
           float f[V];
           unpack<DT>(v[i], f);
