@@ -22,8 +22,11 @@ namespace {
 // thread, whose loads are all in flight together: whole chunks (WHOLE), then
 // one that ends at hi.  There each vector is the row's last where its own
 // would reach past the row (see Tail), so that no load waits for a branch.
-// TINY: rows of a vector or less, element by element.
-constexpr int kHeld = 8;
+// TINY: rows of a vector or less, element by element.  Four vectors: a
+// gradient's workgroup of 16 KiB ends sooner, so that fewer reads and writes of
+// different runs meet in memory (4,096 x 50,021 bf16: 145 us; with eight 157,
+// with two 155).
+constexpr int kHeld = 4;
 template <int DT> constexpr uint32_t chunk_cols() { return kHeld * kBlock * epv<DT>(); }
 // `lone`: column 0 by itself before lo, thread 0's (see lone_columns).
 struct Columns {
@@ -37,8 +40,8 @@ __device__ __forceinline__ Columns columns_of(const DistillArgs& a, const void* 
   const int64_t lo = min(a.cols, split * a.span + off), hi = min(a.cols, (split + 1) * a.span + off);
   return {(uint32_t)lo, (uint32_t)hi, (uint32_t)a.cols, off != 0 && split == 0};
 }
-// (a thread's place is worked out at each use: kept for eight vectors, it
-// takes 40 registers)
+// (a thread's place is worked out at each use: kept for all vectors of a chunk,
+// it would take more registers than the vectors)
 template <int DT>
 __device__ __forceinline__ Tail<DT> tail(uint32_t col, int i, int tid, const Columns& r) {
   constexpr int V = epv<DT>();
