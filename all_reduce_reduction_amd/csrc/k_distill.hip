@@ -89,6 +89,9 @@ __device__ __forceinline__ void each_chunk(const void* x, int tid, const Columns
   use(v, col, std::false_type());
 }
 
+// Bound by the read: 24 to 27 us for 4,096 rows x 16,384 bf16 (5.0 to 5.6 TB/s),
+// 67 us for 4,096 x 50,021 (6.1 TB/s).  Workgroups of 256 threads, as many of
+// them share a compute unit (512 threads: 47 us for 4,096 x 16,385 against 30).
 template <int DT, bool TINY>
 __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
   constexpr int V = epv<DT>(), W = kBlock / 64;
@@ -174,7 +177,8 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
   }
 }
 
-// one wave per row
+// One wave per row, a lane per part: 3.8 us for 333 rows, 5.0 for 4,096, most
+// of it the launch and one round trip to memory (a loop over the parts: 11).
 __global__ void __launch_bounds__(kBlock) k_distill_join(DistillArgs a, float* loss, float* norm) {
   const int64_t row = (int64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
   if (row >= a.rows) return;
@@ -202,6 +206,8 @@ __global__ void __launch_bounds__(kBlock) k_distill_merge(DistillArgs a, float* 
 }
 
 // The gradient of a run of columns, from the row's joined parts or its norm.
+// Bound by reading and writing at once: 48 us for 4,096 rows x 16,384 bf16 (5.5
+// TB/s; a copy of as many bytes 42).
 template <int DT, bool TINY>
 __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
   constexpr int V = epv<DT>();
