@@ -80,6 +80,8 @@ struct PtrSlot {
   bool ready = false;
 };
 
+constexpr size_t kTurns = 64, kTurnWords = 32;  // streams with a counter; a 128-byte line each
+
 struct Ctx {
   bool init = false;
   int device = 0;
@@ -109,6 +111,10 @@ struct Ctx {
   int fifo_vecs = kFifoVecsPerLane;  // 16-byte vectors per lane per slot: 1, 2 or 4
   bool capturing = false;  // the current call's stream is being captured into a graph
   bool captured = false;   // some call has been captured since sim_init
+  // counters of the launches whose last workgroup finishes the work: one per
+  // stream, a cache line apart
+  uint32_t* turns = nullptr;
+  std::vector<hipStream_t> turn_streams;
   std::vector<void*> retired;  // outgrown scratch a captured graph may still use
   // pointer table (one-shot calls outside graph capture): slot i of `ptab`
   // holds a pointer set, copied from slot i of the pinned `ptab_host`; slots
@@ -1326,6 +1332,22 @@ int parse_algo_env(const char* v) {
 bool library_ready() { return g.init; }
 int library_device() { return use_device(); }
 int library_cus() { return g.cu_count; }
+uint32_t* library_turn(hipStream_t stream) {
+  if (!g.turns || stream == hipStreamPerThread) return nullptr;
+  hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(stream, &st) != hipSuccess) {
+    (void)hipGetLastError();
+    return nullptr;
+  }
+  if (st != hipStreamCaptureStatusNone) return nullptr;
+  size_t i = 0;
+  while (i < g.turn_streams.size() && g.turn_streams[i] != stream) i++;
+  if (i == g.turn_streams.size()) {
+    if (i == kTurns) return nullptr;
+    g.turn_streams.push_back(stream);
+  }
+  return g.turns + i * kTurnWords;
+}
 
 }  // namespace simar
 
@@ -1354,7 +1376,7 @@ const char* sim_status_string(int status) {
 int sim_finalize(void) {
   // (also releases what a failed sim_init had allocated before it gave up)
   if (!g.init && !g.err && !g.ll && !g.fifo_sem && !g.scratch && !g.ptab && !g.ptab_host && !g.ph_mem &&
-      !g.ph_host_done)
+      !g.ph_host_done && !g.turns)
     return SIM_OK;
   // teardown is best effort: every allocation is released even if one call fails
   (void)hipSetDevice(g.device);
@@ -1365,6 +1387,7 @@ int sim_finalize(void) {
   if (g.fifo) (void)hipFree(g.fifo);
   if (g.fifo_sem) (void)hipFree(g.fifo_sem);
   if (g.ph_mem) (void)hipFree(g.ph_mem);
+  if (g.turns) (void)hipFree(g.turns);
   if (g.ph_host_done) (void)hipHostFree(g.ph_host_done);
   if (g.err) (void)hipFree(g.err);
   for (PtrSlot& sl : g.ptab_slots)
@@ -1436,6 +1459,15 @@ int sim_init(int device, int p_max, size_t max_bytes_per_rank) {
     g.ph_dev_done = nullptr;
   } else {
     *g.ph_host_done = 0;
+  }
+  // (without the counters a second launch finishes such work)
+  if (hipMalloc(&g.turns, kTurns * kTurnWords * 4) != hipSuccess) {
+    (void)hipGetLastError();
+    g.turns = nullptr;
+  } else if (launch_fill64((unsigned long long*)g.turns, 0ull, kTurns * kTurnWords / 2, nullptr) != hipSuccess ||
+             hipDeviceSynchronize() != hipSuccess) {
+    sim_finalize();
+    return SIM_ERR_HIP;
   }
   // the pointer table only makes launches cheaper: without it every call
   // carries its pointers in its kernel arguments

@@ -140,8 +140,10 @@ int sim_route(const void* logits, int64_t row_stride, int dtype, const uint8_t* 
                        {need ? work : nullptr, need, 4, true}};
   if ((rc = check_arrays(all, -1, -1, false))) return rc;
   if ((rc = library_device())) return rc;
+  const int wg = route_workgroups(tokens, experts, dtype);
+  uint32_t* const turn = route_sums_itself(wg, experts) ? library_turn((hipStream_t)stream) : nullptr;
   const RouteArgs a{logits, row_stride, keep, tokens, experts, topk, normalize != 0, chosen, weights, counts, prob_sums,
-                    (uint32_t*)work, route_workgroups(tokens, experts, dtype)};
+                    (uint32_t*)work, wg, turn};
   return hip_status(launch_route(a, dtype, (hipStream_t)stream));
 }
 

@@ -18,7 +18,7 @@
 // a group's loads cover whole lines.  With many rows per wave the cross-lane
 // steps of one row (log2 L of them) serve 64 / L rows at once, and they run
 // over DPP while L is 8 or 16.
-#include "device_common.h"
+#include "device_sync.h"
 #include "launch.h"
 #include "loss.h"
 #include "loss_device.h"
@@ -250,6 +250,48 @@ __device__ __forceinline__ void top_in_turn(const Gate<DT, L, N>& g, int l, int 
   }
 }
 
+// ---- the workgroups' counts and sums ------------------------------------------------
+// A word that another workgroup of this launch reads goes to device scope.
+__device__ __forceinline__ void put(uint32_t* p, uint32_t v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The workgroup that arrives last adds up what all of them have written, in
+// the workgroups' order.  No workgroup waits for another one.  This takes a
+// launch less than k_route_sum (1,003 rows x 60 fp32, top 4: 7.2 us against
+// 9.7).
+__device__ __forceinline__ void sum_in_last(const RouteArgs& a, uint32_t* word_s) {
+  constexpr int kFlight = 32;  // loads of a thread under way (16: 9.3 us where 32 take 8.5)
+  wait_stores();
+  __syncthreads();
+  if (threadIdx.x == 0) *word_s = __hip_atomic_fetch_add(a.turn, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (*word_s != (uint32_t)a.workgroups - 1) return;
+  const int all = 2 * a.experts + 1;
+  for (int e = threadIdx.x; e < all; e += kBlock) {
+    uint32_t n = 0;
+    float s = 0.0f;
+    for (int w0 = 0; w0 < a.workgroups; w0 += kFlight) {
+      uint32_t v[kFlight];
+      const uint32_t* from = a.partial + (int64_t)w0 * all + e;
+#pragma unroll
+      for (int i = 0; i < kFlight; i++) {
+        v[i] = 0;
+        if (w0 + i < a.workgroups)
+          v[i] = __hip_atomic_load(from + (int64_t)i * all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+#pragma unroll
+      for (int i = 0; i < kFlight; i++) {
+        n += v[i];
+        s += __builtin_bit_cast(float, v[i]);
+      }
+    }
+    if (e <= a.experts) a.counts[e] = (int32_t)n;
+    else a.sums[e - a.experts - 1] = s;
+  }
+  if (threadIdx.x == 0) put(a.turn, 0);
+}
+
 // ---- forward ------------------------------------------------------------------------
 // Up to eight chosen experts come from one pass of the exchange networks; each
 // further eight from another one below the last key.  MANY: topk > 8.
@@ -418,10 +460,11 @@ __global__ void __launch_bounds__(kBlock, N == 32 ? 3 : 4) k_route(RouteArgs a) 
       a.counts[e] = (int32_t)n;
       if (e < a.experts) a.sums[e] = s;
     } else {
-      part[e] = n;
-      if (e < a.experts) part[a.experts + 1 + e] = __builtin_bit_cast(uint32_t, s);
+      put(part + e, n);
+      if (e < a.experts) put(part + a.experts + 1 + e, __builtin_bit_cast(uint32_t, s));
     }
   }
+  if (a.turn) sum_in_last(a, &count_s[0]);
 }
 
 // The workgroups' counts and sums, kSumCols of them per workgroup: 1024
@@ -620,11 +663,20 @@ int route_workgroups(int64_t tokens, int experts, int dtype) {
   return (int)(wg < 3 ? 1 : wg);
 }
 
+// One compute unit reads few words at a time: the workgroups add up their own
+// sums up to this many words (bf16, top 8: 1,024 rows x 256, 16,416 words, 8.5
+// us against 9.7 with the second launch; 2,048 rows, 32,832 words, 11.0 against
+// 9.8), and up to as many workgroups as k_route_sum takes in plain order, so
+// that both give the same bits.
+bool route_sums_itself(int workgroups, int experts) {
+  return workgroups > 1 && workgroups <= kSumRows && workgroups * (2 * experts + 1) <= 24 << 10;
+}
+
 hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s) {
   const hipError_t e = dtype == SIM_FP32   ? route_dtype<SIM_FP32>(a, s)
                        : dtype == SIM_FP16 ? route_dtype<SIM_FP16>(a, s)
                                            : route_dtype<SIM_BF16>(a, s);
-  if (e != hipSuccess || a.workgroups == 1) return e;
+  if (e != hipSuccess || a.workgroups == 1 || a.turn) return e;
   return launch<k_route_sum>(dim3((2 * a.experts + kSumCols) / kSumCols), dim3(kSumCols * kSumRows), s, a);
 }
 hipError_t launch_route_grad(const RouteGradArgs& a, int dtype, hipStream_t s) {

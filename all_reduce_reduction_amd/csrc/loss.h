@@ -18,6 +18,11 @@ namespace simar {
 bool library_ready();
 int library_device();
 int library_cus();
+// A word of device memory that holds 0 between the launches of `stream`, for
+// those launches alone; NULL where there is none: a captured stream (its graph
+// may run on any other), the per-thread stream (one handle for many), more
+// streams than there are words.
+uint32_t* library_turn(hipStream_t stream);
 
 struct RouteArgs {
   const void* x;
@@ -31,6 +36,7 @@ struct RouteArgs {
   float* sums;
   uint32_t* partial;  // per workgroup: experts + 1 counts, then experts sums
   int workgroups;
+  uint32_t* turn;     // 0 before and after the launch: the workgroups add up their own sums
 };
 
 struct RouteGradArgs {
@@ -71,6 +77,7 @@ struct DistillArgs {
 };
 
 int route_workgroups(int64_t tokens, int experts, int dtype);
+bool route_sums_itself(int workgroups, int experts);
 hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s);
 hipError_t launch_route_grad(const RouteGradArgs& a, int dtype, hipStream_t s);
 

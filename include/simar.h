@@ -456,7 +456,8 @@ int sim_verify_custom(int algo, int p, int nchunks, int rounds, int nsteps, cons
  *   - Statistics are fp32 whatever `dtype` is, and every sum is taken in an
  *     order that depends on the sizes alone: the same call on the same data
  *     gives the same bits.
- *   - Library memory is not used.  `work` is the caller's scratch of at
+ *   - Of library memory only one counter per stream is used, by sim_route
+ *     outside of capture.  `work` is the caller's scratch of at
  *     least the bytes the matching *_work function says (0: it may be NULL),
  *     4-byte aligned, free for reuse once the call's stream work is done;
  *     too little is SIM_ERR_NOMEM.

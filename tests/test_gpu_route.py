@@ -270,3 +270,61 @@ def test_refusals(lib):
     with pytest.raises(lib.SimError):
         lib.route(x, 40)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("t,e,k", [(96, 8, 2), (97, 256, 8), (700, 100, 16), (1024, 256, 8), (2048, 64, 8), (2049, 64, 8),
+                                   (512, 512, 4)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sums_of_a_graph_have_the_bits_of_a_call(lib, t, e, k, dtype):
+    """A captured call adds up its workgroups' sums in a launch of its own."""
+    x = logits(t, e, dtype, 23).cuda()
+    want = [v.clone() for v in lib.route(x, k)]
+    out = tuple(torch.empty_like(v) for v in want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lib.route(x, k, out=out)
+    for _ in range(3):
+        for v in out:
+            v.zero_()
+        graph.replay()
+        again = lib.route(x, k)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) and torch.equal(c, b) for a, b, c in zip(out, want, again))
+
+
+def test_small_calls_on_several_streams_at_once(lib):
+    t = 1500
+    xs = [logits(t, 64, torch.bfloat16, 30 + i).cuda() for i in range(6)]
+    want = [[v.clone() for v in lib.route(x, 6)] for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[] for _ in xs]
+    for _ in range(20):
+        for x, s, g in zip(xs, streams, got):
+            g.append(lib.route(x, 6, stream=s))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(a, b) for call in g for a, b in zip(call, w))
+
+
+def test_more_streams_than_counters(lib):
+    import ctypes
+    hip = ctypes.CDLL("libamdhip64.so")
+    x = logits(500, 32, torch.float16, 41).cuda()
+    want = [v.clone() for v in lib.route(x, 4)]
+    torch.cuda.synchronize()
+    raw = []
+    try:
+        for _ in range(70):
+            s = ctypes.c_void_p()
+            assert hip.hipStreamCreate(ctypes.byref(s)) == 0
+            raw.append(s)
+        out = [tuple(torch.empty_like(v) for v in want) for _ in raw]
+        torch.cuda.synchronize()
+        for s, o in zip(raw, out):
+            lib.route(x, 4, out=o, stream=torch.cuda.ExternalStream(s.value))
+        torch.cuda.synchronize()
+    finally:
+        for s in raw:
+            hip.hipStreamDestroy(s)
+    assert all(torch.equal(a, b) for o in out for a, b in zip(o, want))

@@ -9,6 +9,7 @@ from tests import loss_oracle as oracle
 
 def test_refused_before_init():
     import all_reduce_reduction_amd as sim
+    sim.sim_finalize()
     assert sim.sim_route(None, 8, "bf16", None, 0, 8, 2, 1, None, None, None, None, None, 0) == -9
     assert sim.sim_route_grad(None, 8, "bf16", None, 0, 8, 2, 1, None, None, None, None, 0.0, None, 8, None) == -9
     assert sim.sim_distill_step(None, 8, "bf16", 0, 8, None, None, "fp32", 2, 1.0, None, 1.0, None, 8, None, None,
