@@ -462,40 +462,48 @@ def _vec_py(t, what, dtypes, device, *shape):
     """Pointer of a contiguous device tensor of the given shape and one of the given dtypes (None: None)."""
     if t is None:
         return None
-    if t.dtype not in dtypes or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous tensor {shape!r} of one of {dtypes!r} on {device}")
+    if t.dtype not in dtypes or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous tensor {shape!r} of one of {dtypes!r} on cuda:{device}")
     return t.data_ptr()
 
 
-if hasattr(_pycall, "bind"):
-    # arguments converted and tensors checked in C: of a small call's 7.3 us on the host, ctypes and the same checks
-    # in Python took about 2
-    for _name in _ENTRIES:
-        _pycall.bind(_name, ctypes.cast(lib["sim_" + _name], ctypes.c_void_p).value)
-    _entry, _vec = _pycall, _pycall.pointer
-else:
-    import types as _types
-    _entry, _vec = _types.SimpleNamespace(**{n: getattr(lib, "sim_" + n) for n in _ENTRIES}), _vec_py
-
-
-def _code_of(t) -> int:
-    c = _TORCH_CODE.get(t.dtype)
-    if c is None:
-        raise ValueError(f"unsupported dtype {t.dtype}")
-    return c
-
-
-def _rows(t, what, like=None):
-    """(pointer, row stride) of a 2-D device tensor whose rows are contiguous."""
+def _rows_py(t, what, like):
+    """(pointer, row stride, rows, columns, dtype code, device index) of a 2-D device tensor whose rows are
+    contiguous; like: None, or the tuple of a tensor whose shape, dtype and device it must have."""
     if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{what} must be a 2-D device tensor")
     n, c = t.shape
     st = t.stride()
     if st[1] != 1 and c > 1:
         raise ValueError(f"{what}'s rows must be contiguous")
-    if like is not None and (t.dtype is not like.dtype or t.shape != like.shape or t.device != like.device):
+    if t.dtype not in _TORCH_CODE:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    got = (t.data_ptr(), st[0] if n > 1 else c, n, c, _TORCH_CODE[t.dtype], t.get_device())
+    if like is not None and got[2:] != like[2:]:
         raise ValueError(f"{what} must have the logits' shape, dtype and device")
-    return t.data_ptr(), (st[0] if n > 1 else c)
+    return got
+
+
+def _slots_py(ids, teacher, dtypes, rows, device):
+    """(ids pointer, teacher pointer, its dtype code, topk)"""
+    if ids.dim() != 2:
+        raise ValueError("ids must be [rows, topk]")
+    k = ids.shape[1]
+    return (_vec_py(ids, "ids", dtypes, device, rows, k), _vec_py(teacher, "teacher", _FLOATS, device, rows, k),
+            _TORCH_CODE[teacher.dtype], k)
+
+
+if hasattr(_pycall, "slots") and torch is not None:
+    # arguments converted and tensors checked in C: of a small call's 7.3 us on the host, ctypes and the same checks
+    # in Python took about 3
+    for _name in _ENTRIES:
+        _pycall.bind(_name, ctypes.cast(lib["sim_" + _name], ctypes.c_void_p).value)
+    _pycall.types(*_FLOATS)
+    _entry, _vec, _rows, _slots = _pycall, _pycall.pointer, _pycall.rows, _pycall.slots
+else:
+    import types as _types
+    _entry, _vec = _types.SimpleNamespace(**{n: getattr(lib, "sim_" + n) for n in _ENTRIES}), _vec_py
+    _rows, _slots = _rows_py, _slots_py
 
 
 def _on(stream, device):
@@ -504,7 +512,7 @@ def _on(stream, device):
     if stream is not None:
         return stream.cuda_stream or None
     if _raw_stream is not None:
-        return _raw_stream(device.index) or None
+        return _raw_stream(device) or None
     return torch.cuda.current_stream(device).cuda_stream or None
 
 
@@ -529,9 +537,7 @@ def route(logits, topk: int, keep=None, normalize: bool = True, out=None, stream
     """Softmax gate of logits [tokens, experts]: (chosen int32 [tokens, topk], weights fp32 [tokens, topk], counts
     int32 [experts + 1], prob_sums fp32 [experts]); ``sim_route`` in include/simar.h says what each holds.  keep:
     bool or uint8 [tokens].  out: the same four tensors, to write into."""
-    ptr, ld = _rows(logits, "logits")
-    n, e = logits.shape
-    dev, dt = logits.device, _code_of(logits)
+    ptr, ld, n, e, dt, dev = _rows(logits, "logits", None)
     if out is None:
         out = (_empty((n, topk), torch.int32, dev, stream), _empty((n, topk), torch.float32, dev, stream),
                _empty(e + 1, torch.int32, dev, stream), _empty(e, torch.float32, dev, stream))
@@ -550,15 +556,13 @@ def route_grad(logits, chosen, dweights=None, counts=None, prob_sums=None, coef:
     """Balance loss of the (reduced) counts and prob_sums, and the gradient of that loss and of the combine weights
     for the logits: (loss fp32 [1], dlogits); ``sim_route_grad`` in include/simar.h says what each holds.  out: the
     same two tensors, to write into (dlogits may be the logits)."""
-    ptr, ld = _rows(logits, "logits")
-    n, e = logits.shape
-    dev = logits.device
+    ptr, ld, n, e, dt, dev = mine = _rows(logits, "logits", None)
     topk = chosen.shape[1]
     if out is None:
         out = (_empty(1, torch.float32, dev, stream), _empty((n, e), logits.dtype, dev, stream))
     loss, dlogits = out
-    dptr, dld = _rows(dlogits, "dlogits", like=logits)
-    _check(_entry.route_grad(ptr, ld, _code_of(logits), _vec(keep, "keep", _MASK, dev, n), n, e, topk,
+    dptr, dld, *_ = _rows(dlogits, "dlogits", mine)
+    _check(_entry.route_grad(ptr, ld, dt, _vec(keep, "keep", _MASK, dev, n), n, e, topk,
                              bool(normalize), _vec(chosen, "chosen", _I32, dev, n, topk),
                              _vec(dweights, "dweights", _F32, dev, n, topk), _vec(counts, "counts", _I32, dev, e + 1),
                              _vec(prob_sums, "prob_sums", _F32, dev, e), coef, dptr, dld,
@@ -566,28 +570,17 @@ def route_grad(logits, chosen, dweights=None, counts=None, prob_sums=None, coef:
     return out
 
 
-def _slots(ids, teacher, rows, device):
-    """(ids pointer, teacher pointer, its dtype code, topk)"""
-    if ids.dim() != 2:
-        raise ValueError("ids must be [rows, topk]")
-    k = ids.shape[1]
-    return (_vec(ids, "ids", _I32, device, rows, k), _vec(teacher, "teacher", _FLOATS, device, rows, k),
-            _code_of(teacher), k)
-
-
 def distill_step(logits, ids, teacher, temperature: float = 1.0, row_scale=None, coef: float = 1.0, out=None,
                  stream=None):
     """Distillation of logits [rows, vocab] from a teacher's top logits (ids int32 [rows, topk], teacher [rows,
     topk]): (loss fp32 [rows], dlogits); ``sim_distill_step`` in include/simar.h says what each holds.  out: the same
     two tensors, to write into (dlogits may be the logits)."""
-    ptr, ld = _rows(logits, "logits")
-    n, v = logits.shape
-    dev, dt = logits.device, _code_of(logits)
+    ptr, ld, n, v, dt, dev = mine = _rows(logits, "logits", None)
     if out is None:
         out = (_empty(n, torch.float32, dev, stream), _empty((n, v), logits.dtype, dev, stream))
     loss, dlogits = out
-    dptr, dld = _rows(dlogits, "dlogits", like=logits)
-    ip, tp, tdt, k = _slots(ids, teacher, n, dev)
+    dptr, dld, *_ = _rows(dlogits, "dlogits", mine)
+    ip, tp, tdt, k = _slots(ids, teacher, _I32, n, dev)
     nb = sim_distill_work(n, v, dt)
     w, wp = _work(nb, dev, stream)
     _check(_entry.distill_step(ptr, ld, dt, n, v, ip, tp, tdt, k, temperature,
@@ -600,12 +593,10 @@ def distill_parts(logits, ids, teacher, temperature: float = 1.0, first: int = 0
                   out=None, stream=None):
     """A vocabulary shard's statistics, fp32 [4, rows]: logits hold the columns from `first` on of `vocab` (default:
     up to the shard's end)."""
-    ptr, ld = _rows(logits, "logits")
-    n, c = logits.shape
-    dev, dt = logits.device, _code_of(logits)
+    ptr, ld, n, c, dt, dev = _rows(logits, "logits", None)
     if out is None:
         out = _empty((4, n), torch.float32, dev, stream)
-    ip, tp, tdt, k = _slots(ids, teacher, n, dev)
+    ip, tp, tdt, k = _slots(ids, teacher, _I32, n, dev)
     nb = sim_distill_work(n, c, dt)
     w, wp = _work(nb, dev, stream)
     _check(_entry.distill_parts(ptr, ld, dt, n, c, first, first + c if vocab is None else vocab, ip, tp, tdt, k,
@@ -620,11 +611,11 @@ def distill_join(parts, ids, teacher, temperature: float = 1.0, vocab: Optional[
     if parts.dim() != 3 or not parts.is_cuda:
         raise ValueError("parts must be a device tensor [nparts, 4, rows]")
     p, _, n = parts.shape
-    dev = parts.device
+    dev = parts.get_device()
     if out is None:
         out = (_empty(n, torch.float32, dev, stream), _empty((2, n), torch.float32, dev, stream))
     loss, norm = out
-    ip, tp, tdt, k = _slots(ids, teacher, n, dev)
+    ip, tp, tdt, k = _slots(ids, teacher, _I32, n, dev)
     _check(_entry.distill_join(_vec(parts, "parts", _F32, dev, p, 4, n), p, n, 2 ** 31 - 1 if vocab is None else vocab,
                                ip, tp, tdt, k, temperature, _vec(loss, "loss", _F32, dev, n),
                                _vec(norm, "norm", _F32, dev, 2, n), _on(stream, dev)), "sim_distill_join")
@@ -635,14 +626,12 @@ def distill_grad(logits, ids, teacher, norm, temperature: float = 1.0, row_scale
                  first: int = 0, vocab: Optional[int] = None, out=None, stream=None):
     """The gradient of a vocabulary shard's logits from the joined norm [2, rows].  out: the gradient, to write into
     (it may be the logits)."""
-    ptr, ld = _rows(logits, "logits")
-    n, c = logits.shape
-    dev = logits.device
+    ptr, ld, n, c, dt, dev = mine = _rows(logits, "logits", None)
     if out is None:
         out = _empty((n, c), logits.dtype, dev, stream)
-    dptr, dld = _rows(out, "dlogits", like=logits)
-    ip, tp, tdt, k = _slots(ids, teacher, n, dev)
-    _check(_entry.distill_grad(ptr, ld, _code_of(logits), n, c, first, first + c if vocab is None else vocab, ip, tp,
+    dptr, dld, *_ = _rows(out, "dlogits", mine)
+    ip, tp, tdt, k = _slots(ids, teacher, _I32, n, dev)
+    _check(_entry.distill_grad(ptr, ld, dt, n, c, first, first + c if vocab is None else vocab, ip, tp,
                                tdt, k, temperature, _vec(norm, "norm", _F32, dev, 2, n),
                                _vec(row_scale, "row_scale", _F32, dev, n), coef, dptr, dld, _on(stream, dev)),
            "sim_distill_grad")

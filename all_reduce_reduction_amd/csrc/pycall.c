@@ -195,58 +195,202 @@ static PyObject* py_bind(PyObject* self, PyObject* args) {
   return NULL;
 }
 
-/* pointer(tensor, what, dtypes, device, *shape): the data pointer of a
- * contiguous tensor of that shape, device and one of those dtypes (None for
- * None). */
-static PyObject *s_dtype, *s_shape, *s_device, *s_contiguous, *s_data_ptr;
+/* ---- tensors -------------------------------------------------------------------
+ * What the helpers have to know of a tensor, through its own attributes and
+ * methods.  types(...) sets the logit types once: code i + 1 is entry i. */
+#define TYPES 3
+static PyObject* logit_type[TYPES];
+static PyObject *s_dtype, *s_shape, *s_device, *s_contiguous, *s_data_ptr, *s_stride;
+
+static PyObject* py_types(PyObject* self, PyObject* args) {
+  (void)self;
+  PyObject* t[TYPES];
+  if (!PyArg_ParseTuple(args, "OOO", &t[0], &t[1], &t[2])) return NULL;
+  for (int i = 0; i < TYPES; i++) {
+    Py_INCREF(t[i]);
+    Py_XSETREF(logit_type[i], t[i]);
+  }
+  Py_RETURN_NONE;
+}
+
+/* the code of a tensor's type, 0 for any other type, -1 on an error */
+static int code_of(PyObject* t) {
+  PyObject* v = PyObject_GetAttr(t, s_dtype);
+  if (!v) return -1;
+  Py_DECREF(v);  /* types live as long as their module */
+  for (int i = 0; i < TYPES; i++)
+    if (logit_type[i] == v) return i + 1;
+  return 0;
+}
+
+/* a method's result as an integer (-1: look for an error) */
+static long number(PyObject* t, PyObject* method) {
+  PyObject* v = PyObject_CallMethodNoArgs(t, method);
+  if (!v) return -1;
+  const long n = PyLong_AsLong(v);
+  Py_DECREF(v);
+  return n;
+}
+
+/* whether a 2-tuple of integers was read */
+static int pair_of(PyObject* v, long long* a, long long* b) {
+  const int two = PyTuple_Check(v) && PyTuple_GET_SIZE(v) == 2;
+  if (two) {
+    *a = PyLong_AsLongLong(PyTuple_GET_ITEM(v, 0));
+    *b = PyLong_AsLongLong(PyTuple_GET_ITEM(v, 1));
+  }
+  return two && !PyErr_Occurred();
+}
+
+/* rows(tensor, what, like): (pointer, row stride, rows, columns, type code,
+ * device index) of a 2-D device tensor with contiguous rows; like: None, or
+ * the tuple of a tensor whose shape, type and device it must have. */
+static PyObject* py_rows(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 3) {
+    PyErr_SetString(PyExc_TypeError, "rows(tensor, what, like)");
+    return NULL;
+  }
+  long long rows = 0, cols = 0, ld = 0, step = 0;
+  PyObject* v = PyObject_GetAttr(a[0], s_shape);
+  if (!v) return NULL;
+  int ok = pair_of(v, &rows, &cols);
+  Py_DECREF(v);
+  const long dev = ok ? number(a[0], s_device) : -1;
+  if (PyErr_Occurred()) return NULL;
+  if (dev < 0) return PyErr_Format(PyExc_ValueError, "%S must be a 2-D device tensor", a[1]);
+  if (!(v = PyObject_CallMethodNoArgs(a[0], s_stride))) return NULL;
+  ok = pair_of(v, &ld, &step);
+  Py_DECREF(v);
+  if (PyErr_Occurred()) return NULL;
+  if (!ok || (step != 1 && cols > 1)) return PyErr_Format(PyExc_ValueError, "%S's rows must be contiguous", a[1]);
+  if (rows <= 1) ld = cols;
+  const int code = code_of(a[0]);
+  if (code < 0) return NULL;
+  if (code == 0) {
+    if ((v = PyObject_GetAttr(a[0], s_dtype))) {
+      PyErr_Format(PyExc_ValueError, "unsupported dtype %S", v);
+      Py_DECREF(v);
+    }
+    return NULL;
+  }
+  if (a[2] != Py_None) {
+    if (!PyTuple_Check(a[2]) || PyTuple_GET_SIZE(a[2]) != 6) {
+      PyErr_SetString(PyExc_TypeError, "like: a tuple that rows() returned");
+      return NULL;
+    }
+    ok = PyLong_AsLongLong(PyTuple_GET_ITEM(a[2], 2)) == rows && PyLong_AsLongLong(PyTuple_GET_ITEM(a[2], 3)) == cols &&
+         PyLong_AsLong(PyTuple_GET_ITEM(a[2], 4)) == code && PyLong_AsLong(PyTuple_GET_ITEM(a[2], 5)) == dev;
+    if (PyErr_Occurred()) return NULL;
+    if (!ok) return PyErr_Format(PyExc_ValueError, "%S must have the logits' shape, dtype and device", a[1]);
+  }
+  if (!(v = PyObject_CallMethodNoArgs(a[0], s_data_ptr))) return NULL;
+  return Py_BuildValue("(NLLLil)", v, ld, rows, cols, code, dev);
+}
+
+/* whether a tensor is contiguous, on that device, of that shape and one of
+ * those types; -1 on an error */
+static int fits(PyObject* t, PyObject* const* types, Py_ssize_t ntypes, long dev, const long long* shape,
+                Py_ssize_t dims) {
+  int ok = 0;
+  PyObject* v = PyObject_GetAttr(t, s_dtype);
+  if (!v) return -1;
+  for (Py_ssize_t i = 0; i < ntypes; i++) ok = ok || types[i] == v;
+  Py_DECREF(v);
+  if (!ok) return 0;
+  if (!(v = PyObject_GetAttr(t, s_shape))) return -1;
+  ok = PyTuple_Check(v) && PyTuple_GET_SIZE(v) == dims;
+  for (Py_ssize_t i = 0; ok && i < dims; i++) ok = PyLong_AsLongLong(PyTuple_GET_ITEM(v, i)) == shape[i];
+  Py_DECREF(v);
+  if (PyErr_Occurred()) return -1;
+  if (!ok) return 0;
+  ok = number(t, s_device) == dev;
+  if (PyErr_Occurred()) return -1;
+  if (!ok) return 0;
+  if (!(v = PyObject_CallMethodNoArgs(t, s_contiguous))) return -1;
+  ok = PyObject_IsTrue(v);
+  Py_DECREF(v);
+  return ok;
+}
+
+/* the pointer of a tensor that fits, or an error that says what it must be */
+static PyObject* pointer_of(PyObject* t, PyObject* what, PyObject* const* types, Py_ssize_t ntypes, long dev,
+                            const long long* shape, Py_ssize_t dims) {
+  const int ok = fits(t, types, ntypes, dev, shape, dims);
+  if (ok < 0) return NULL;
+  if (ok) return PyObject_CallMethodNoArgs(t, s_data_ptr);
+  PyObject *of = PyTuple_New(ntypes), *sizes = PyTuple_New(dims);
+  for (Py_ssize_t i = 0; of && i < ntypes; i++) {
+    Py_INCREF(types[i]);
+    PyTuple_SET_ITEM(of, i, types[i]);
+  }
+  for (Py_ssize_t i = 0; sizes && i < dims; i++) {
+    PyObject* d = PyLong_FromLongLong(shape[i]);
+    if (!d) Py_CLEAR(sizes);
+    else PyTuple_SET_ITEM(sizes, i, d);
+  }
+  if (of && sizes)
+    PyErr_Format(PyExc_ValueError, "%S must be a contiguous tensor %R of one of %R on cuda:%ld", what, sizes, of, dev);
+  Py_XDECREF(of);
+  Py_XDECREF(sizes);
+  return NULL;
+}
+
+/* pointer(tensor, what, types, device index, *shape): the data pointer of a
+ * contiguous tensor of that shape and device and one of those types (None
+ * for None). */
+#define DIMS 4
 static PyObject* py_pointer(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
-  if (n < 4 || !PyTuple_Check(a[2])) {
-    PyErr_SetString(PyExc_TypeError, "pointer(tensor, what, dtypes, device, *shape)");
+  if (n < 4 || n > 4 + DIMS || !PyTuple_Check(a[2])) {
+    PyErr_SetString(PyExc_TypeError, "pointer(tensor, what, types, device, *shape)");
     return NULL;
   }
   if (a[0] == Py_None) Py_RETURN_NONE;
-  int ok = 0;
-  PyObject* v = PyObject_GetAttr(a[0], s_dtype);
+  long long shape[DIMS];
+  for (Py_ssize_t i = 4; i < n; i++) shape[i - 4] = PyLong_AsLongLong(a[i]);
+  const long dev = PyLong_AsLong(a[3]);
+  if (PyErr_Occurred()) return NULL;
+  return pointer_of(a[0], a[1], PySequence_Fast_ITEMS(a[2]), PyTuple_GET_SIZE(a[2]), dev, shape, n - 4);
+}
+
+/* slots(ids, teacher, ids' types, rows, device index): (ids pointer, teacher
+ * pointer, the teacher's type code, topk) of contiguous [rows, topk] tensors. */
+static PyObject *s_ids, *s_teacher;
+static PyObject* py_slots(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 5 || !PyTuple_Check(a[2])) {
+    PyErr_SetString(PyExc_TypeError, "slots(ids, teacher, types, rows, device)");
+    return NULL;
+  }
+  long long had = 0, shape[2] = {PyLong_AsLongLong(a[3]), 0};
+  const long dev = PyLong_AsLong(a[4]);
+  if (PyErr_Occurred()) return NULL;
+  PyObject* v = PyObject_GetAttr(a[0], s_shape);
   if (!v) return NULL;
-  for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(a[2]); i++) ok = ok || PyTuple_GET_ITEM(a[2], i) == v;
+  const int ok = pair_of(v, &had, &shape[1]);
   Py_DECREF(v);
-  if (ok) {
-    if (!(v = PyObject_GetAttr(a[0], s_shape))) return NULL;
-    ok = PyTuple_Check(v) && PyTuple_GET_SIZE(v) == n - 4;
-    for (Py_ssize_t i = 4; ok && i < n; i++)
-      ok = PyLong_AsLongLong(PyTuple_GET_ITEM(v, i - 4)) == PyLong_AsLongLong(a[i]);
-    Py_DECREF(v);
-    if (PyErr_Occurred()) return NULL;
+  if (PyErr_Occurred()) return NULL;
+  if (!ok) return PyErr_Format(PyExc_ValueError, "ids must be [rows, topk]");
+  PyObject* ids = pointer_of(a[0], s_ids, PySequence_Fast_ITEMS(a[2]), PyTuple_GET_SIZE(a[2]), dev, shape, 2);
+  if (!ids) return NULL;
+  PyObject* teacher = pointer_of(a[1], s_teacher, logit_type, TYPES, dev, shape, 2);
+  const int code = teacher ? code_of(a[1]) : -1;
+  if (code < 0) {
+    Py_DECREF(ids);
+    Py_XDECREF(teacher);
+    return NULL;
   }
-  if (ok) {
-    if (!(v = PyObject_GetAttr(a[0], s_device))) return NULL;
-    ok = PyObject_RichCompareBool(v, a[3], Py_EQ);
-    Py_DECREF(v);
-    if (ok < 0) return NULL;
-  }
-  if (ok) {
-    if (!(v = PyObject_CallMethodNoArgs(a[0], s_contiguous))) return NULL;
-    ok = PyObject_IsTrue(v);
-    Py_DECREF(v);
-    if (ok < 0) return NULL;
-  }
-  if (ok) return PyObject_CallMethodNoArgs(a[0], s_data_ptr);
-  PyObject* shape = PyTuple_New(n - 4);
-  if (!shape) return NULL;
-  for (Py_ssize_t i = 4; i < n; i++) {
-    Py_INCREF(a[i]);
-    PyTuple_SET_ITEM(shape, i - 4, a[i]);
-  }
-  PyErr_Format(PyExc_ValueError, "%U must be a contiguous tensor %R of one of %R on %S", a[1], shape, a[2], a[3]);
-  Py_DECREF(shape);
-  return NULL;
+  return Py_BuildValue("(NNiL)", ids, teacher, code, shape[1]);
 }
 
 #define METHOD(name, f, doc) {name, (PyCFunction)(void (*)(void))f, METH_FASTCALL, doc}
 static PyMethodDef pycall_methods[] = {
     {"bind", py_bind, METH_VARARGS, "bind(name, address): set an entry point"},
-    METHOD("pointer", py_pointer, "pointer(tensor, what, dtypes, device, *shape): the checked data pointer"),
+    {"types", py_types, METH_VARARGS, "types(fp32, fp16, bf16): set the logit types"},
+    METHOD("rows", py_rows, "rows(tensor, what, like): pointer, row stride, rows, columns, type code, device"),
+    METHOD("pointer", py_pointer, "pointer(tensor, what, types, device, *shape): the checked data pointer"),
+    METHOD("slots", py_slots, "slots(ids, teacher, types, rows, device): pointers, teacher's type code, topk"),
     METHOD("route", py_route, "sim_route"),
     METHOD("route_grad", py_route_grad, "sim_route_grad"),
     METHOD("distill_step", py_distill_step, "sim_distill_step"),
@@ -264,10 +408,13 @@ PyMODINIT_FUNC PyInit__pycall(void) {
   if (PyType_Ready(&PreparedCallType) < 0) return NULL;
   s_dtype = PyUnicode_InternFromString("dtype");
   s_shape = PyUnicode_InternFromString("shape");
-  s_device = PyUnicode_InternFromString("device");
+  s_device = PyUnicode_InternFromString("get_device");
   s_contiguous = PyUnicode_InternFromString("is_contiguous");
   s_data_ptr = PyUnicode_InternFromString("data_ptr");
-  if (!s_dtype || !s_shape || !s_device || !s_contiguous || !s_data_ptr) return NULL;
+  s_stride = PyUnicode_InternFromString("stride");
+  s_ids = PyUnicode_InternFromString("ids");
+  s_teacher = PyUnicode_InternFromString("teacher");
+  if (!s_dtype || !s_shape || !s_device || !s_contiguous || !s_data_ptr || !s_stride || !s_ids || !s_teacher) return NULL;
   PyObject* m = PyModule_Create(&pycall_module);
   if (!m) return NULL;
   Py_INCREF(&PreparedCallType);

@@ -341,3 +341,26 @@ def test_refusals(lib):
     with pytest.raises(lib.SimError):
         lib.distill_step(x, i, z, temperature=0.0)
     torch.cuda.synchronize()
+
+
+def test_both_forms_of_the_tensor_checks_agree(lib):
+    """The checks in C and their Python forms return or refuse the same."""
+    f32, i32 = (torch.float32,), (torch.int32,)
+    x = torch.zeros(6, 40, device="cuda")
+    same = [x, x.half(), x.bfloat16(), x[:, 3:9], x[::2], x[:1], x[:0], x[:, :1], x.t(), x[0], x.int(), x.double(), x.cpu(),
+            x.view(2, 3, 40), x[:, ::2]]
+    ids = torch.zeros(6, 3, dtype=torch.int32, device="cuda")
+    rows = [(t, "t", like) for t in same for like in (None, lib._rows_py(x, "x", None))]
+    vecs = [(t, "t", f32, 0, *shape) for t in same + [None] for shape in ((6, 40), (6,), (2, 3, 40))]
+    slots = [(i, z, i32, n, 0) for i in (ids, ids[:5], ids.long(), ids[0], ids.cpu(), ids[:, :2])
+             for z in (ids.float(), ids.half(), ids, ids[:, :2].float(), ids.float().cpu()) for n in (6, 5)]
+    for c, py, calls in ((lib._rows, lib._rows_py, rows), (lib._vec, lib._vec_py, vecs), (lib._slots, lib._slots_py, slots)):
+        assert c is not py
+        for args in calls:
+            got = []
+            for f in (c, py):
+                try:
+                    got.append(f(*args))
+                except ValueError:
+                    got.append("refused")
+            assert got[0] == got[1], args
