@@ -107,8 +107,7 @@ __device__ __forceinline__ int64_t part_index(int64_t part, int which, int64_t r
 // A row's slots as the threads of a workgroup of NT use them.  Slot k hangs on
 // the thread that holds its column (list head[thread], then next[k]); after
 // its vectors a thread writes the full values of its slots' columns.  Its own
-// stores to one address stay in order, so no barrier is needed in between,
-// and slots with the same id write the same value.
+// stores to one address stay in order, so no barrier is needed in between.
 template <int NT>
 struct SlotLists {
   int head[NT];
@@ -142,8 +141,9 @@ __device__ __forceinline__ uint32_t lone_columns(const void* row) {
   return Ty<DT>::E == 2 ? (uint32_t)((uintptr_t)row >> 1) & 1u : 0u;
 }
 // Wave 0, once the row's maximum and its sum against `top` are known: each
-// slot's probability, and its place in its thread's list.  `base`: the first
-// vector's column (the column before it is thread 0's).
+// slot's probability, and its place in its thread's list (a slot of q = 0
+// changes nothing of its column).  `base`: the first vector's column (the
+// column before it is thread 0's).
 template <int DT, int NT>
 __device__ __forceinline__ void hang_slots(const DistillArgs& a, SlotLists<NT>& s, const Slots& sl, int64_t lo,
                                            int64_t hi, int64_t base, const Against& top, float sum, int lane) {
@@ -152,27 +152,48 @@ __device__ __forceinline__ void hang_slots(const DistillArgs& a, SlotLists<NT>& 
     if (64 * i >= a.topk) break;
     const int k = lane + 64 * i;
     const int64_t col = (int64_t)sl.id[i] - a.first;
-    if (!sl.live || sl.id[i] < 0 || col < lo || col >= hi) continue;
+    if (!sl.live || sl.id[i] < 0 || sl.q[i] == 0.0f || col < lo || col >= hi) continue;
     s.x[k] = exp_against(s.x[k], top) / sum;
     s.next[k] = atomicExch(&s.head[col < base ? 0 : (col - base) / epv<DT>() % NT], k);
   }
 }
 // Each slot's column gets up (p - the sum of q over the slots with its id).
 // Slots with one id hang on one thread, so it sees in its own list, whose
-// order depends on timing, whether there are others; then it adds them in
-// the order of the slots.
+// order depends on timing, whether there are others; the first of them then
+// adds them in the order of the slots (79 rows x 2,263 with 101 slots, some
+// of one id: 14.9 us; every slot adding, one load after the other: 27.4).
 template <int DT, int NT>
 __device__ __forceinline__ void write_slots(const DistillArgs& a, const SlotLists<NT>& s, void* dx, float up, int tid) {
-  for (int k = s.head[tid]; k >= 0; k = s.next[k]) {
+  const int head = s.head[tid];
+  for (int k = head; k >= 0; k = s.next[k]) {
+    const int id = s.id[k];
+    bool more = false, first = true;
+    auto other = [&](int j) {
+      if (s.id[j] != id) return;
+      more = true;
+      first = j > k;
+    };
+    for (int j = s.next[k]; j >= 0 && first; j = s.next[j]) other(j);
+    for (int j = head; j != k && first; j = s.next[j]) other(j);
+    if (!first) continue;
     float q = s.q[k];
-    bool more = false;
-    for (int j = s.head[tid]; j >= 0; j = s.next[j]) more = more || (j != k && s.id[j] == s.id[k]);
     if (more) {
       q = 0.0f;
-      for (int j = 0; j < a.topk; j++)
-        if (s.id[j] == s.id[k]) q += s.q[j];
+      constexpr int N = 8;  // a batch of loads at a time
+      for (int j0 = 0; j0 < a.topk; j0 += N) {
+        int ids[N];
+        float qs[N];
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+          ids[j] = s.id[j0 + j];
+          qs[j] = s.q[j0 + j];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < N; j++) q += j0 + j < a.topk && ids[j] == id ? qs[j] : 0.0f;
+      }
     }
-    store_elem<DT>(dx, (int64_t)s.id[k] - a.first, up * (s.x[k] - q));
+    store_elem<DT>(dx, (int64_t)id - a.first, up * (s.x[k] - q));
   }
 }
 
