@@ -207,7 +207,7 @@ __device__ __forceinline__ void top8(const Gate<DT, L, N>& g, int l, uint32_t li
   for (int i = 0; i < 8; i++) top[i] |= mine;
   merge8(top, [](uint32_t k, int) { return dpp<kDppPair>(k); });
   merge8(top, [](uint32_t k, int) { return dpp<kDppQuad>(k); });
-  merge8(top, [](uint32_t k, int) { return dpp<kDppHalfRow>(k); });
+  if constexpr (L >= 8) merge8(top, [](uint32_t k, int) { return dpp<kDppHalfRow>(k); });
   if constexpr (L >= 16) merge8(top, [](uint32_t k, int) { return dpp<kDppRow>(k); });
   // every lane keeps its own row's (half's) eight and takes the other's
   if constexpr (L >= 32) merge8(top, [](uint32_t k, int) { return from_other<16>(k); });
@@ -308,7 +308,8 @@ __device__ __forceinline__ void sum_in_last(const RouteArgs& a, uint32_t* word_s
 template <int DT, int L, int N, bool MANY>
 __global__ void __launch_bounds__(kBlock, N == 32 ? 3 : 4) k_route(RouteArgs a) {
   typedef Gate<DT, L, N> G;
-  constexpr int S = MANY ? (SIM_ROUTE_MAX_TOPK + L - 1) / L : 1;
+  constexpr int TAKE = L < 8 ? 8 / L : 1;  // slots of a round that a lane may get
+  constexpr int S = MANY ? (SIM_ROUTE_MAX_TOPK + L - 1) / L : TAKE;
   __shared__ uint32_t count_s[G::kAll + 1];
   __shared__ float sum_s[kWaves * G::kRows][G::kAll];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l = lane & (L - 1);
@@ -366,15 +367,19 @@ __global__ void __launch_bounds__(kBlock, N == 32 ? 3 : 4) k_route(RouteArgs a) 
       }
       // slot done + i goes to lane (done + i) mod L
       const int i0 = MANY ? (l - done) & (L - 1) : l;
-      uint32_t k = top[0];
 #pragma unroll
-      for (int i = 1; i < 8; i++) k = i0 == i ? top[i] : k;
-      const bool ok = i0 < 8 && done + i0 < a.topk && (k & m) > (ordered_neg_inf<DT>() & m);
+      for (int u = 0; u < TAKE; u++) {
+        const int at_i = i0 + u * L;
+        uint32_t k = top[0];
 #pragma unroll
-      for (int s = 0; s < S; s++) {
-        if (!MANY || (ok && (done + i0) / L == s)) {
-          mine[s] = ok ? G::kAll - 1 - (int)(k & (uint32_t)(G::kAll - 1)) : -1;
-          if constexpr (Ty<DT>::E == 2) at[s] = from_ordered16<DT>(k);
+        for (int i = 1; i < 8; i++) k = at_i == i ? top[i] : k;
+        const bool ok = at_i < 8 && done + at_i < a.topk && (k & m) > (ordered_neg_inf<DT>() & m);
+#pragma unroll
+        for (int s = 0; s < S; s++) {
+          if (MANY ? ok && (done + at_i) / L == s : s == u) {
+            mine[s] = ok ? G::kAll - 1 - (int)(k & (uint32_t)(G::kAll - 1)) : -1;
+            if constexpr (Ty<DT>::E == 2) at[s] = from_ordered16<DT>(k);
+          }
         }
       }
       if (!MANY) break;
@@ -635,6 +640,7 @@ template <int DT, bool MANY>
 hipError_t route_layout(const RouteArgs& a, hipStream_t s) {
   constexpr int N = Ty<DT>::E == 2 ? 32 : 16;
   const dim3 grid(a.workgroups), block(kBlock);
+  if (a.experts <= 32) return launch<k_route<DT, 4, 8, MANY>>(grid, block, s, a);
   if (a.experts <= 64) return launch<k_route<DT, 8, 8, MANY>>(grid, block, s, a);
   if (a.experts <= 128) return launch<k_route<DT, 8, 16, MANY>>(grid, block, s, a);
   if (a.experts <= 256) return launch<k_route<DT, 256 / N, N, MANY>>(grid, block, s, a);
@@ -647,8 +653,9 @@ hipError_t route_dtype(const RouteArgs& a, hipStream_t s) {
 }
 template <int DT>
 hipError_t grad_dtype(const RouteGradArgs& a, hipStream_t s) {
-  const int rows = a.experts <= 128 ? 8 : a.experts <= 256 ? 4 : a.experts <= 512 ? 2 : 1;
+  const int rows = a.experts <= 32 ? 16 : a.experts <= 128 ? 8 : a.experts <= 256 ? 4 : a.experts <= 512 ? 2 : 1;
   const dim3 grid((unsigned)even_workgroups(a.tokens, kWaves * rows, 4 * (int64_t)library_cus())), block(kBlock);
+  if (a.experts <= 32) return launch<k_route_grad<DT, 4, 8>>(grid, block, s, a);
   if (a.experts <= 64) return launch<k_route_grad<DT, 8, 8>>(grid, block, s, a);
   if (a.experts <= 128) return launch<k_route_grad<DT, 8, 16>>(grid, block, s, a);
   if (a.experts <= 256) return launch<k_route_grad<DT, 16, 16>>(grid, block, s, a);
@@ -660,7 +667,7 @@ hipError_t grad_dtype(const RouteGradArgs& a, hipStream_t s) {
 
 int route_workgroups(int64_t tokens, int experts, int dtype) {
   const int n = dtype == SIM_FP32 ? 16 : 32;
-  const int rows = experts <= 128 ? 8 : 64 * n / (experts <= 256 ? 256 : experts <= 512 ? 512 : 1024);
+  const int rows = experts <= 32 ? 16 : experts <= 128 ? 8 : 64 * n / (experts <= 256 ? 256 : experts <= 512 ? 512 : 1024);
   const int64_t wg = even_workgroups(tokens, kWaves * rows, (n == 32 && experts > 128 ? 2 : 4) * (int64_t)library_cus());
   return (int)(wg < 3 ? 1 : wg);
 }

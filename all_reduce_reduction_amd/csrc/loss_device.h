@@ -182,7 +182,7 @@ template <int L, class T, class F>
 __device__ __forceinline__ T group_reduce(T v, F f) {
   v = f(v, dpp<kDppPair>(v));
   v = f(v, dpp<kDppQuad>(v));
-  v = f(v, dpp<kDppHalfRow>(v));
+  if constexpr (L >= 8) v = f(v, dpp<kDppHalfRow>(v));
   if constexpr (L >= 16) v = f(v, dpp<kDppRow>(v));
   if constexpr (L >= 32) v = across_rows(v, f);
   if constexpr (L >= 64) v = across_halves(v, f);
