@@ -174,7 +174,10 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
 //   - fewer rows than compute units: the largest workgroup, as a row's own time
 //     counts (256 rows x 32,768: 1024 threads 11.8, 256 threads 18.3);
 //   - rows of up to 32 KiB, any number: cached accesses, small workgroups
-//     (32,768 x 8,192: 193, streaming 264);
+//     (32,768 x 8,192: 193, streaming 264), of one wave up to 8 KiB, as a
+//     row's steps wait for each other and more rows are then under way
+//     (16,384 x 2,560: 38.5, 256 threads 54; 8,192 x 8,000 in 64 threads of
+//     16 vectors 54.7, in 256 50.2);
 //   - longer rows, less than 512 MiB of them: streaming accesses and the
 //     smallest workgroup that holds a row in 16 vectors per thread, so that
 //     several share a compute unit and one reads while another computes or
@@ -205,7 +208,7 @@ hipError_t launch_row(const DistillArgs& a, hipStream_t s) {
   const bool few = a.rows <= library_cus();
   if (n <= 2048) {
     if (few && n > 512) return launch_row_with<DT, 1024, false, 1, 2>(a, n, s);
-    if (!few && n <= 256) return launch_row_with<DT, 64, false, 1, 4>(a, n, s);
+    if (!few && n <= 512) return launch_row_with<DT, 64, false, 1, 8>(a, n, s);
     return launch_row_with<DT, 256, false, 1, 8>(a, n, s);
   }
   if (!few && a.rows * a.cols * Ty<DT>::E >= ((int64_t)512 << 20))
