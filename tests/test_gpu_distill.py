@@ -364,3 +364,36 @@ def test_both_forms_of_the_tensor_checks_agree(lib):
                 except ValueError:
                     got.append("refused")
             assert got[0] == got[1], args
+
+
+@pytest.mark.parametrize("t", [40, 300])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_step_row_lengths(lib, dtype, t):
+    """Every number of vectors per thread that small rows are held in, one column before it, at it and after it."""
+    vec = 16 // dtype.itemsize
+    lengths = sorted({threads * r * vec + d for threads in (64, 256, 1024) for r in range(1, 9)
+                      if threads * r <= 2048 for d in (-1, 0, 1)})
+    for v in lengths:
+        x, ids, z, scale = case(4, v, 10, dtype, torch.float32, v)
+        pick = (torch.arange(t) % 4).cuda()
+        loss, d = lib.distill_step(x.cuda()[pick], ids.cuda()[pick], z.cuda()[pick], coef=64.0)
+        check(x, ids, z, 1.0, None, 64.0, loss[:4], d[:4], "%d columns" % v)
+        assert torch.equal(d.view(-1, 4, v), d[:4].expand(t // 4, 4, v)), v
+
+
+@pytest.mark.parametrize("t,v", [(3, 70), (300, 3001), (2, 140001)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_many_slots_with_one_id(lib, dtype, t, v):
+    """Rows of one id alone, of a few ids many times, and padded with one id of no mass."""
+    k = 200
+    x, ids, z, scale = case(t, v, k, dtype, torch.float32, 5, holes=False)
+    ids[0] = v // 2
+    ids[1] = torch.arange(k, dtype=torch.int32) % 3 * (v // 4)
+    ids[-1, 20:] = 0
+    z[-1, 20:] = -INF
+    loss, d = step(lib, x, ids, z, 2.0, scale, 64.0)
+    check(x, ids, z, 2.0, scale, 64.0, loss, d)
+    again = step(lib, x, ids, z, 2.0, scale, 64.0)
+    assert torch.equal(again[0], loss) and torch.equal(again[1], d)
+    loss, d, _ = shards(lib, x, ids, z, 2.0, scale, 64.0, 2)
+    check(x, ids, z, 2.0, scale, 64.0, loss, d)
