@@ -27,7 +27,7 @@ namespace {
 // different runs meet in memory (4,096 x 50,021 bf16: 145 us; with eight 157,
 // with two 155).
 constexpr int kHeld = 4;
-template <int DT> constexpr uint32_t chunk_cols() { return kHeld * kBlock * epv<DT>(); }
+template <int DT, int B> constexpr uint32_t chunk_cols() { return kHeld * B * epv<DT>(); }
 // `lone`: column 0 by itself before lo, thread 0's (see lone_columns).
 struct Columns {
   uint32_t lo, hi, cols;
@@ -42,48 +42,48 @@ __device__ __forceinline__ Columns columns_of(const DistillArgs& a, const void* 
 }
 // (a thread's place is worked out at each use: kept for all vectors of a chunk,
 // it would take more registers than the vectors)
-template <int DT>
+template <int DT, int B>
 __device__ __forceinline__ Tail<DT> tail(uint32_t col, int i, int tid, const Columns& r) {
   constexpr int V = epv<DT>();
-  return Tail<DT>(col + i * kBlock * V + lane_offset(tid * V), r.hi, r.cols);
+  return Tail<DT>(col + i * B * V + lane_offset(tid * V), r.hi, r.cols);
 }
-template <int DT, bool WHOLE, bool TINY>
+template <int DT, int B, bool WHOLE, bool TINY>
 __device__ __forceinline__ void load_chunk(const void* x, uint32_t col, int tid, const Columns& r,
                                            u32x4 (&v)[kHeld]) {
   constexpr int V = epv<DT>();
 #pragma unroll
   for (int i = 0; i < kHeld; i++) {
-    if constexpr (TINY) v[i] = ld_guarded<DT>(x, (i * kBlock + tid) * V, r.cols);
-    else if constexpr (WHOLE) v[i] = ld_row_lane<DT, true>(x, col + i * kBlock * V, tid * V);
-    else v[i] = tail<DT>(col, i, tid, r).load(x);
+    if constexpr (TINY) v[i] = ld_guarded<DT>(x, (i * B + tid) * V, r.cols);
+    else if constexpr (WHOLE) v[i] = ld_row_lane<DT, true>(x, col + i * B * V, tid * V);
+    else v[i] = tail<DT, B>(col, i, tid, r).load(x);
   }
 }
 // All chunks: load, `first` behind the first loads, use(v, col, whole).  A
 // last chunk of one vector per thread or less is asked for with the first, so
 // that it costs no wait of its own.
-template <int DT, bool TINY, class First, class Use>
+template <int DT, int B, bool TINY, class First, class Use>
 __device__ __forceinline__ void each_chunk(const void* x, int tid, const Columns& r, First first, Use use) {
-  constexpr uint32_t chunk = chunk_cols<DT>();
+  constexpr uint32_t chunk = chunk_cols<DT, B>();
   uint32_t col = r.lo;
   u32x4 v[kHeld];
   if (!TINY && col + chunk <= r.hi) {
     const uint32_t last = r.hi - (r.hi - r.lo) % chunk;
-    load_chunk<DT, true, false>(x, col, tid, r, v);
-    u32x4 few[1] = {tail<DT>(last, 0, tid, r).load(x)};
+    load_chunk<DT, B, true, false>(x, col, tid, r, v);
+    u32x4 few[1] = {tail<DT, B>(last, 0, tid, r).load(x)};
     first();
     use(v, col, std::true_type());
 #pragma unroll 1
     for (col += chunk; col < last; col += chunk) {
-      load_chunk<DT, true, false>(x, col, tid, r, v);
+      load_chunk<DT, B, true, false>(x, col, tid, r, v);
       use(v, col, std::true_type());
     }
-    if (last + kBlock * epv<DT>() >= r.hi) {
+    if (last + B * epv<DT>() >= r.hi) {
       use(few, last, std::false_type());
       return;
     }
-    load_chunk<DT, false, TINY>(x, last, tid, r, v);
+    load_chunk<DT, B, false, TINY>(x, last, tid, r, v);
   } else {
-    load_chunk<DT, false, TINY>(x, col, tid, r, v);
+    load_chunk<DT, B, false, TINY>(x, col, tid, r, v);
     first();
   }
   use(v, col, std::false_type());
@@ -92,9 +92,9 @@ __device__ __forceinline__ void each_chunk(const void* x, int tid, const Columns
 // Bound by the read: 24 to 27 us for 4,096 rows x 16,384 bf16 (5.0 to 5.6 TB/s),
 // 67 us for 4,096 x 50,021 (6.1 TB/s).  Workgroups of 256 threads, as many of
 // them share a compute unit (512 threads: 47 us for 4,096 x 16,385 against 30).
-template <int DT, bool TINY>
-__global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
-  constexpr int V = epv<DT>(), W = kBlock / 64;
+template <int DT, int B, bool TINY>
+__global__ void __launch_bounds__(B) k_distill_stats(DistillArgs a) {
+  constexpr int V = epv<DT>(), W = B / 64;
   __shared__ float m_s[W], s_s[W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
   float at[kSlotsPerLane];
   Scan scan;
   const float alone = range.lone && tid == 0 ? load_elem<DT>(x, 0) : kNegInf;
-  each_chunk<DT, TINY>(
+  each_chunk<DT, B, TINY>(
       x, tid, range,
       [&]() __attribute__((always_inline)) {
         if (wave != 0) return;
@@ -127,10 +127,10 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
       [&](auto& v, uint32_t col, auto whole) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < (int)(sizeof v / sizeof v[0]); i++) {
-          if (!whole() && col + i * kBlock * V >= range.hi) break;
+          if (!whole() && col + i * B * V >= range.hi) break;
           float f[V];
           unpack<DT>(v[i], f);
-          if (!whole() && !TINY && col + (i + 1) * kBlock * V > range.hi) tail<DT>(col, i, tid, range).mask(f);
+          if (!whole() && !TINY && col + (i + 1) * B * V > range.hi) tail<DT, B>(col, i, tid, range).mask(f);
           scan.add(f, c);
         }
       });
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_stats(DistillArgs a) {
   r = wave_running(r, c);
   if (__builtin_expect(far(r.m, c), 0)) {
     float top = alone == r.m ? 1.0f : 0.0f;
-    for (int64_t col = range.lo + tid * V; col < range.hi; col += kBlock * V) {
+    for (int64_t col = range.lo + tid * V; col < range.hi; col += B * V) {
       float f[V];
       load_cols<DT>(x, col, range.hi, f);
       top += count_of(f, r.m);
@@ -208,10 +208,10 @@ __global__ void __launch_bounds__(kBlock) k_distill_merge(DistillArgs a, float* 
 // The gradient of a run of columns, from the row's joined parts or its norm.
 // Bound by reading and writing at once: 48 us for 4,096 rows x 16,384 bf16 (5.5
 // TB/s; a copy of as many bytes 42).
-template <int DT, bool TINY>
-__global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
+template <int DT, int B, bool TINY>
+__global__ void __launch_bounds__(B) k_distill_grad(DistillArgs a) {
   constexpr int V = epv<DT>();
-  __shared__ SlotLists<kBlock> slots;
+  __shared__ SlotLists<B> slots;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
   const void* x = row_at(a.x, row, a.stride, Ty<DT>::E);
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
   const SlotLoads asked = ask_slots(a, row, lane, wave == 0);
   if (a.look_first && !has_slots(a, asked)) {
     const float f[V] = {};
-    for (uint32_t col = range.lo + tid * V; col < range.hi; col += kBlock * V) st_guarded<DT>(dx, col, range.hi, f);
+    for (uint32_t col = range.lo + tid * V; col < range.hi; col += B * V) st_guarded<DT>(dx, col, range.hi, f);
     if (range.lone && tid == 0) store_elem<DT>(dx, 0, 0.0f);
     if (a.loss && split == 0 && tid == 0) a.loss[row] = 0.0f;
     return;
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
   const float k2 = up / sum;
   bool live = true;
   const float alone = range.lone && tid == 0 ? load_elem<DT>(x, 0) : kNegInf;
-  each_chunk<DT, TINY>(
+  each_chunk<DT, B, TINY>(
       x, tid, range,
       [&]() __attribute__((always_inline)) {
         __syncthreads();
@@ -257,15 +257,15 @@ __global__ void __launch_bounds__(kBlock) k_distill_grad(DistillArgs a) {
       [&](auto& v, uint32_t col, auto whole) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < (int)(sizeof v / sizeof v[0]); i++) {
-          if (!whole() && col + i * kBlock * V >= range.hi) break;
+          if (!whole() && col + i * B * V >= range.hi) break;
           float f[V];
           unpack<DT>(v[i], f);
           // (0 * p would keep the NaN of a row that does not count)
 #pragma unroll
           for (int j = 0; j < V; j++) f[j] = live ? exp_against(f[j], top) * k2 : 0.0f;
-          if (whole()) st_row_lane<DT, true>(dx, col + i * kBlock * V, tid * V, pack_rounded<DT>(f));
-          else if (!TINY) tail<DT>(col, i, tid, range).store(dx, f);
-          else st_guarded<DT>(dx, (i * kBlock + tid) * V, range.cols, f);
+          if (whole()) st_row_lane<DT, true>(dx, col + i * B * V, tid * V, pack_rounded<DT>(f));
+          else if (!TINY) tail<DT, B>(col, i, tid, range).store(dx, f);
+          else st_guarded<DT>(dx, (i * B + tid) * V, range.cols, f);
         }
       });
   if (range.lone && tid == 0) store_elem<DT>(dx, 0, live ? exp_against(alone, top) * k2 : 0.0f);
@@ -291,12 +291,30 @@ int64_t distill_span(int64_t cols, int splits) {
   return (v + 7) / 8 * 8;
 }
 
-#define BY_DTYPE(K, ...)                                                                              \
-  switch (dtype) {                                                                                    \
-    case SIM_FP32: return a.cols <= 4 ? launch<K<SIM_FP32, true>>(__VA_ARGS__) : launch<K<SIM_FP32, false>>(__VA_ARGS__); \
-    case SIM_FP16: return a.cols <= 8 ? launch<K<SIM_FP16, true>>(__VA_ARGS__) : launch<K<SIM_FP16, false>>(__VA_ARGS__); \
-    default: return a.cols <= 8 ? launch<K<SIM_BF16, true>>(__VA_ARGS__) : launch<K<SIM_BF16, false>>(__VA_ARGS__);       \
-  }
+// Many short runs, of at most `chunks` chunks of one wave, take a workgroup of
+// one wave each: a run's steps wait for each other, and more runs are then under
+// way (8,192 rows x 1,000 bf16: statistics 8.8 us, gradient 11.7; 256 threads
+// 19.5 and 21.2).  A run that is only read pays longer (8,192 x 8,192: 25.9, 256
+// threads 32.5; 4,096 x 16,384: 25.7 and 26.2) than one that is written too
+// (4,096 x 8,192: 27.1 and 25.7).
+template <int DT>
+bool one_wave(const DistillArgs& a, int chunks) {
+  return a.span <= chunks * (int64_t)chunk_cols<DT, 64>() && a.rows * a.splits >= 4 * (int64_t)library_cus();
+}
+template <int DT>
+hipError_t stats_dtype(const DistillArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)(a.rows * a.splits));
+  if (a.cols <= epv<DT>()) return launch<k_distill_stats<DT, 64, true>>(grid, dim3(64), s, a);
+  if (one_wave<DT>(a, 8)) return launch<k_distill_stats<DT, 64, false>>(grid, dim3(64), s, a);
+  return launch<k_distill_stats<DT, kBlock, false>>(grid, dim3(kBlock), s, a);
+}
+template <int DT>
+hipError_t grad_dtype(const DistillArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)(a.rows * a.splits));
+  if (a.cols <= epv<DT>()) return launch<k_distill_grad<DT, 64, true>>(grid, dim3(64), s, a);
+  if (one_wave<DT>(a, 2)) return launch<k_distill_grad<DT, 64, false>>(grid, dim3(64), s, a);
+  return launch<k_distill_grad<DT, kBlock, false>>(grid, dim3(kBlock), s, a);
+}
 
 // Whether a workgroup waits for the slots before it reads its columns, to
 // leave out rows without any: where eight or more workgroups share a compute
@@ -308,13 +326,13 @@ DistillArgs with_look(const DistillArgs& in) {
 }
 hipError_t launch_distill_stats(const DistillArgs& in, int dtype, hipStream_t s) {
   const DistillArgs a = with_look(in);
-  const dim3 grid((unsigned)(a.rows * a.splits)), block(kBlock);
-  BY_DTYPE(k_distill_stats, grid, block, s, a)
+  if (dtype == SIM_FP32) return stats_dtype<SIM_FP32>(a, s);
+  return dtype == SIM_FP16 ? stats_dtype<SIM_FP16>(a, s) : stats_dtype<SIM_BF16>(a, s);
 }
 hipError_t launch_distill_grad(const DistillArgs& in, int dtype, hipStream_t s) {
   const DistillArgs a = with_look(in);
-  const dim3 grid((unsigned)(a.rows * a.splits)), block(kBlock);
-  BY_DTYPE(k_distill_grad, grid, block, s, a)
+  if (dtype == SIM_FP32) return grad_dtype<SIM_FP32>(a, s);
+  return dtype == SIM_FP16 ? grad_dtype<SIM_FP16>(a, s) : grad_dtype<SIM_BF16>(a, s);
 }
 hipError_t launch_distill_join(const DistillArgs& a, float* loss, float* norm, hipStream_t s) {
   return launch<k_distill_join>(dim3((unsigned)((a.rows + 3) / 4)), dim3(kBlock), s, a, loss, norm);

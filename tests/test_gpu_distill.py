@@ -397,3 +397,17 @@ def test_many_slots_with_one_id(lib, dtype, t, v):
     assert torch.equal(again[0], loss) and torch.equal(again[1], d)
     loss, d, _ = shards(lib, x, ids, z, 2.0, scale, 64.0, 2)
     check(x, ids, z, 2.0, scale, 64.0, loss, d)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_shards_of_many_rows(lib, dtype):
+    """Short runs of many rows: around every number of chunks of a wave, with odd starts of rows too."""
+    t, vec = 1040, 16 // dtype.itemsize
+    for n in (1, 2, 8):
+        for d in (-1, 0, 1, 33):
+            v = 256 * vec * n + d
+            x, ids, z, scale = case(8, v, 12, dtype, torch.float32, v)
+            pick = torch.arange(t) % 8
+            loss, grad, _ = shards(lib, x[pick], ids[pick], z[pick], 1.5, None, 64.0, 2 if d == 33 else 1)
+            check(x, ids, z, 1.5, None, 64.0, loss[:8], grad[:8], "%d columns" % v)
+            assert torch.equal(grad.view(-1, 8, v), grad[:8].expand(t // 8, 8, v)), v
