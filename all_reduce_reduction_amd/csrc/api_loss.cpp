@@ -80,9 +80,10 @@ int check_distill(int64_t rows, int64_t cols, int64_t stride, int dtype, int64_t
 
 // Least columns per workgroup where a row is split.  A shard's parts need one
 // more launch to merge splits, so a row's statistics are split no finer than
-// 32 KiB; a gradient and a step's two launches, which need none, split down to
-// 8 KiB.
-int64_t stats_least(int dtype) { return (32 << 10) / size_of(dtype); }
+// 256 KiB (64 rows x 32,768 bf16 whole 5.2 us, in two 9.1; 400 rows x 131,072
+// whole 20.7, in two 24.2); a gradient and a step's two launches, which need
+// none, split down to 8 KiB.
+int64_t stats_least(int dtype) { return (256 << 10) / size_of(dtype); }
 int64_t grad_least(int dtype) { return (8 << 10) / size_of(dtype); }
 // A gradient's workgroup takes one chunk of 16 KiB at most: with more, its
 // loads would wait for its stores (1,024 rows x 65,536 bf16: 97 us in four

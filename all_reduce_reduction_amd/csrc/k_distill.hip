@@ -90,8 +90,9 @@ __device__ __forceinline__ void each_chunk(const void* x, int tid, const Columns
 }
 
 // Bound by the read: 24 to 27 us for 4,096 rows x 16,384 bf16 (5.0 to 5.6 TB/s),
-// 67 us for 4,096 x 50,021 (6.1 TB/s).  Workgroups of 256 threads, as many of
-// them share a compute unit (512 threads: 47 us for 4,096 x 16,385 against 30).
+// 67 us for 4,096 x 50,021 (6.1 TB/s).  Workgroups of B threads: 256, as many of
+// them share a compute unit (512: 47 us for 4,096 x 16,385 against 30), unless
+// the rows are few or short (see stats_dtype).
 template <int DT, int B, bool TINY>
 __global__ void __launch_bounds__(B) k_distill_stats(DistillArgs a) {
   constexpr int V = epv<DT>(), W = B / 64;
@@ -306,6 +307,14 @@ hipError_t stats_dtype(const DistillArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)(a.rows * a.splits));
   if (a.cols <= epv<DT>()) return launch<k_distill_stats<DT, 64, true>>(grid, dim3(64), s, a);
   if (one_wave<DT>(a, 8)) return launch<k_distill_stats<DT, 64, false>>(grid, dim3(64), s, a);
+  // Few rows of more than a chunk: workgroups as wide as they can all be under
+  // way at once, so that a row takes fewer waits in a row (64 rows x 32,768
+  // bf16: 5.2 us; two splits of 256 threads and a launch to merge them 9.1).
+  const int64_t n = a.rows * a.splits, cus = library_cus();
+  if (n <= cus && a.span > chunk_cols<DT, 512>())
+    return launch<k_distill_stats<DT, 1024, false>>(grid, dim3(1024), s, a);
+  if (n <= 2 * cus && a.span > chunk_cols<DT, kBlock>())
+    return launch<k_distill_stats<DT, 512, false>>(grid, dim3(512), s, a);
   return launch<k_distill_stats<DT, kBlock, false>>(grid, dim3(kBlock), s, a);
 }
 template <int DT>
