@@ -17,7 +17,7 @@
 // 16-byte vectors, vector j of lane l being the row's vector j L + l, so that
 // a group's loads cover whole lines.  With many rows per wave the cross-lane
 // steps of one row (log2 L of them) serve 64 / L rows at once, and they run
-// over DPP while L is 8 or 16.
+// over DPP while L is at most 16.
 #include "device_sync.h"
 #include "launch.h"
 #include "loss.h"
