@@ -115,6 +115,9 @@ template <int DT> constexpr uint32_t ordered_inf() {
 template <int DT> constexpr uint32_t ordered_neg_inf() {
   return DT == SIM_FP32 ? 0x007fffffu : DT == SIM_FP16 ? 0x04000000u : 0x00800000u;
 }
+__device__ __forceinline__ float from_ordered32(uint32_t key) {
+  return __builtin_bit_cast(float, key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
 template <int DT>
 __device__ __forceinline__ float from_ordered16(uint32_t key) {
   const uint32_t h = key >> 16;
@@ -387,9 +390,15 @@ __global__ void __launch_bounds__(kBlock, N == 32 ? 3 : 4) k_route(RouteArgs a) 
     g.renew();
     if constexpr (Ty<DT>::E == 4) {
       odd_key = odd_key || (last & m) <= (ordered_neg_inf<DT>() & m);
+      // (values compare like their keys, and as values they need not be made
+      // into keys again; a NaN counts as none here and as odd above)
+      const float least = from_ordered32(last & m);
       float n = 0.0f;
 #pragma unroll
-      for (int i = 0; i < N; i++) n += ordered<DT>(g.v[i / G::V][i % G::V]) >= (last & m) ? 1.0f : 0.0f;
+      for (int i = 0; i < N; i++) {
+        const uint32_t bits = g.v[i / G::V][i % G::V];
+        n += __builtin_bit_cast(float, bits) >= least ? 1.0f : 0.0f;
+      }
       odd_key = odd_key || group_sum<L>(n) != (float)a.topk;
     }
     const bool in_turn = __any(odd_key && kept);
