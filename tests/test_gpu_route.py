@@ -328,3 +328,16 @@ def test_more_streams_than_counters(lib):
         for s in raw:
             hip.hipStreamDestroy(s)
     assert all(torch.equal(a, b) for o in out for a, b in zip(o, want))
+
+
+@pytest.mark.parametrize("e,k", [(16, 5), (32, 32), (60, 8), (128, 20), (256, 8), (500, 16), (1000, 32)])
+def test_fp32_logits_a_bit_apart(lib, e, k):
+    """Neighbouring values, of either sign and below the smallest normal number, are told apart to the last bit."""
+    g = torch.Generator().manual_seed(e)
+    order = torch.rand(200, e, generator=g).argsort(1).float()
+    x = 1.0 + order * 2.0 ** -23
+    x[50:100] = -1.0 - order[50:100] * 2.0 ** -23
+    x[100:150] = (order[100:150] - e // 2) * 2.0 ** -149
+    x[150:] = torch.where(order[150:] < e // 2, 2.0 * order[150:] / e, x[150:])
+    check_route(lib, x, k, None, True)
+    check_route(lib, x, k, None, False)
