@@ -411,18 +411,12 @@ __global__ void __launch_bounds__(kBlock, N == 32 ? 3 : 4) k_route(RouteArgs a) 
     // the softmax
     float f[N];
     g.logits(f);
-    bool odd = false;
     if (Ty<DT>::E == 4 || in_turn) {
       top_logit = kNegInf;
 #pragma unroll
       for (int i = 0; i < N; i++) top_logit = fmaxf(top_logit, f[i]);
       top_logit = group_max<L>(top_logit);
-      // a row of NaN and -inf alone is not empty
-#pragma unroll
-      for (int i = 0; i < N; i++) odd = odd || f[i] != f[i];
-      odd = group_any<L>(odd, lane);
     }
-    const bool live = odd || top_logit > kNegInf;
     const Against base = against(top_logit, kLog2e);
     float z = 0.0f;
 #pragma unroll
@@ -431,6 +425,10 @@ __global__ void __launch_bounds__(kBlock, N == 32 ? 3 : 4) k_route(RouteArgs a) 
       z += f[i];
     }
     z = group_sum<L>(z);
+    // Only a row of -inf alone sums to 0: the largest logit's own term is 2^-56
+    // or more, and a NaN makes the sum one.  (The keys do not tell an empty row:
+    // NaN with the sign set lies below -inf.)
+    const bool live = z != 0.0f;
     const float inv = live ? 1.0f / z : 0.0f;
 #pragma unroll
     for (int i = 0; i < N; i++) sums[i] = __builtin_fmaf(f[i], inv, sums[i]);

@@ -198,10 +198,6 @@ __device__ __forceinline__ float group_max(float v) {
 }
 __device__ __forceinline__ float wave_sum(float v) { return group_sum<64>(v); }
 __device__ __forceinline__ float wave_max(float v) { return group_max<64>(v); }
-template <int L>
-__device__ __forceinline__ bool group_any(bool v, int lane) {
-  return (__ballot(v) >> (lane & (64 - L))) & (~0ull >> (64 - L));
-}
 
 // LDS accesses of a wave before this line and after it stay apart
 __device__ __forceinline__ void wave_fence() {

@@ -341,3 +341,30 @@ def test_fp32_logits_a_bit_apart(lib, e, k):
     x[150:] = torch.where(order[150:] < e // 2, 2.0 * order[150:] / e, x[150:])
     check_route(lib, x, k, None, True)
     check_route(lib, x, k, None, False)
+
+
+def nan_with_the_sign_set(dtype):
+    bits, as_int = {torch.float32: (-0x400000, torch.int32), torch.float16: (-0x200, torch.int16),
+                    torch.bfloat16: (-0x40, torch.int16)}[dtype]
+    v = torch.tensor([bits], dtype=as_int).view(dtype)
+    assert torch.isnan(v).all() and torch.signbit(v).all()
+    return v
+
+
+@pytest.mark.parametrize("e,k", [(4, 2), (30, 4), (32, 20), (64, 8), (100, 6), (256, 8), (256, 12), (500, 8), (1000, 32)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_nan_with_the_sign_set(lib, dtype, e, k):
+    """Such a NaN orders below -inf; its row is live and not a number all the same, forward and backward."""
+    nan = nan_with_the_sign_set(dtype)
+    dw = torch.randn(70, k, generator=torch.Generator().manual_seed(7))
+    for rows in ("nan", "nan and -inf", "one nan", "one nan among -inf"):
+        x = logits(70, e, dtype, 50 + e)
+        if rows in ("nan and -inf", "one nan among -inf"):
+            x[[0, 33]] = -INF
+        x[[0, 33], (slice(None) if rows == "nan" else slice(1, e, 2) if rows == "nan and -inf" else e // 2)] = nan
+        for normalize in (True, False):
+            got = check_route(lib, x, k, None, normalize)
+            assert got[2][e].item() == 70 and torch.isnan(got[3]).all(), rows
+            _, d = lib.route_grad(x.cuda(), got[0], dw.cuda(), got[2], torch.ones(e, device="cuda"), 1.0,
+                                  normalize=normalize)
+            check_grad_values(x, got[0].cpu(), dw, got[2].cpu(), 1.0, None, normalize, d)
