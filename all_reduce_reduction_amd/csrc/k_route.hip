@@ -615,6 +615,8 @@ __global__ void __launch_bounds__(kBlock) k_route_grad(RouteGradArgs a) {
         if (mine[s] >= 0 && live) add[mine[s]] = p[s] * dw[s];
     }
     dot = group_sum<L>(dot);
+    // (an empty row's p are 0, but its slots' dweights and coef may be anything)
+    const bool some_empty = __any(!live);
     wave_fence();
 #pragma unroll
     for (int j = 0; j < G::NV; j++) {
@@ -623,6 +625,10 @@ __global__ void __launch_bounds__(kBlock) k_route_grad(RouteGradArgs a) {
       for (int t = 0; t < V; t++) {
         const int e = G::col(j, l) + t;
         d[t] = __builtin_fmaf(f[j * V + t], g_s[e] - dot, add[e]);
+      }
+      if (some_empty) {
+#pragma unroll
+        for (int t = 0; t < V; t++) d[t] = live ? d[t] : 0.0f;
       }
       if (here) {
         if (a.experts == G::kAll) st_row<DT>(dx, G::col(j, l), pack_rounded<DT>(d));

@@ -368,3 +368,25 @@ def test_nan_with_the_sign_set(lib, dtype, e, k):
             _, d = lib.route_grad(x.cuda(), got[0], dw.cuda(), got[2], torch.ones(e, device="cuda"), 1.0,
                                   normalize=normalize)
             check_grad_values(x, got[0].cpu(), dw, got[2].cpu(), 1.0, None, normalize, d)
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_empty_rows_get_zeros_whatever_their_slots_and_coef_hold(lib, dtype, normalize):
+    t, e, k = 300, 40, 4
+    x = logits(t, e, dtype, 60)
+    keep = torch.arange(t) % 4 != 1
+    x[2] = -INF
+    empty = ~keep
+    empty[2] = True
+    chosen, _, counts, sums = lib.route(x.cuda(), k, normalize=normalize)  # every row has slots
+    chosen[2] = torch.arange(k, dtype=torch.int32, device="cuda")
+    dw = torch.randn(t, k, generator=torch.Generator().manual_seed(8))
+    odd = dw.clone()
+    odd[empty] = torch.tensor([float("nan"), INF, -INF, 1.0])
+    _, d = lib.route_grad(x.cuda(), chosen, odd.cuda(), counts, sums, 1.0, keep=keep.cuda(), normalize=normalize)
+    assert not d[empty.cuda()].any()
+    check_grad_values(x, chosen.cpu(), torch.where(empty[:, None], 0.0, dw), counts.cpu(), 1.0, keep, normalize, d)
+    for coef in (INF, float("nan")):
+        _, d = lib.route_grad(x.cuda(), chosen, dw.cuda(), counts, sums, coef, keep=keep.cuda(), normalize=normalize)
+        assert not d[empty.cuda()].any() and torch.isnan(d[~empty.cuda()]).all()
