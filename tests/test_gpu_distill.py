@@ -411,3 +411,25 @@ def test_shards_of_many_rows(lib, dtype):
             loss, grad, _ = shards(lib, x[pick], ids[pick], z[pick], 1.5, None, 64.0, 2 if d == 33 else 1)
             check(x, ids, z, 1.5, None, 64.0, loss[:8], grad[:8], "%d columns" % v)
             assert torch.equal(grad.view(-1, 8, v), grad[:8].expand(t // 8, 8, v)), v
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("t", [6, 600])
+def test_logits_at_both_ends_of_the_type(lib, dtype, t):
+    """The type's lowest value beside its highest: their distance is past fp32's range, over the temperature it is not."""
+    v, k = 2100, 5
+    x, ids, z, _ = case(t, v, k, dtype, torch.float32, 79, holes=False)
+    low, high = torch.finfo(dtype).min, torch.finfo(dtype).max
+    ids[:5] = torch.arange(k, dtype=torch.int32) * 400 + 7
+    x[0, 100], x[0, 7] = high, low           # in one shard
+    x[1, 2000], x[1, 407] = high, low        # in two
+    x[2, :1050], x[2, 2000] = low, high      # a shard of the lowest value alone
+    x[3, 1050:], x[3, 3] = low, high
+    x[4], x[4, 1:3] = low, high              # all of a row at one end or the other
+    for tau in (3.0, 1e4, 1e15):
+        loss, d = step(lib, x, ids, z, tau)
+        check(x, ids, z, tau, None, 1.0, loss, d, f"tau {tau}")
+        assert torch.isfinite(loss).all()
+        for p in (2, 3):
+            loss, d, _ = shards(lib, x, ids, z, tau, None, 1.0, p)
+            check(x, ids, z, tau, None, 1.0, loss, d, f"{p} shards, tau {tau}")
