@@ -589,17 +589,28 @@ def distill_step(logits, ids, teacher, temperature: float = 1.0, row_scale=None,
     return out
 
 
+def _whole(vocab, rows, columns):
+    """The whole vocabulary's size.  A teacher's slots are those with an id in it, so parts, join and gradient have to
+    be told the same one; no size that one shard could take by itself is right for all of them.  (Without rows there is
+    nothing to be told.)"""
+    if vocab is not None:
+        return vocab
+    if rows:
+        raise ValueError("vocab must be given: the columns of all shards together")
+    return columns
+
+
 def distill_parts(logits, ids, teacher, temperature: float = 1.0, first: int = 0, vocab: Optional[int] = None,
                   out=None, stream=None):
-    """A vocabulary shard's statistics, fp32 [4, rows]: logits hold the columns from `first` on of `vocab` (default:
-    up to the shard's end)."""
+    """A vocabulary shard's statistics, fp32 [4, rows]: logits hold the columns from `first` on of all `vocab` ones
+    (must be given)."""
     ptr, ld, n, c, dt, dev = _rows(logits, "logits", None)
     if out is None:
         out = _empty((4, n), torch.float32, dev, stream)
     ip, tp, tdt, k = _slots(ids, teacher, _I32, n, dev)
     nb = sim_distill_work(n, c, dt)
     w, wp = _work(nb, dev, stream)
-    _check(_entry.distill_parts(ptr, ld, dt, n, c, first, first + c if vocab is None else vocab, ip, tp, tdt, k,
+    _check(_entry.distill_parts(ptr, ld, dt, n, c, first, _whole(vocab, n, first + c), ip, tp, tdt, k,
                                 temperature, _vec(out, "parts", _F32, dev, 4, n), wp, nb, _on(stream, dev)),
            "sim_distill_parts")
     return out
@@ -607,7 +618,7 @@ def distill_parts(logits, ids, teacher, temperature: float = 1.0, first: int = 0
 
 def distill_join(parts, ids, teacher, temperature: float = 1.0, vocab: Optional[int] = None, out=None, stream=None):
     """Loss of all shards' parts [nparts, 4, rows], as all_gather leaves them: (loss fp32 [rows], norm fp32 [2,
-    rows]).  vocab: the whole vocabulary (an id outside it is an empty slot; default: only a negative one is)."""
+    rows]).  vocab: the columns of all shards together (must be given; an id outside it is an empty slot)."""
     if parts.dim() != 3 or not parts.is_cuda:
         raise ValueError("parts must be a device tensor [nparts, 4, rows]")
     p, _, n = parts.shape
@@ -616,7 +627,7 @@ def distill_join(parts, ids, teacher, temperature: float = 1.0, vocab: Optional[
         out = (_empty(n, torch.float32, dev, stream), _empty((2, n), torch.float32, dev, stream))
     loss, norm = out
     ip, tp, tdt, k = _slots(ids, teacher, _I32, n, dev)
-    _check(_entry.distill_join(_vec(parts, "parts", _F32, dev, p, 4, n), p, n, 2 ** 31 - 1 if vocab is None else vocab,
+    _check(_entry.distill_join(_vec(parts, "parts", _F32, dev, p, 4, n), p, n, _whole(vocab, n, 1),
                                ip, tp, tdt, k, temperature, _vec(loss, "loss", _F32, dev, n),
                                _vec(norm, "norm", _F32, dev, 2, n), _on(stream, dev)), "sim_distill_join")
     return out
@@ -624,14 +635,14 @@ def distill_join(parts, ids, teacher, temperature: float = 1.0, vocab: Optional[
 
 def distill_grad(logits, ids, teacher, norm, temperature: float = 1.0, row_scale=None, coef: float = 1.0,
                  first: int = 0, vocab: Optional[int] = None, out=None, stream=None):
-    """The gradient of a vocabulary shard's logits from the joined norm [2, rows].  out: the gradient, to write into
-    (it may be the logits)."""
+    """The gradient of a vocabulary shard's logits, the columns from `first` on of all `vocab` ones (must be given),
+    from the joined norm [2, rows].  out: the gradient, to write into (it may be the logits)."""
     ptr, ld, n, c, dt, dev = mine = _rows(logits, "logits", None)
     if out is None:
         out = _empty((n, c), logits.dtype, dev, stream)
     dptr, dld, *_ = _rows(out, "dlogits", mine)
     ip, tp, tdt, k = _slots(ids, teacher, _I32, n, dev)
-    _check(_entry.distill_grad(ptr, ld, dt, n, c, first, first + c if vocab is None else vocab, ip, tp,
+    _check(_entry.distill_grad(ptr, ld, dt, n, c, first, _whole(vocab, n, first + c), ip, tp,
                                tdt, k, temperature, _vec(norm, "norm", _F32, dev, 2, n),
                                _vec(row_scale, "row_scale", _F32, dev, n), coef, dptr, dld, _on(stream, dev)),
            "sim_distill_grad")

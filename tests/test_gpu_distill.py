@@ -433,3 +433,17 @@ def test_logits_at_both_ends_of_the_type(lib, dtype, t):
         for p in (2, 3):
             loss, d, _ = shards(lib, x, ids, z, tau, None, 1.0, p)
             check(x, ids, z, tau, None, 1.0, loss, d, f"{p} shards, tau {tau}")
+
+
+def test_shards_have_to_be_told_the_whole_vocabulary(lib):
+    """One shard cannot know which ids are slots of the row: a size of its own would drop those of later shards."""
+    x, ids, z, _ = case(6, 90, 4, torch.bfloat16, torch.float32, 80, holes=False)
+    ids[:, 0] = 80
+    xs, i, y = [x[:, :50].contiguous().cuda(), x[:, 50:].contiguous().cuda()], ids.cuda(), z.cuda()
+    parts = lib.distill_parts(xs[0], i, y, vocab=90)
+    gathered = torch.stack([parts, lib.distill_parts(xs[1], i, y, first=50, vocab=90)])
+    _, norm = lib.distill_join(gathered, i, y, vocab=90)
+    for call in (lambda: lib.distill_parts(xs[0], i, y), lambda: lib.distill_parts(xs[1], i, y, first=50),
+                 lambda: lib.distill_join(gathered, i, y), lambda: lib.distill_grad(xs[0], i, y, norm)):
+        with pytest.raises(ValueError, match="vocab"):
+            call()
