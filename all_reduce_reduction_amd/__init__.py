@@ -46,7 +46,7 @@ DEBUG = {"epoch": 0, "spin_limit": 1, "ll_wait_skew": 2, "fill_ll": 3, "log": 4,
          "unroll": 6, "fifo_channels": 7, "fifo_slots": 8, "fifo_withhold": 9, "fifo_vecs": 10,
          "ptr_table": 11, "ptr_sets": 12, "ring_ll_max": 13,
               "phased": 14, "phased_min": 15, "phased_expired": 16, "phased_last": 17,
-         "phased_layout": 18, "phased_whole_last": 19}
+         "phased_layout": 18, "phased_whole_last": 19, "route_launches": 20}
 MAX_RANKS = 16
 ROUTE_MAX_EXPERTS, ROUTE_MAX_TOPK, DISTILL_MAX_TOPK = 1024, 32, 256
 LL_MAX_BYTES_PER_RANK = 1 << 20

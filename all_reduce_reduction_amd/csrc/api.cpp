@@ -80,7 +80,7 @@ struct PtrSlot {
   bool ready = false;
 };
 
-constexpr size_t kTurns = 64, kTurnWords = 32;  // streams with a counter; a 128-byte line each
+constexpr uint32_t kTurns = 4096, kTurnWords = 32;  // launches with a counter at a time; a 128-byte line each
 
 struct Ctx {
   bool init = false;
@@ -111,10 +111,15 @@ struct Ctx {
   int fifo_vecs = kFifoVecsPerLane;  // 16-byte vectors per lane per slot: 1, 2 or 4
   bool capturing = false;  // the current call's stream is being captured into a graph
   bool captured = false;   // some call has been captured since sim_init
-  // counters of the launches whose last workgroup finishes the work: one per
-  // stream, a cache line apart
+  // counters of the launches whose last workgroup finishes the work, handed out
+  // in turn: how often each was, and (in pinned host memory) how often the
+  // launch has reported back
   uint32_t* turns = nullptr;
-  std::vector<hipStream_t> turn_streams;
+  uint32_t* turns_done = nullptr;      // the host's address
+  uint32_t* turns_dev_done = nullptr;  // the device's
+  std::vector<uint32_t> turn_calls;
+  uint32_t turn_next = 0;
+  int route_launches = 0;  // kernels of the last routing call
   std::vector<void*> retired;  // outgrown scratch a captured graph may still use
   // pointer table (one-shot calls outside graph capture): slot i of `ptab`
   // holds a pointer set, copied from slot i of the pinned `ptab_host`; slots
@@ -1332,21 +1337,27 @@ int parse_algo_env(const char* v) {
 bool library_ready() { return g.init; }
 int library_device() { return use_device(); }
 int library_cus() { return g.cu_count; }
-uint32_t* library_turn(hipStream_t stream) {
-  if (!g.turns || stream == hipStreamPerThread) return nullptr;
+Turn library_turn(hipStream_t stream) {
+  const Turn none{};
+  if (!g.turns) return none;
   hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
   if (hipStreamIsCapturing(stream, &st) != hipSuccess) {
     (void)hipGetLastError();
-    return nullptr;
+    return none;
   }
-  if (st != hipStreamCaptureStatusNone) return nullptr;
-  size_t i = 0;
-  while (i < g.turn_streams.size() && g.turn_streams[i] != stream) i++;
-  if (i == g.turn_streams.size()) {
-    if (i == kTurns) return nullptr;
-    g.turn_streams.push_back(stream);
+  if (st != hipStreamCaptureStatusNone) return none;
+  const uint32_t i = g.turn_next;
+  if (__atomic_load_n(&g.turns_done[i], __ATOMIC_ACQUIRE) != g.turn_calls[i]) {
+    g.turn_next = (i + 1) % kTurns;
+    return none;
   }
-  return g.turns + i * kTurnWords;
+  return Turn{g.turns + (size_t)i * kTurnWords, g.turns_dev_done + i, g.turn_calls[i] + 1};
+}
+void library_turn_used(const Turn& t, int launches) {
+  g.route_launches = launches;
+  if (!t.word) return;
+  g.turn_calls[g.turn_next] = t.call;
+  g.turn_next = (g.turn_next + 1) % kTurns;
 }
 
 }  // namespace simar
@@ -1376,7 +1387,7 @@ const char* sim_status_string(int status) {
 int sim_finalize(void) {
   // (also releases what a failed sim_init had allocated before it gave up)
   if (!g.init && !g.err && !g.ll && !g.fifo_sem && !g.scratch && !g.ptab && !g.ptab_host && !g.ph_mem &&
-      !g.ph_host_done && !g.turns)
+      !g.ph_host_done && !g.turns && !g.turns_done)
     return SIM_OK;
   // teardown is best effort: every allocation is released even if one call fails
   (void)hipSetDevice(g.device);
@@ -1388,6 +1399,7 @@ int sim_finalize(void) {
   if (g.fifo_sem) (void)hipFree(g.fifo_sem);
   if (g.ph_mem) (void)hipFree(g.ph_mem);
   if (g.turns) (void)hipFree(g.turns);
+  if (g.turns_done) (void)hipHostFree(g.turns_done);
   if (g.ph_host_done) (void)hipHostFree(g.ph_host_done);
   if (g.err) (void)hipFree(g.err);
   for (PtrSlot& sl : g.ptab_slots)
@@ -1461,13 +1473,21 @@ int sim_init(int device, int p_max, size_t max_bytes_per_rank) {
     *g.ph_host_done = 0;
   }
   // (without the counters a second launch finishes such work)
-  if (hipMalloc(&g.turns, kTurns * kTurnWords * 4) != hipSuccess) {
+  if (hipHostMalloc((void**)&g.turns_done, kTurns * 4, hipHostMallocMapped | hipHostMallocCoherent) != hipSuccess ||
+      hipHostGetDevicePointer((void**)&g.turns_dev_done, g.turns_done, 0) != hipSuccess ||
+      hipMalloc(&g.turns, (size_t)kTurns * kTurnWords * 4) != hipSuccess) {
     (void)hipGetLastError();
+    if (g.turns_done) (void)hipHostFree(g.turns_done);
+    g.turns_done = nullptr;
     g.turns = nullptr;
-  } else if (launch_fill64((unsigned long long*)g.turns, 0ull, kTurns * kTurnWords / 2, nullptr) != hipSuccess ||
-             hipDeviceSynchronize() != hipSuccess) {
-    sim_finalize();
-    return SIM_ERR_HIP;
+  } else {
+    if (launch_fill64((unsigned long long*)g.turns, 0ull, kTurns * kTurnWords / 2, nullptr) != hipSuccess ||
+        hipDeviceSynchronize() != hipSuccess) {
+      sim_finalize();
+      return SIM_ERR_HIP;
+    }
+    std::memset(g.turns_done, 0, kTurns * 4);
+    g.turn_calls.assign(kTurns, 0);
   }
   // the pointer table only makes launches cheaper: without it every call
   // carries its pointers in its kernel arguments
@@ -2008,6 +2028,7 @@ int sim_debug_get(int key, uint64_t* value) {
     case SIM_DEBUG_PHASED_LAST: *value = g.last_phased ? 1 : 0; return SIM_OK;
     case SIM_DEBUG_PHASED_LAYOUT: *value = (uint64_t)g.ph_layout; return SIM_OK;
     case SIM_DEBUG_PHASED_WHOLE_LAST: *value = g.last_whole ? 1 : 0; return SIM_OK;
+    case SIM_DEBUG_ROUTE_LAUNCHES: *value = (uint64_t)g.route_launches; return SIM_OK;
     case SIM_DEBUG_PHASED_EXPIRED: {
       if (!g.init) return SIM_ERR_NOT_INIT;
       unsigned int v = 0;

@@ -142,10 +142,12 @@ int sim_route(const void* logits, int64_t row_stride, int dtype, const uint8_t* 
   if ((rc = check_arrays(all, -1, -1, false))) return rc;
   if ((rc = library_device())) return rc;
   const int wg = route_workgroups(tokens, experts, dtype);
-  uint32_t* const turn = route_sums_itself(wg, experts) ? library_turn((hipStream_t)stream) : nullptr;
+  const Turn turn = route_sums_itself(wg, experts) ? library_turn((hipStream_t)stream) : Turn{};
   const RouteArgs a{logits, row_stride, keep, tokens, experts, topk, normalize != 0, chosen, weights, counts, prob_sums,
                     (uint32_t*)work, wg, turn};
-  return hip_status(launch_route(a, dtype, (hipStream_t)stream));
+  const hipError_t e = launch_route(a, dtype, (hipStream_t)stream);
+  if (e == hipSuccess) library_turn_used(turn, wg == 1 || turn.word ? 1 : 2);
+  return hip_status(e);
 }
 
 int sim_route_grad(const void* logits, int64_t row_stride, int dtype, const uint8_t* keep, int64_t tokens,

@@ -269,7 +269,7 @@ __device__ __forceinline__ void sum_in_last(const RouteArgs& a, uint32_t* word_s
   constexpr int kFlight = 32;  // loads of a thread under way (16: 9.3 us where 32 take 8.5)
   wait_stores();
   __syncthreads();
-  if (threadIdx.x == 0) *word_s = __hip_atomic_fetch_add(a.turn, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (threadIdx.x == 0) *word_s = __hip_atomic_fetch_add(a.turn.word, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   if (*word_s != (uint32_t)a.workgroups - 1) return;
   const int all = 2 * a.experts + 1;
@@ -294,7 +294,11 @@ __device__ __forceinline__ void sum_in_last(const RouteArgs& a, uint32_t* word_s
     if (e <= a.experts) a.counts[e] = (int32_t)n;
     else a.sums[e - a.experts - 1] = s;
   }
-  if (threadIdx.x == 0) put(a.turn, 0);
+  if (threadIdx.x == 0) {
+    put(a.turn.word, 0);
+    wait_stores();
+    __hip_atomic_store(a.turn.done, a.turn.call, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+  }
 }
 
 // ---- forward ------------------------------------------------------------------------
@@ -478,7 +482,7 @@ __global__ void __launch_bounds__(kBlock, N == 32 ? 3 : 4) k_route(RouteArgs a) 
       if (e < a.experts) put(part + a.experts + 1 + e, __builtin_bit_cast(uint32_t, s));
     }
   }
-  if (a.turn) sum_in_last(a, &count_s[0]);
+  if (a.turn.word) sum_in_last(a, &count_s[0]);
 }
 
 // The workgroups' counts and sums, kSumCols of them per workgroup: 1024
@@ -698,7 +702,7 @@ hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s) {
   const hipError_t e = dtype == SIM_FP32   ? route_dtype<SIM_FP32>(a, s)
                        : dtype == SIM_FP16 ? route_dtype<SIM_FP16>(a, s)
                                            : route_dtype<SIM_BF16>(a, s);
-  if (e != hipSuccess || a.workgroups == 1 || a.turn) return e;
+  if (e != hipSuccess || a.workgroups == 1 || a.turn.word) return e;
   return launch<k_route_sum>(dim3((2 * a.experts + kSumCols) / kSumCols), dim3(kSumCols * kSumRows), s, a);
 }
 hipError_t launch_route_grad(const RouteGradArgs& a, int dtype, hipStream_t s) {

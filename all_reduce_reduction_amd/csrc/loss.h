@@ -18,11 +18,21 @@ namespace simar {
 bool library_ready();
 int library_device();
 int library_cus();
-// A word of device memory that holds 0 between the launches of `stream`, for
-// those launches alone; NULL where there is none: a captured stream (its graph
-// may run on any other), the per-thread stream (one handle for many), more
-// streams than there are words.
-uint32_t* library_turn(hipStream_t stream);
+// A word of device memory for one launch alone, 0 before it.  The launch leaves
+// 0 there and then reports `call` to `done`, in host memory; only then is the
+// word handed out again, so that no two launches can meet in it, on whatever
+// streams they are.  A launch that should ever end without its report keeps its
+// word for good.
+struct Turn {
+  uint32_t* word;  // NULL: none
+  uint32_t* done;
+  uint32_t call;
+};
+// A word for the next launch on `stream`; none for a captured one (its graph is
+// replayed with the same arguments) or while the next word is still in use.
+Turn library_turn(hipStream_t stream);
+// That launch was made, with `launches` kernels in all.
+void library_turn_used(const Turn& t, int launches);
 
 struct RouteArgs {
   const void* x;
@@ -36,7 +46,7 @@ struct RouteArgs {
   float* sums;
   uint32_t* partial;  // per workgroup: experts + 1 counts, then experts sums
   int workgroups;
-  uint32_t* turn;     // 0 before and after the launch: the workgroups add up their own sums
+  Turn turn;          // with a word: the workgroups add up their own sums
 };
 
 struct RouteGradArgs {

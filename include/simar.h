@@ -456,11 +456,11 @@ int sim_verify_custom(int algo, int p, int nchunks, int rounds, int nsteps, cons
  *   - Statistics are fp32 whatever `dtype` is, and every sum is taken in an
  *     order that depends on the sizes alone: the same call on the same data
  *     gives the same bits.
- *   - Of library memory only one counter per stream is used, by sim_route
- *     outside of capture.  `work` is the caller's scratch of at
- *     least the bytes the matching *_work function says (0: it may be NULL),
- *     4-byte aligned, free for reuse once the call's stream work is done;
- *     too little is SIM_ERR_NOMEM.
+ *   - Of library memory only one counter is used, by a small sim_route call
+ *     outside of capture, for as long as the call's stream work takes.  `work`
+ *     is the caller's scratch of at least the bytes the matching *_work
+ *     function says (0: it may be NULL), 4-byte aligned, free for reuse once
+ *     the call's stream work is done; too little is SIM_ERR_NOMEM.
  *   - 0 rows are a no-op, except that sim_route writes zero counts and sums
  *     and sim_route_grad writes the loss.
  */
@@ -585,8 +585,9 @@ enum {
                                   buffer's blocks in turn over the grid where every chunk is the
                                   same whole number of blocks, no fewer than the grid's
                                   workgroups; 1 each chunk's blocks over its own workgroups */
-  SIM_DEBUG_PHASED_WHOLE_LAST = 19 /* get only: 1 if the last collective call ran the phased
+  SIM_DEBUG_PHASED_WHOLE_LAST = 19, /* get only: 1 if the last collective call ran the phased
                                   one-shot in the whole-buffer layout */
+  SIM_DEBUG_ROUTE_LAUNCHES = 20 /* get only: kernels that the last sim_route call enqueued */
 };
 int sim_debug_set(int key, uint64_t value);
 int sim_debug_get(int key, uint64_t* value);

@@ -390,3 +390,65 @@ def test_empty_rows_get_zeros_whatever_their_slots_and_coef_hold(lib, dtype, nor
     for coef in (INF, float("nan")):
         _, d = lib.route_grad(x.cuda(), chosen, dw.cuda(), counts, sums, coef, keep=keep.cuda(), normalize=normalize)
         assert not d[empty.cuda()].any() and torch.isnan(d[~empty.cuda()]).all()
+
+
+def test_streams_that_come_and_go_keep_the_one_launch_form(lib):
+    """However many streams a process has made, a small call's workgroups add up their own sums."""
+    import ctypes
+    hip = ctypes.CDLL("libamdhip64.so")
+    x = logits(500, 32, torch.bfloat16, 61).cuda()
+    want = [v.clone() for v in lib.route(x, 4)]
+    out = tuple(torch.empty_like(v) for v in want)
+    torch.cuda.synchronize()
+    for _ in range(150):
+        s = ctypes.c_void_p()
+        assert hip.hipStreamCreate(ctypes.byref(s)) == 0
+        try:
+            lib.route(x, 4, out=out, stream=torch.cuda.ExternalStream(s.value))
+            assert lib.sim_debug_get("route_launches") == 1
+        finally:
+            torch.cuda.synchronize()
+            hip.hipStreamDestroy(s)
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+        for v in out:
+            v.zero_()
+
+
+def test_many_small_calls_in_a_row(lib):
+    """More calls than the library has counters, waited for and not; a captured call takes none."""
+    x = logits(700, 24, torch.float32, 62).cuda()
+    want = [v.clone() for v in lib.route(x, 3)]
+    out = tuple(torch.empty_like(v) for v in want)
+    for n in (1, 500, 4096, 5000, 9000):
+        for v in out:
+            v.zero_()
+        for _ in range(n):
+            lib.route(x, 3, out=out)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), n
+    lib.route(x, 3, out=out)
+    assert lib.sim_debug_get("route_launches") == 1
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lib.route(x, 3, out=out)
+        assert lib.sim_debug_get("route_launches") == 2
+    for _ in range(3):
+        for v in out:
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_the_per_thread_stream(lib):
+    t, e, k = 900, 48, 5
+    x = logits(t, e, torch.bfloat16, 63).cuda()
+    want = lib.route(x, k)
+    out = tuple(torch.zeros_like(v) for v in want)
+    need = lib.sim_route_work(t, e, k, "bf16")
+    work = torch.empty(need, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert lib.sim_route(x.data_ptr(), e, "bf16", None, t, e, k, 1, *(v.data_ptr() for v in out), work.data_ptr(), need,
+                         stream=2) == 0  # hipStreamPerThread
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
