@@ -53,7 +53,12 @@ int check_arrays(const Array (&a)[N], int under, int over, bool same_stride) {
   return SIM_OK;
 }
 
-int hip_status(hipError_t e) { return e == hipSuccess ? SIM_OK : SIM_ERR_HIP; }
+// Too many rows for a launch are the caller's error.  It is always a call's
+// first launch that has too many: the others are only made for few rows, or
+// with as many threads as the first.
+int hip_status(hipError_t e) {
+  return e == hipSuccess ? SIM_OK : e == hipErrorInvalidConfiguration ? SIM_ERR_INVALID_ARG : SIM_ERR_HIP;
+}
 
 int check_route(int64_t tokens, int experts, int topk, int dtype) {
   if (!float_dtype(dtype)) return SIM_ERR_INVALID_ARG;
@@ -229,7 +234,7 @@ int sim_distill_step(const void* logits, int64_t row_stride, int dtype, int64_t 
                       : dtype == SIM_FP16 ? launch_distill_row_fp16(a, s)
                                           : launch_distill_row_bf16(a, s));
   const hipError_t e = launch_distill_stats(a, dtype, s);
-  if (e != hipSuccess) return SIM_ERR_HIP;
+  if (e != hipSuccess) return hip_status(e);
   return hip_status(launch_distill_grad(a, dtype, s));
 }
 
@@ -267,7 +272,7 @@ int sim_distill_parts(const void* logits, int64_t row_stride, int dtype, int64_t
   if ((int64_t)a.splits * rows > kMaxGrid) return SIM_ERR_INVALID_ARG;
   a.parts = a.splits > 1 ? (float*)work : parts;
   const hipError_t e = launch_distill_stats(a, dtype, (hipStream_t)stream);
-  if (e != hipSuccess) return SIM_ERR_HIP;
+  if (e != hipSuccess) return hip_status(e);
   return a.splits > 1 ? hip_status(launch_distill_merge(a, parts, (hipStream_t)stream)) : SIM_OK;
 }
 

@@ -27,6 +27,8 @@ struct Kernel;
 template <class... P, void (*K)(P...)>
 struct Kernel<K> {
   static hipError_t launch(dim3 grid, dim3 block, hipStream_t s, const P&... a) {
+    // (a launch's threads are counted in 32 bits)
+    if ((uint64_t)grid.x * block.x >> 32) return hipErrorInvalidConfiguration;
     static hipFunction_t fn[kMaxDevices];  // per device, filled on first use
     const int d = g_launch_device;
     if (d < 0 || d >= kMaxDevices) return hipErrorInvalidDevice;

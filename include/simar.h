@@ -462,7 +462,10 @@ int sim_verify_custom(int algo, int p, int nchunks, int rounds, int nsteps, cons
  *     function says (0: it may be NULL), 4-byte aligned, free for reuse once
  *     the call's stream work is done; too little is SIM_ERR_NOMEM.
  *   - 0 rows are a no-op, except that sim_route writes zero counts and sums
- *     and sim_route_grad writes the loss.
+ *     and sim_route_grad writes the loss.  A distillation call of so many
+ *     rows that a launch would need 2^32 threads is SIM_ERR_INVALID_ARG: each
+ *     takes 64 where its columns are few (and always in sim_distill_join), up
+ *     to 1,024 otherwise, or 256 per 16 KiB of it.
  */
 #define SIM_ROUTE_MAX_EXPERTS 1024
 #define SIM_ROUTE_MAX_TOPK 32

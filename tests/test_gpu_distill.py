@@ -447,3 +447,31 @@ def test_shards_have_to_be_told_the_whole_vocabulary(lib):
                  lambda: lib.distill_join(gathered, i, y), lambda: lib.distill_grad(xs[0], i, y, norm)):
         with pytest.raises(ValueError, match="vocab"):
             call()
+
+
+def test_more_rows_than_a_launch_has_threads_for(lib):
+    """Refused as the caller's error, before anything is enqueued; one row fewer runs."""
+    t = 1 << 26  # 64 threads a row
+    x, d = (torch.zeros(t, 1, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ids = torch.zeros(t, 1, dtype=torch.int32, device="cuda")
+    z = torch.zeros(t, 1, dtype=torch.bfloat16, device="cuda")
+    loss = torch.full((t,), 7.0, device="cuda")
+    norm = torch.full((2, t), 7.0, device="cuda")
+    parts = torch.full((4, t), 7.0, device="cuda")
+    need = lib.sim_distill_work(t, 1, "bf16")
+    work = torch.empty(need, dtype=torch.uint8, device="cuda")
+    common = dict(rows=t, vocab=1, ids=ids.data_ptr(), teacher=z.data_ptr(), teacher_dtype="bf16", topk=1, temperature=1.0)
+    shard = dict(common, logits=x.data_ptr(), row_stride=1, dtype="bf16", columns=1, first=0)
+    step = dict(common, logits=x.data_ptr(), row_stride=1, dtype="bf16", row_scale=None, coef=1.0, dlogits=d.data_ptr(),
+                drow_stride=1, loss=loss.data_ptr(), work=work.data_ptr(), work_bytes=need)
+    assert lib.sim_distill_step(**step) == -1
+    assert lib.sim_distill_parts(**shard, parts=parts.data_ptr(), work=work.data_ptr(), work_bytes=need) == -1
+    assert lib.sim_distill_grad(**shard, norm=norm.data_ptr(), row_scale=None, coef=1.0, dlogits=d.data_ptr(),
+                                drow_stride=1) == -1
+    assert lib.sim_distill_join(**common, parts=parts.data_ptr(), nparts=1, loss=loss.data_ptr(),
+                                norm=norm.data_ptr()) == -1
+    torch.cuda.synchronize()
+    assert (loss == 7).all() and (norm == 7).all() and (parts == 7).all() and not d.any()
+    assert lib.sim_distill_step(**{**step, "rows": t - 64}) == 0
+    torch.cuda.synchronize()
+    assert not loss[:t - 64].any() and (loss[t - 64:] == 7).all()
