@@ -16,23 +16,36 @@ constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
 bool float_dtype(int d) { return d == SIM_FP32 || d == SIM_FP16 || d == SIM_BF16; }
 int64_t size_of(int d) { return d == SIM_FP32 ? 4 : 2; }
 
-// An array of a call: its address range (first to last element) and the
-// alignment its elements need.
+// An array of a call: its address range (first to last element), the alignment
+// its elements need, and for rows with others' elements between them the bytes
+// of a row and from one to the next.
 struct Array {
   const void* p;
   int64_t bytes;
   int64_t align;
   bool output;
+  int64_t width = 0, pitch = 0;
 };
 
 Array rows_of(const void* p, int64_t rows, int64_t cols, int64_t stride, int dtype, bool output) {
   const int64_t e = size_of(dtype);
-  return {p, rows > 0 ? ((rows - 1) * stride + cols) * e : 0, e, output};
+  return {p, rows > 0 ? ((rows - 1) * stride + cols) * e : 0, e, output, cols * e, stride * e};
 }
 
 bool rows_fit(int64_t rows, int64_t cols, int64_t stride) {
   return rows >= 0 && cols >= 1 && stride >= cols && stride <= kMaxBytes / 4 &&
          (rows == 0 || rows <= kMaxBytes / 4 / stride);
+}
+
+// Whether two arrays share a byte.  Rows at the same distances may lie between
+// each other's: column slices of one wide buffer.
+bool overlap(const Array& a, const Array& b) {
+  const uintptr_t p = (uintptr_t)a.p, q = (uintptr_t)b.p;
+  if (!(p < q + (uintptr_t)b.bytes && q < p + (uintptr_t)a.bytes)) return false;
+  if (a.pitch == 0 || a.pitch != b.pitch) return true;
+  const int64_t to_b = p <= q ? (int64_t)((q - p) % (uintptr_t)a.pitch)
+                              : (a.pitch - (int64_t)((p - q) % (uintptr_t)a.pitch)) % a.pitch;
+  return to_b < a.width || to_b + b.width > a.pitch;
 }
 
 // NULL arrays are absent ones.  `over`: the index of an output that may lie
@@ -46,8 +59,7 @@ int check_arrays(const Array (&a)[N], int under, int over, bool same_stride) {
     for (int j = 0; j < N; j++) {
       if (j == i || !a[j].p || a[j].bytes == 0) continue;
       if (i == over && j == under && a[i].p == a[j].p && same_stride) continue;
-      const uintptr_t p = (uintptr_t)a[i].p, q = (uintptr_t)a[j].p;
-      if (p < q + (uintptr_t)a[j].bytes && q < p + (uintptr_t)a[i].bytes) return SIM_ERR_ALIAS;
+      if (overlap(a[i], a[j])) return SIM_ERR_ALIAS;
     }
   }
   return SIM_OK;

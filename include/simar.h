@@ -450,9 +450,9 @@ int sim_verify_custom(int algo, int p, int nchunks, int rounds, int nsteps, cons
  *     elements apart, row_stride >= the row's columns; they and every other
  *     array need only the alignment of their own elements (SIM_ERR_ALIGN).
  *     The other arrays are contiguous.
- *   - A gradient may be written over its logits (same address and stride).
- *     Any other overlap of an output with an input or another output is
- *     SIM_ERR_ALIAS.
+ *   - A gradient may be written over its logits (same address and stride), or
+ *     between them: other columns of the same wide rows.  Any overlap of an
+ *     output with an input or another output but the first is SIM_ERR_ALIAS.
  *   - Statistics are fp32 whatever `dtype` is, and every sum is taken in an
  *     order that depends on the sizes alone: the same call on the same data
  *     gives the same bits.

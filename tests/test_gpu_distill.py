@@ -475,3 +475,45 @@ def test_more_rows_than_a_launch_has_threads_for(lib):
     assert lib.sim_distill_step(**{**step, "rows": t - 64}) == 0
     torch.cuda.synchronize()
     assert not loss[:t - 64].any() and (loss[t - 64:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gradients_into_other_columns_of_the_same_buffer(lib, dtype):
+    """Logits and gradient are slices of one wide buffer, side by side, in either order, of several widths."""
+    for t, v, gap, wide in ((7, 1001, 0, 2002), (7, 1001, 3, 2010), (300, 333, 1, 700), (1, 40, 0, 80)):
+        x, ids, z, scale = case(t, v, 9, dtype, torch.float32, 81)
+        for at, to in ((0, v + gap), (v + gap, 0)):
+            big = torch.full((t, wide), 7.0, dtype=dtype, device="cuda")
+            big[:, at:at + v] = x.cuda()
+            part, out = big[:, at:at + v], big[:, to:to + v]
+            _, want = step(lib, x, ids, z, 1.0, scale, 16.0, xd=part)
+            step(lib, x, ids, z, 1.0, scale, 16.0, xd=part, out=(torch.empty(t, device="cuda"), out))
+            assert torch.equal(out, want)
+            out.fill_(7.0)
+            i, y = ids.cuda(), z.cuda()
+            loss, norm = lib.distill_join(lib.distill_parts(part, i, y, vocab=v)[None], i, y, vocab=v)
+            lib.distill_grad(part, i, y, norm, row_scale=scale.cuda(), coef=16.0, vocab=v, out=out)
+            check(x, ids, z, 1.0, scale, 16.0, loss, out)
+            assert torch.equal(part.cpu(), x)
+            rest = torch.ones(wide, dtype=torch.bool)
+            rest[at:at + v] = rest[to:to + v] = False
+            assert (big[:, rest.cuda()] == 7).all()
+
+
+def test_gradients_into_shared_columns_are_refused(lib):
+    big = torch.zeros(5, 200, dtype=torch.bfloat16, device="cuda")
+    ids, z = torch.zeros(5, 2, dtype=torch.int32, device="cuda"), torch.zeros(5, 2, device="cuda")
+    loss = torch.zeros(5, device="cuda")
+    for a, b, shared in ((big[:, :90], big[:, 89:179], True), (big[:, 89:179], big[:, :90], True),
+                         (big[:, :90], big[:, 90:180], False), (big[:, 110:], big[:, 19:109], False),
+                         (big[:4, 100:190], big[1:, 50:140], True), (big[1:, 50:140], big[:4, 100:190], True),
+                         (big[:4, 100:190], big[1:, 10:100], False), (big[1:, 110:200], big[:4, 10:100], False),
+                         (big.view(-1)[:900].view(5, 180)[:, :80], big[:, 90:170], True)):  # rows at other distances
+        n = a.shape[0]
+        call = lambda: lib.distill_step(a, ids[:n], z[:n], out=(loss[:n], b))
+        if shared:
+            with pytest.raises(lib.SimError):
+                call()
+        else:
+            call()
+    torch.cuda.synchronize()
