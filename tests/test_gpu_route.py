@@ -452,3 +452,38 @@ def test_the_per_thread_stream(lib):
                          stream=2) == 0  # hipStreamPerThread
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("t,e,k", [(40003, 256, 8), (9001, 1024, 32), (70001, 100, 12), (140007, 32, 4)])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("normalize", [False, True])
+def test_more_rows_than_the_grid_takes_at_once(lib, dtype, normalize, t, e, k):
+    """Every workgroup goes over its rows several times: a few distinct rows over and over, each repeat with the bits
+    of the first."""
+    n = 37
+    x = logits(n, e, dtype, 70 + e)
+    x[5] = -INF
+    keep = torch.arange(n) % 7 != 3
+    x[~keep] = float("nan")
+    pick = torch.arange(t) % n
+    reps = torch.bincount(pick, minlength=n)
+    on = pick.cuda()
+    xd, kd = x.cuda()[on], keep.cuda()[on]
+    chosen, w, counts, sums = lib.route(xd, k, keep=kd, normalize=normalize)
+    want, ww, _, _, wtol, _ = oracle.route(x, k, keep, normalize)
+    assert torch.equal(chosen[:n].cpu(), want)
+    oracle.assert_within(w[:n], ww, wtol, "weights")
+    assert torch.equal(chosen, chosen[:n][on]) and torch.equal(w, w[:n][on])
+    each = [oracle.route(x[i:i + 1], k, keep[i:i + 1], normalize) for i in range(n)]
+    assert torch.equal(counts.cpu().long(), sum(int(reps[i]) * r[2].long() for i, r in enumerate(each)))
+    total = sum(int(reps[i]) * r[3] for i, r in enumerate(each))
+    oracle.assert_within(sums, total, sum(int(reps[i]) * r[5] for i, r in enumerate(each)) + t * oracle.U * total, "prob_sums")
+    dw = torch.randn(n, k, generator=torch.Generator().manual_seed(9))
+    dwd = dw.cuda()[on]
+    loss, d = lib.route_grad(xd, chosen, dwd, counts, sums, 30.0, keep=kd, normalize=normalize)
+    check_grad_values(x, want, dw, counts.cpu(), 30.0, keep, normalize, d[:n])
+    assert torch.equal(d, d[:n][on])
+    oracle.assert_within(loss, oracle.balance_loss(None, counts.cpu(), sums.cpu(), k, 30.0).reshape(1),
+                         (e + 16) * oracle.U * loss.abs().cpu().double())
+    lib.route_grad(xd, chosen, dwd, counts, sums, 30.0, keep=kd, normalize=normalize, out=(loss, xd))  # over its logits
+    assert torch.equal(xd, d)
