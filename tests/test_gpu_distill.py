@@ -517,3 +517,60 @@ def test_gradients_into_shared_columns_are_refused(lib):
         else:
             call()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("t,v,first,wide", [(6, 9000, 1, 9011), (530, 1234, 3, 1301), (530, 20001, 5, 20013),
+                                            (1040, 500, 1, 503), (4, 33333, 0, 33333)])
+def test_shards_inside_wider_rows(lib, dtype, t, v, first, wide):
+    """Shards are column slices of one buffer, at any alignment, their gradients slices of another."""
+    x, ids, z, scale = case(t, v, 12, dtype, dtype, 82)
+    big = torch.full((t, wide), 5.0, dtype=dtype, device="cuda")
+    big[:, first:first + v] = x.cuda()
+    out = torch.full((t, wide + 3), 7.0, dtype=dtype, device="cuda")
+    i, y, sc = ids.cuda(), z.cuda(), scale.cuda()
+    cut = [0, v // 3, v // 3 + 8, v]
+    xs = [big[:, first + a:first + b] for a, b in zip(cut, cut[1:])]
+    ds = [out[:, 2 + a:2 + b] for a, b in zip(cut, cut[1:])]
+    parts = [lib.distill_parts(s, i, y, temperature=1.5, first=a, vocab=v) for s, a in zip(xs, cut)]
+    loss, norm = lib.distill_join(torch.stack(parts), i, y, temperature=1.5, vocab=v)
+    for s, a, d in zip(xs, cut, ds):
+        lib.distill_grad(s, i, y, norm, temperature=1.5, row_scale=sc, coef=64.0, first=a, vocab=v, out=d)
+    check(x, ids, z, 1.5, scale, 64.0, loss, out[:, 2:2 + v])
+    assert (out[:, :2] == 7).all() and (out[:, 2 + v:] == 7).all()
+    for s, a, d in zip(xs, cut, ds):  # over its logits
+        lib.distill_grad(s, i, y, norm, temperature=1.5, row_scale=sc, coef=64.0, first=a, vocab=v, out=s)
+        assert torch.equal(s, d)
+    assert (big[:, :first] == 5).all() and (big[:, first + v:] == 5).all()
+
+
+def test_shards_with_offsets_past_32_bits(lib):
+    v, rows, ld = 2001, 5, (1 << 30) + 1  # rows at either alignment
+    big = torch.empty(4 * ld + v, dtype=torch.bfloat16, device="cuda")
+    part = big.as_strided((rows, v), (ld, 1))
+    x, ids, z, scale = case(rows, v, 9, torch.bfloat16, torch.float32, 83)
+    part.copy_(x)
+    i, y = ids.cuda(), z.cuda()
+    loss, norm = lib.distill_join(lib.distill_parts(part, i, y, vocab=v)[None], i, y, vocab=v)
+    lib.distill_grad(part, i, y, norm, row_scale=scale.cuda(), coef=4.0, vocab=v, out=part)
+    check(x, ids, z, 1.0, scale, 4.0, loss, part)
+
+
+@pytest.mark.parametrize("tdtype", DTYPES)
+@pytest.mark.parametrize("t", [8, 600])
+def test_an_infinite_teacher_stays_in_its_row(lib, tdtype, t):
+    v, k = 3001, 9
+    x, ids, z, scale = case(t, v, k, torch.bfloat16, tdtype, 84, holes=False)
+    z[0, 3] = INF
+    z[1] = INF
+    z[2, 4], z[2, 5] = INF, -INF
+    z[3, 2], z[3, 6] = INF, NAN
+    ids[4, 1], z[4, 1] = -1, INF       # an empty slot holds anything
+    z[5, :] = -INF
+    z[5, 0] = INF
+    loss, d = step(lib, x, ids, z, 1.5, scale, 2.0)
+    check(x, ids, z, 1.5, scale, 2.0, loss, d)
+    assert torch.isnan(loss[[0, 1, 2, 3, 5]]).all() and torch.isfinite(loss[[4, 6, 7]]).all()
+    for p in (1, 3):
+        loss, d, _ = shards(lib, x, ids, z, 1.5, scale, 2.0, p)
+        check(x, ids, z, 1.5, scale, 2.0, loss, d)
