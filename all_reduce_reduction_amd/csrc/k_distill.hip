@@ -275,6 +275,13 @@ __global__ void __launch_bounds__(B) k_distill_grad(DistillArgs a) {
 
 }  // namespace
 
+// A step takes one workgroup per row where that holds the row in registers, or
+// where half the compute units have a row each; two launches over runs of
+// columns otherwise (they read the row twice, but by more workgroups).  Measured
+// (us, bf16, whole / runs): 1 row x 32,768 6.2 / 9.2, 160 x 200,003 31.8 / 46.4,
+// 64 x 200,003 27.6 / 21.6.  Both limits are round numbers, and near them the
+// other side can be the faster one: 1 x 131,072 14.2 / 9.5, 64 x 131,072 16.6 /
+// 15.5, 127 x 200,003 29.4 / 35.6.
 bool distill_whole_rows(int64_t rows, int64_t cols, int dtype) {
   const int v = dtype == SIM_FP32 ? 4 : 8;
   if (cols <= v) return false;
@@ -327,7 +334,10 @@ hipError_t grad_dtype(const DistillArgs& a, hipStream_t s) {
 
 // Whether a workgroup waits for the slots before it reads its columns, to
 // leave out rows without any: where eight or more workgroups share a compute
-// unit, others fill the wait; with fewer it would be part of the call's time.
+// unit, others fill the wait (statistics and gradient, us, looking / not: 4,096
+// rows x 16,384 bf16, half of them empty, 18.5 and 34.5 / 24.2 and 46.3, none
+// empty 25.1 and 47.4 / 24.8 and 47.3).  With fewer, little is to be gained: 400
+// x 12,505, half of them empty, 5.2 and 7.3 / 5.3 and 8.1.
 DistillArgs with_look(const DistillArgs& in) {
   DistillArgs a = in;
   a.look_first = a.rows * a.splits >= 8 * (int64_t)library_cus();

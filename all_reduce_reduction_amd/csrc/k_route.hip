@@ -311,7 +311,7 @@ __device__ __forceinline__ void sum_in_last(const RouteArgs& a, uint32_t* word_s
 // (bf16, top 8; one wave per row with eight rounds of a wave-wide maximum: 370).
 // 16-bit rows keep 32 logits per lane, so that 8 rows share a wave's cross-lane
 // steps (16 per lane: 22 us); fp32 rows 16, as their keys and values take twice
-// the registers (32 per lane: 36 us against 32).
+// the registers (32 per lane: 36 us against 32; 28.6 since).
 template <int DT, int L, int N, bool MANY>
 __global__ void __launch_bounds__(kBlock, N == 32 ? 3 : 4) k_route(RouteArgs a) {
   typedef Gate<DT, L, N> G;
@@ -682,6 +682,10 @@ hipError_t grad_dtype(const RouteGradArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// At most two workgroups per compute unit where a lane holds 32 logits, whose
+// registers let no more of them be under way (65,536 rows x 256 bf16: 19.2 us, with
+// four 20.4); four otherwise (65,536 x 256 fp32 28.6, with two 32.3; x 128 bf16
+// 14.7 and 15.1).
 int route_workgroups(int64_t tokens, int experts, int dtype) {
   const int n = dtype == SIM_FP32 ? 16 : 32;
   const int rows = experts <= 32 ? 16 : experts <= 128 ? 8 : 64 * n / (experts <= 256 ? 256 : experts <= 512 ? 512 : 1024);

@@ -148,7 +148,7 @@ struct Tail {
 // under what a sum that holds 1 can see)
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Reductions over groups of L = 8, 16, 32 or 64 neighbouring lanes without
+// Reductions over groups of L = 4, 8, 16, 32 or 64 neighbouring lanes without
 // LDS: with the partner in the pair, in the quad, in the mirrored half row and
 // in the mirrored row by DPP, then between the two rows of 16 of a half wave
 // and between the half waves by lane swaps.  Both partners combine the same
@@ -247,12 +247,6 @@ struct Running {
 // factor that brings a sum taken against m over to the maximum top >= m
 __device__ __forceinline__ float rebase(float m, float top, float c) {
   return m == top ? 1.0f : exp2_hw((m - top) * c);
-}
-__device__ __forceinline__ Running running_join(const Running& a, const Running& b, float c) {
-  Running r;
-  r.m = fmaxf(a.m, b.m);
-  r.s = a.s * rebase(a.m, r.m, c) + b.s * rebase(b.m, r.m, c);
-  return r;
 }
 __device__ __forceinline__ Running wave_running(Running r, float c) {
   const float top = wave_max(r.m);

@@ -454,8 +454,9 @@ int sim_verify_custom(int algo, int p, int nchunks, int rounds, int nsteps, cons
  *     between them: other columns of the same wide rows.  Any overlap of an
  *     output with an input or another output but the first is SIM_ERR_ALIAS.
  *   - Statistics are fp32 whatever `dtype` is, and every sum is taken in an
- *     order that depends on the sizes alone: the same call on the same data
- *     gives the same bits.
+ *     order that depends on the sizes alone and, for distillation from 16-bit
+ *     logits, on which rows start in the middle of a 4-byte word: the same
+ *     call on the same data in such places gives the same bits.
  *   - Of library memory only one counter is used, by a small sim_route call
  *     outside of capture, for as long as the call's stream work takes.  `work`
  *     is the caller's scratch of at least the bytes the matching *_work
