@@ -112,12 +112,12 @@ struct Ctx {
   bool capturing = false;  // the current call's stream is being captured into a graph
   bool captured = false;   // some call has been captured since sim_init
   // counters of the launches whose last workgroup finishes the work, handed out
-  // in turn: how often each was, and (in pinned host memory) how often the
-  // launch has reported back
+  // in turn: how often each was, what its launches have counted up to, and (in
+  // pinned host memory) the last launch that has reported back
   uint32_t* turns = nullptr;
   uint32_t* turns_done = nullptr;      // the host's address
   uint32_t* turns_dev_done = nullptr;  // the device's
-  std::vector<uint32_t> turn_calls;
+  std::vector<uint32_t> turn_calls, turn_base;
   uint32_t turn_next = 0;
   int route_launches = 0;  // kernels of the last routing call
   std::vector<void*> retired;  // outgrown scratch a captured graph may still use
@@ -1351,12 +1351,13 @@ Turn library_turn(hipStream_t stream) {
     g.turn_next = (i + 1) % kTurns;
     return none;
   }
-  return Turn{g.turns + (size_t)i * kTurnWords, g.turns_dev_done + i, g.turn_calls[i] + 1};
+  return Turn{g.turns + (size_t)i * kTurnWords, g.turn_base[i], g.turns_dev_done + i, g.turn_calls[i] + 1};
 }
-void library_turn_used(const Turn& t, int launches) {
+void library_turn_used(const Turn& t, int workgroups, int launches) {
   g.route_launches = launches;
   if (!t.word) return;
   g.turn_calls[g.turn_next] = t.call;
+  g.turn_base[g.turn_next] += (uint32_t)workgroups;
   g.turn_next = (g.turn_next + 1) % kTurns;
 }
 
@@ -1488,6 +1489,7 @@ int sim_init(int device, int p_max, size_t max_bytes_per_rank) {
     }
     std::memset(g.turns_done, 0, kTurns * 4);
     g.turn_calls.assign(kTurns, 0);
+    g.turn_base.assign(kTurns, 0);
   }
   // the pointer table only makes launches cheaper: without it every call
   // carries its pointers in its kernel arguments

@@ -163,7 +163,7 @@ int sim_route(const void* logits, int64_t row_stride, int dtype, const uint8_t* 
   const RouteArgs a{logits, row_stride, keep, tokens, experts, topk, normalize != 0, chosen, weights, counts, prob_sums,
                     (uint32_t*)work, wg, turn};
   const hipError_t e = launch_route(a, dtype, (hipStream_t)stream);
-  if (e == hipSuccess) library_turn_used(turn, wg == 1 || turn.word ? 1 : 2);
+  if (e == hipSuccess) library_turn_used(turn, wg, wg == 1 || turn.word ? 1 : 2);
   return hip_status(e);
 }
 

@@ -262,8 +262,9 @@ __device__ __forceinline__ void put(uint32_t* p, uint32_t v) {
 }
 
 // The workgroup that arrives last adds up what all of them have written, in
-// the workgroups' order.  No workgroup waits for another one.  This takes a
-// launch less than k_route_sum (1,003 rows x 60 fp32, top 4: 7.2 us against
+// the workgroups' order.  No workgroup waits for another one.  From its arrival
+// on nobody touches the counter, so it reports that first.  This takes a launch
+// less than k_route_sum (1,003 rows x 60 fp32, top 4: 7.2 us against
 // 9.7).
 __device__ __forceinline__ void sum_in_last(const RouteArgs& a, uint32_t* word_s) {
   constexpr int kFlight = 32;  // loads of a thread under way (16: 9.3 us where 32 take 8.5)
@@ -271,7 +272,8 @@ __device__ __forceinline__ void sum_in_last(const RouteArgs& a, uint32_t* word_s
   __syncthreads();
   if (threadIdx.x == 0) *word_s = __hip_atomic_fetch_add(a.turn.word, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
-  if (*word_s != (uint32_t)a.workgroups - 1) return;
+  if (*word_s != a.turn.base + (uint32_t)a.workgroups - 1) return;
+  if (threadIdx.x == 0) __hip_atomic_store(a.turn.done, a.turn.call, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
   const int all = 2 * a.experts + 1;
   for (int e = threadIdx.x; e < all; e += kBlock) {
     uint32_t n = 0;
@@ -293,11 +295,6 @@ __device__ __forceinline__ void sum_in_last(const RouteArgs& a, uint32_t* word_s
     }
     if (e <= a.experts) a.counts[e] = (int32_t)n;
     else a.sums[e - a.experts - 1] = s;
-  }
-  if (threadIdx.x == 0) {
-    put(a.turn.word, 0);
-    wait_stores();
-    __hip_atomic_store(a.turn.done, a.turn.call, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
   }
 }
 

@@ -18,21 +18,23 @@ namespace simar {
 bool library_ready();
 int library_device();
 int library_cus();
-// A word of device memory for one launch alone, 0 before it.  The launch leaves
-// 0 there and then reports `call` to `done`, in host memory; only then is the
-// word handed out again, so that no two launches can meet in it, on whatever
+// A word of device memory for one launch alone.  Each of its workgroups adds 1
+// to it, and the last one reports `call` to `done`, in host memory; only then is
+// the word handed out again, so that no two launches can meet in it, on whatever
 // streams they are.  A launch that should ever end without its report keeps its
 // word for good.
 struct Turn {
   uint32_t* word;  // NULL: none
+  uint32_t base;   // what the word holds before the launch
   uint32_t* done;
   uint32_t call;
 };
 // A word for the next launch on `stream`; none for a captured one (its graph is
 // replayed with the same arguments) or while the next word is still in use.
 Turn library_turn(hipStream_t stream);
-// That launch was made, with `launches` kernels in all.
-void library_turn_used(const Turn& t, int launches);
+// That launch was made, of `workgroups` workgroups and with `launches` kernels
+// in all.
+void library_turn_used(const Turn& t, int workgroups, int launches);
 
 struct RouteArgs {
   const void* x;
