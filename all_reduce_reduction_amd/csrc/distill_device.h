@@ -95,10 +95,11 @@ __device__ __forceinline__ Slots make_slots(const DistillArgs& a, const SlotLoad
   return s;
 }
 
-// (a - b) / tau, whose difference alone may lie past fp32's range (a masked
-// logit of the type's lowest value beside a large one); halves are exact
-__device__ __forceinline__ float distance(float a, float b, float tau) {
-  return 2.0f * ((0.5f * a - 0.5f * b) / tau);
+// q (a - b) / tau for q <= 1, of which the difference, or the difference over
+// tau, may lie past fp32's range where the whole does not (a masked logit of the
+// type's lowest value); halves are exact
+__device__ __forceinline__ float times_distance(float q, float a, float b, float tau) {
+  return 2.0f * (q * (0.5f * a - 0.5f * b) / tau);
 }
 
 __device__ __forceinline__ void* row_at(const void* base, int64_t row, int64_t stride, int esize) {
@@ -213,8 +214,8 @@ __device__ __forceinline__ Part join_two(const Part& p, const Part& q, float tau
   t.s = p.s * rebase(p.m, t.m, c) + q.s * rebase(q.m, t.m, c);
   t.a = p.a + q.a;
   // (a part without slots moves nothing, wherever its own maximum is)
-  const float dp = p.a == 0.0f || p.m == t.m ? 0.0f : p.a * distance(p.m, t.m, tau);
-  const float dq = q.a == 0.0f || q.m == t.m ? 0.0f : q.a * distance(q.m, t.m, tau);
+  const float dp = p.a == 0.0f || p.m == t.m ? 0.0f : times_distance(p.a, p.m, t.m, tau);
+  const float dq = q.a == 0.0f || q.m == t.m ? 0.0f : times_distance(q.a, q.m, t.m, tau);
   t.d = (p.d + dp) + (q.d + dq);
   return t;
 }

@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(NT, 4) k_distill_row(DistillArgs a) {
       if (64 * i >= a.topk) break;
       if (sl.id[i] < 0 || sl.q[i] == 0.0f) continue;
       const float at = slots.x[lane + 64 * i];
-      dot += at == kNegInf ? sl.q[i] * kNegInf : sl.q[i] * distance(at, r.m, a.tau);
+      dot += at == kNegInf ? sl.q[i] * kNegInf : times_distance(sl.q[i], at, r.m, a.tau);
     }
     dot = wave_sum(dot);
     if (lane == 0) a.loss[row] = live ? sl.entropy + __logf(r.s) - dot : 0.0f;

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(B) k_distill_stats(DistillArgs a) {
       if (64 * i >= a.topk) break;
       if (sl.q[i] == 0.0f) continue;
       mass += sl.q[i];
-      dot += at[i] == kNegInf ? sl.q[i] * kNegInf : sl.q[i] * distance(at[i], r.m, a.tau);
+      dot += at[i] == kNegInf ? sl.q[i] * kNegInf : times_distance(sl.q[i], at[i], r.m, a.tau);
     }
     mass = wave_sum(mass);
     dot = wave_sum(dot);

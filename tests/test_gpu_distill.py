@@ -574,3 +574,28 @@ def test_an_infinite_teacher_stays_in_its_row(lib, tdtype, t):
     for p in (1, 3):
         loss, d, _ = shards(lib, x, ids, z, 1.5, scale, 2.0, p)
         check(x, ids, z, 1.5, scale, 2.0, loss, d)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("t", [6, 600])
+def test_a_slot_of_little_mass_on_a_masked_logit(lib, dtype, t):
+    """The slot's mass brings a distance over the temperature that is past fp32's range back into it."""
+    v, k = 2100, 5
+    x, ids, z, _ = case(t, v, k, dtype, torch.float32, 85, holes=False)
+    low = torch.finfo(dtype).min
+    ids[:4] = torch.arange(k, dtype=torch.int32) * 400 + 7
+    x[0, 7] = low                            # one masked logit with a slot
+    z[0, 0] = z[0].max() - 12.0
+    x[1, :1050] = low                        # masked up to the middle
+    z[1, :3] = z[1].max() - 14.0
+    x[2, 407] = low
+    z[2, 1] = z[2].max() - 25.0
+    x[3, 1050:] = low
+    z[3, 3:] = z[3].max() - 16.0
+    for tau in (0.9, 0.5, 0.3):
+        loss, d = step(lib, x, ids, z, tau)
+        check(x, ids, z, tau, None, 1.0, loss, d, f"tau {tau}")
+        assert torch.isfinite(loss).all()
+        for p in (1, 2, 3):
+            loss, d, _ = shards(lib, x, ids, z, tau, None, 1.0, p)
+            check(x, ids, z, tau, None, 1.0, loss, d, f"{p} shards, tau {tau}")
