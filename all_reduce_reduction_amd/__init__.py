@@ -49,6 +49,7 @@ DEBUG = {"epoch": 0, "spin_limit": 1, "ll_wait_skew": 2, "fill_ll": 3, "log": 4,
          "phased_layout": 18, "phased_whole_last": 19, "route_launches": 20}
 MAX_RANKS = 16
 ROUTE_MAX_EXPERTS, ROUTE_MAX_TOPK, DISTILL_MAX_TOPK = 1024, 32, 256
+NORM_MAX_COLUMNS, CLIP_MAX_TENSORS = 32768, 65536
 LL_MAX_BYTES_PER_RANK = 1 << 20
 
 
@@ -102,6 +103,16 @@ def _load() -> ctypes.CDLL:
         "sim_distill_parts": ([vp, i64, i, i64, i64, i64, i64, vp, vp, i, i, f, vp, vp, sz, vp], i),
         "sim_distill_join": ([vp, i, i64, i64, vp, vp, i, i, f, vp, vp, vp], i),
         "sim_distill_grad": ([vp, i64, i, i64, i64, i64, i64, vp, vp, i, i, f, vp, vp, f, vp, i64, vp], i),
+        "sim_norm": ([vp, i64, i, vp, i64, i64, i64, vp, i, f, vp, i64, vp, i64, vp, i, vp], i),
+        "sim_norm_grad_work": ([i64, i64, i, psz], i),
+        "sim_norm_grad": ([vp, i64, i, i64, i64, vp, i, f, vp, i64, vp, i64, vp, i64, vp, vp, sz, vp], i),
+        "sim_dispatch_work": ([i64, i, i, psz], i),
+        "sim_dispatch": ([vp, i64, i64, vp, i64, vp, i64, i, i, vp, i64, vp, vp, vp, vp, sz, vp], i),
+        "sim_combine": ([vp, i64, i, i64, i64, vp, vp, i64, i, vp, i64, vp], i),
+        "sim_combine_grad": ([vp, i64, i, vp, i64, i64, i64, vp, vp, i64, i, vp, i64, vp, vp], i),
+        "sim_clip_work": ([vp, vp, i, psz], i),
+        "sim_clip_norm": ([vp, vp, vp, i, vp, vp, sz, vp], i),
+        "sim_clip": ([vp, vp, vp, vp, i, vp, i, f, vp, vp, sz, vp], i),
         "sim_status_string": ([i], ctypes.c_char_p),
         "sim_version": ([], i),
     }
@@ -145,18 +156,28 @@ CALIBRATION = os.path.join(_HERE, "calib", "mi355x.json")
 
 
 # ---- the C functions, one to one ------------------------------------------------
+_device: Optional[int] = None  # the one that sim_init chose
+
+
+def _forget_sizes() -> None:
+    for f in (sim_route_work, sim_distill_work, sim_norm_grad_work, sim_dispatch_work):
+        f.cache_clear()
+
+
 def sim_init(device: int = 0, p_max: int = MAX_RANKS, max_bytes_per_rank: int = 0) -> None:
-    sim_route_work.cache_clear()
-    sim_distill_work.cache_clear()
+    global _device
+    _forget_sizes()
     _check(lib.sim_init(device, p_max, max_bytes_per_rank), "sim_init")
+    _device = device
     if not os.environ.get("SIM_CALIB") and os.path.exists(CALIBRATION):
         sim_model_load(CALIBRATION)
 
 
 def sim_finalize() -> None:
-    sim_route_work.cache_clear()
-    sim_distill_work.cache_clear()
+    global _device
+    _forget_sizes()
     _check(lib.sim_finalize(), "sim_finalize")
+    _device = None
 
 
 def sim_allreduce(in_ptrs, out_ptrs, p, n, dtype, op, algo, stream=0) -> int:
@@ -310,6 +331,81 @@ def sim_distill_grad(logits, row_stride, dtype, rows, columns, first, vocab, ids
                                 coef, dlogits, drow_stride, stream or None)
 
 
+def sim_norm(x, x_stride, dtype, residual, residual_stride, rows, columns, gain, gain_dtype, eps, sum, sum_stride, out,
+             out_stride, scales, group, stream=0) -> int:
+    return lib.sim_norm(x, x_stride, _code(DTYPES, dtype, "dtype"), residual, residual_stride, rows, columns, gain,
+                        _code(DTYPES, gain_dtype, "dtype"), eps, sum, sum_stride, out, out_stride, scales, group,
+                        stream or None)
+
+
+@functools.lru_cache(maxsize=1024)
+def sim_norm_grad_work(rows: int, columns: int, dtype) -> int:
+    """Workspace bytes of sim_norm_grad with a dgain."""
+    n = ctypes.c_size_t(0)
+    _check(lib.sim_norm_grad_work(rows, columns, _code(DTYPES, dtype, "dtype"), ctypes.byref(n)), "sim_norm_grad_work")
+    return n.value
+
+
+def sim_norm_grad(h, h_stride, dtype, rows, columns, gain, gain_dtype, eps, dy, dy_stride, dsum, dsum_stride, dx,
+                  dx_stride, dgain, work, work_bytes, stream=0) -> int:
+    return lib.sim_norm_grad(h, h_stride, _code(DTYPES, dtype, "dtype"), rows, columns, gain,
+                             _code(DTYPES, gain_dtype, "dtype"), eps, dy, dy_stride, dsum, dsum_stride, dx, dx_stride,
+                             dgain, work, work_bytes, stream or None)
+
+
+@functools.lru_cache(maxsize=1024)
+def sim_dispatch_work(tokens: int, topk: int, experts: int) -> int:
+    """Workspace bytes of sim_dispatch."""
+    n = ctypes.c_size_t(0)
+    _check(lib.sim_dispatch_work(tokens, topk, experts, ctypes.byref(n)), "sim_dispatch_work")
+    return n.value
+
+
+def sim_dispatch(x, x_pitch, row_bytes, scales, groups, chosen, tokens, topk, experts, rows, rows_pitch, row_scales,
+                 place, offsets, work, work_bytes, stream=0) -> int:
+    return lib.sim_dispatch(x, x_pitch, row_bytes, scales, groups, chosen, tokens, topk, experts, rows, rows_pitch,
+                            row_scales, place, offsets, work, work_bytes, stream or None)
+
+
+def sim_combine(rows, rows_stride, dtype, nrows, columns, place, weights, tokens, topk, out, out_stride,
+                stream=0) -> int:
+    return lib.sim_combine(rows, rows_stride, _code(DTYPES, dtype, "dtype"), nrows, columns, place, weights, tokens,
+                           topk, out, out_stride, stream or None)
+
+
+def sim_combine_grad(dy, dy_stride, dtype, rows, rows_stride, nrows, columns, place, weights, tokens, topk, drows,
+                     drows_stride, dweights, stream=0) -> int:
+    return lib.sim_combine_grad(dy, dy_stride, _code(DTYPES, dtype, "dtype"), rows, rows_stride, nrows, columns, place,
+                                weights, tokens, topk, drows, drows_stride, dweights, stream or None)
+
+
+def _host_array(values, ctype):
+    """A host array of a C call (None: none)."""
+    return None if values is None else (ctype * len(values))(*values)
+
+
+def sim_clip_work(counts, dtypes) -> int:
+    """Workspace bytes of sim_clip_norm, and of sim_clip without parts, over tensors of these sizes and types."""
+    n = ctypes.c_size_t(0)
+    _check(lib.sim_clip_work(_host_array(counts, ctypes.c_int64),
+                             _host_array([_code(DTYPES, d, "dtype") for d in dtypes], ctypes.c_int), len(counts),
+                             ctypes.byref(n)), "sim_clip_work")
+    return n.value
+
+
+def sim_clip_norm(grads, counts, dtypes, norm, work, work_bytes, stream=0) -> int:
+    return lib.sim_clip_norm(_host_array(grads, ctypes.c_void_p), _host_array(counts, ctypes.c_int64),
+                             _host_array([_code(DTYPES, d, "dtype") for d in dtypes], ctypes.c_int), len(grads), norm,
+                             work, work_bytes, stream or None)
+
+
+def sim_clip(grads, outs, counts, dtypes, parts, nparts, max_norm, norm, work, work_bytes, stream=0) -> int:
+    return lib.sim_clip(_host_array(grads, ctypes.c_void_p), _host_array(outs, ctypes.c_void_p),
+                        _host_array(counts, ctypes.c_int64),
+                        _host_array([_code(DTYPES, d, "dtype") for d in dtypes], ctypes.c_int), len(grads), parts,
+                        nparts, max_norm, norm, work, work_bytes, stream or None)
+
+
 def sim_config_set(key, value: int) -> None:
     _check(lib.sim_config_set(_code(CONFIG, key, "config key"), int(value)), "sim_config_set")
 
@@ -455,7 +551,8 @@ if torch is not None:
     _F32, _I32, _MASK = (torch.float32,), (torch.int32,), (torch.bool, torch.uint8)
     _FLOATS = tuple(_TORCH_CODE)
 
-_ENTRIES = ("route", "route_grad", "distill_step", "distill_parts", "distill_join", "distill_grad")
+_ENTRIES = ("route", "route_grad", "distill_step", "distill_parts", "distill_join", "distill_grad", "norm", "norm_grad",
+            "dispatch", "combine", "combine_grad", "clip_norm", "clip")
 
 
 def _vec_py(t, what, dtypes, device, *shape):
@@ -480,7 +577,7 @@ def _rows_py(t, what, like):
         raise ValueError(f"unsupported dtype {t.dtype}")
     got = (t.data_ptr(), st[0] if n > 1 else c, n, c, _TORCH_CODE[t.dtype], t.get_device())
     if like is not None and got[2:] != like[2:]:
-        raise ValueError(f"{what} must have the logits' shape, dtype and device")
+        raise ValueError(f"{what} must have the first tensor's shape, dtype and device")
     return got
 
 
@@ -493,17 +590,46 @@ def _slots_py(ids, teacher, dtypes, rows, device):
             _TORCH_CODE[teacher.dtype], k)
 
 
-if hasattr(_pycall, "slots") and torch is not None:
+def _raw_py(t, what, dtype):
+    """(pointer, bytes from row to row, rows, bytes of a row, device index) of a 2-D device tensor of any type whose
+    rows are contiguous; dtype: the one it must have, or None."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{what} must be a 2-D device tensor")
+    n, c = t.shape
+    st = t.stride()
+    if st[1] != 1 and c > 1:
+        raise ValueError(f"{what}'s rows must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be of type {dtype}")
+    e = t.element_size()
+    return t.data_ptr(), (st[0] if n > 1 else c) * e, n, c * e, t.get_device()
+
+
+def _tensors_py(ts, what, device, like):
+    """(pointers, counts, type codes), each an array of the host, of contiguous tensors on that device; like: None, or
+    such a tuple whose counts and types they must have."""
+    for i, t in enumerate(ts):
+        if t.dtype not in _TORCH_CODE or t.get_device() != device or not t.is_contiguous():
+            raise ValueError(f"{what}[{i}] must be a contiguous tensor of one of the float types on cuda:{device}")
+    got = (_host_array([t.data_ptr() for t in ts], ctypes.c_void_p), _host_array([t.numel() for t in ts], ctypes.c_int64),
+           _host_array([_TORCH_CODE[t.dtype] for t in ts], ctypes.c_int))
+    if like is not None and (list(got[1]) != list(like[1]) or list(got[2]) != list(like[2])):
+        raise ValueError(f"{what} must have the gradients' sizes and types")
+    return got
+
+
+if hasattr(_pycall, "tensors") and torch is not None:
     # arguments converted and tensors checked in C: of a small call's 7.3 us on the host, ctypes and the same checks
     # in Python took about 3
     for _name in _ENTRIES:
         _pycall.bind(_name, ctypes.cast(lib["sim_" + _name], ctypes.c_void_p).value)
     _pycall.types(*_FLOATS)
     _entry, _vec, _rows, _slots = _pycall, _pycall.pointer, _pycall.rows, _pycall.slots
+    _raw, _tensors = _pycall.raw, _pycall.tensors
 else:
     import types as _types
     _entry, _vec = _types.SimpleNamespace(**{n: getattr(lib, "sim_" + n) for n in _ENTRIES}), _vec_py
-    _rows, _slots = _rows_py, _slots_py
+    _rows, _slots, _raw, _tensors = _rows_py, _slots_py, _raw_py, _tensors_py
 
 
 def _on(stream, device):
@@ -647,3 +773,201 @@ def distill_grad(logits, ids, teacher, norm, temperature: float = 1.0, row_scale
                                _vec(row_scale, "row_scale", _F32, dev, n), coef, dptr, dld, _on(stream, dev)),
            "sim_distill_grad")
     return out
+
+
+# ---- around the experts, and before the optimizer (torch tensors; marshalling only) --
+_E4M3 = getattr(torch, "float8_e4m3fn", None)
+
+
+def _here(device):
+    """The library works on one device: tensors elsewhere are the caller's error."""
+    if _device is not None and device != _device:
+        raise ValueError(f"tensors must be on cuda:{_device}, the device that sim_init chose")
+
+
+def _gain(gain, columns, device):
+    """(pointer, type code) of a norm's gain (None: all 1)."""
+    if gain is None:
+        return None, 1
+    return _vec(gain, "gain", _FLOATS, device, columns), _TORCH_CODE[gain.dtype]
+
+
+def norm(x, gain=None, residual=None, eps: float = 1e-6, out=None, stream=None):
+    """Root-mean-square norm of the rows of x (+ residual): (y, x + residual; without a residual None); ``sim_norm`` in
+    include/simar.h says what each holds.  out: the same two, to write into (each may be x or residual)."""
+    ptr, ld, n, c, dt, dev = mine = _rows(x, "x", None)
+    _here(dev)
+    if out is None:
+        out = (_empty((n, c), x.dtype, dev, stream),
+               None if residual is None else _empty((n, c), x.dtype, dev, stream))
+    y, total = out
+    yp, yld, *_ = _rows(y, "y", mine)
+    rp, rld, *_ = (None, c) if residual is None else _rows(residual, "residual", mine)
+    tp, tld, *_ = (None, c) if total is None else _rows(total, "total", mine)
+    _check(_entry.norm(ptr, ld, dt, rp, rld, n, c, *_gain(gain, c, dev), eps, tp, tld, yp, yld, None, 0,
+                       _on(stream, dev)), "sim_norm")
+    return out
+
+
+def norm_quant(x, gain=None, residual=None, eps: float = 1e-6, group: int = 128, out=None, stream=None):
+    """The same with y in 8 bits: (float8_e4m3fn [rows, columns], scales fp32 [rows, groups], x + residual or None).
+    group: the columns of a scale, 32, 64 or 128, or all columns of a row."""
+    ptr, ld, n, c, dt, dev = mine = _rows(x, "x", None)
+    _here(dev)
+    if group not in (32, 64, 128, c):
+        raise ValueError("group must be 32, 64, 128 or all columns")
+    groups = 1 if group == c else -(-c // group)
+    if out is None:
+        out = (_empty((n, c), _E4M3, dev, stream), _empty((n, groups), torch.float32, dev, stream),
+               None if residual is None else _empty((n, c), x.dtype, dev, stream))
+    q, scales, total = out
+    qp, qld, qn, qc, qdev = _raw(q, "q", _E4M3)
+    if (qn, qc, qdev) != (n, c, dev):
+        raise ValueError("q must have x's shape and device")
+    rp, rld, *_ = (None, c) if residual is None else _rows(residual, "residual", mine)
+    tp, tld, *_ = (None, c) if total is None else _rows(total, "total", mine)
+    _check(_entry.norm(ptr, ld, dt, rp, rld, n, c, *_gain(gain, c, dev), eps, tp, tld, qp, qld,
+                       _vec(scales, "scales", _F32, dev, n, groups), 0 if group == c else group,
+                       _on(stream, dev)), "sim_norm")
+    return out
+
+
+def norm_grad(total, gain, dout, dtotal=None, eps: float = 1e-6, out=None, stream=None):
+    """Gradient of the norm of `total` (x, or x + residual): (dx, dgain fp32 [columns]); dtotal: the gradient that
+    reaches `total` by another way.  out: the same two, to write into (dx may be any of the three inputs; dgain None:
+    not wanted)."""
+    ptr, ld, n, c, dt, dev = mine = _rows(total, "total", None)
+    _here(dev)
+    if out is None:
+        out = (_empty((n, c), total.dtype, dev, stream), _empty(c, torch.float32, dev, stream))
+    dx, dgain = out
+    dp, dld, *_ = _rows(dx, "dx", mine)
+    op, old, *_ = _rows(dout, "dout", mine)
+    tp, tld, *_ = (None, c) if dtotal is None else _rows(dtotal, "dtotal", mine)
+    nb = 0 if dgain is None else sim_norm_grad_work(n, c, dt)
+    w, wp = _work(nb, dev, stream)
+    _check(_entry.norm_grad(ptr, ld, dt, n, c, *_gain(gain, c, dev), eps, op, old, tp, tld, dp, dld,
+                            _vec(dgain, "dgain", _F32, dev, c), wp, nb, _on(stream, dev)), "sim_norm_grad")
+    return out
+
+
+def dispatch(x, chosen, experts: int, scales=None, out=None, stream=None):
+    """The rows of x [tokens, columns] (any type) sorted by the experts of chosen int32 [tokens, topk]: (rows
+    [tokens * topk, columns], place int32 [tokens, topk], offsets int32 [experts + 1], the rows' scales fp32
+    [tokens * topk, groups]; without scales None); ``sim_dispatch`` in include/simar.h says what each holds.  Rows
+    from offsets[experts] on are not written.  scales: fp32 [tokens, groups] of x.  out: the same four, to write into."""
+    ptr, pitch, n, nb, dev = _raw(x, "x", None)
+    _here(dev)
+    if chosen.dim() != 2:
+        raise ValueError("chosen must be [tokens, topk]")
+    k = chosen.shape[1]
+    groups = 0 if scales is None else scales.shape[-1]
+    if out is None:
+        out = (_empty((n * k, x.shape[1]), x.dtype, dev, stream), _empty((n, k), torch.int32, dev, stream),
+               _empty(experts + 1, torch.int32, dev, stream),
+               None if scales is None else _empty((n * k, groups), torch.float32, dev, stream))
+    rows, place, offsets, row_scales = out
+    rp, rpitch, rn, rnb, rdev = _raw(rows, "rows", x.dtype)
+    if (rn, rnb, rdev) != (n * k, nb, dev):
+        raise ValueError("rows must be [tokens * topk, columns] on x's device")
+    if (scales is None) != (row_scales is None):
+        raise ValueError("scales and the rows' scales: both or neither")
+    wb = sim_dispatch_work(n, k, experts)
+    w, wp = _work(wb, dev, stream)
+    _check(_entry.dispatch(ptr, pitch, nb, _vec(scales, "scales", _F32, dev, n, groups), groups,
+                           _vec(chosen, "chosen", _I32, dev, n, k), n, k, experts, rp, rpitch,
+                           _vec(row_scales, "row_scales", _F32, dev, n * k, groups),
+                           _vec(place, "place", _I32, dev, n, k), _vec(offsets, "offsets", _I32, dev, experts + 1), wp,
+                           wb, _on(stream, dev)), "sim_dispatch")
+    return out
+
+
+def combine(rows, place, weights=None, out=None, stream=None):
+    """The experts' rows back to their tokens, [tokens, columns]: the sum over a token's slots of weights fp32 [tokens,
+    topk] (None: all 1) times rows[place]; ``sim_combine`` in include/simar.h.  out: the result, to write into."""
+    ptr, ld, m, c, dt, dev = _rows(rows, "rows", None)
+    _here(dev)
+    if place.dim() != 2:
+        raise ValueError("place must be [tokens, topk]")
+    n, k = place.shape
+    if out is None:
+        out = _empty((n, c), rows.dtype, dev, stream)
+    op, old, *_ = _rows(out, "out", (None, None, n, c, dt, dev))
+    _check(_entry.combine(ptr, ld, dt, m, c, _vec(place, "place", _I32, dev, n, k),
+                          _vec(weights, "weights", _F32, dev, n, k), n, k, op, old, _on(stream, dev)), "sim_combine")
+    return out
+
+
+def dispatch_grad(drows, place, out=None, stream=None):
+    """The gradient of dispatch for x: combine without weights."""
+    return combine(drows, place, out=out, stream=stream)
+
+
+def combine_grad(dout, rows, place, weights=None, out=None, stream=None):
+    """The gradient of combine for the rows and the weights: (drows, dweights fp32 [tokens, topk]); ``sim_combine_grad``
+    in include/simar.h says what each holds.  Rows that no place names are not written.  out: the same two, to write
+    into (drows may be the rows; either may be None: not wanted)."""
+    dp, dld, n, c, dt, dev = _rows(dout, "dout", None)
+    _here(dev)
+    rp, rld, m, *_ = theirs = _rows(rows, "rows", None)
+    if theirs[3:] != (c, dt, dev):
+        raise ValueError("rows must have dout's columns, dtype and device")
+    if place.dim() != 2:
+        raise ValueError("place must be [tokens, topk]")
+    k = place.shape[1]
+    if out is None:
+        out = (_empty((m, c), rows.dtype, dev, stream), _empty((n, k), torch.float32, dev, stream))
+    drows, dweights = out
+    gp, gld, *_ = (None, c) if drows is None else _rows(drows, "drows", theirs)
+    _check(_entry.combine_grad(dp, dld, dt, rp, rld, m, c, _vec(place, "place", _I32, dev, n, k),
+                               _vec(weights, "weights", _F32, dev, n, k), n, k, gp, gld,
+                               _vec(dweights, "dweights", _F32, dev, n, k), _on(stream, dev)), "sim_combine_grad")
+    return out
+
+
+def _list_device(grads):
+    if not grads:
+        return _device if _device is not None else torch.cuda.current_device()
+    if not grads[0].is_cuda:
+        raise ValueError("grads must be device tensors")
+    return grads[0].get_device()
+
+
+def _clip_work(lists, n, device, stream):
+    """Scratch of a norm over a list: (tensor, pointer, bytes)."""
+    nb = ctypes.c_size_t(0)
+    _check(lib.sim_clip_work(lists[1], lists[2], n, ctypes.byref(nb)), "sim_clip_work")
+    return (*_work(nb.value, device, stream), nb.value)
+
+
+def grad_norm(grads, out=None, stream=None):
+    """The norm over all elements of a list of gradients, fp32 [1] (``sim_clip_norm`` in include/simar.h): a rank's part
+    of clip_grads where each rank holds a part of them.  out: the norm, to write into."""
+    grads = list(grads)
+    dev = _list_device(grads)
+    _here(dev)
+    lists = _tensors(grads, "grads", dev, None)
+    if out is None:
+        out = _empty(1, torch.float32, dev, stream)
+    w, wp, nb = _clip_work(lists, len(grads), dev, stream)
+    _check(_entry.clip_norm(*lists, len(grads), _vec(out, "norm", _F32, dev, 1), wp, nb, _on(stream, dev)),
+           "sim_clip_norm")
+    return out
+
+
+def clip_grads(grads, max_norm: float, parts=None, out=None, norm=None, stream=None):
+    """A list of gradients scaled down to a norm of at most max_norm, in place (out: or into tensors of the same sizes
+    and types); returns their norm before, fp32 [1] (``sim_clip`` in include/simar.h).  parts: fp32 [ranks], every
+    rank's grad_norm, where this rank's list is not all of them.  norm: the norm, to write into."""
+    grads = list(grads)
+    dev = _list_device(grads)
+    _here(dev)
+    lists = _tensors(grads, "grads", dev, None)
+    outs = None if out is None else _tensors(list(out), "out", dev, lists)[0]
+    if norm is None:
+        norm = _empty(1, torch.float32, dev, stream)
+    w, wp, nb = (None, None, 0) if parts is not None else _clip_work(lists, len(grads), dev, stream)
+    nparts = 0 if parts is None else parts.numel()
+    _check(_entry.clip(lists[0], outs, lists[1], lists[2], len(grads), _vec(parts, "parts", _F32, dev, nparts), nparts,
+                       max_norm, _vec(norm, "norm", _F32, dev, 1), wp, nb, _on(stream, dev)), "sim_clip")
+    return norm

@@ -5,72 +5,14 @@
 
 #include <algorithm>
 
+#include "api_checks.h"
 #include "loss.h"
 
 namespace simar {
 namespace {
 
-constexpr int64_t kMaxBytes = (int64_t)1 << 46;
-constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
-
-bool float_dtype(int d) { return d == SIM_FP32 || d == SIM_FP16 || d == SIM_BF16; }
-int64_t size_of(int d) { return d == SIM_FP32 ? 4 : 2; }
-
-// An array of a call: its address range (first to last element), the alignment
-// its elements need, and for rows with others' elements between them the bytes
-// of a row and from one to the next.
-struct Array {
-  const void* p;
-  int64_t bytes;
-  int64_t align;
-  bool output;
-  int64_t width = 0, pitch = 0;
-};
-
-Array rows_of(const void* p, int64_t rows, int64_t cols, int64_t stride, int dtype, bool output) {
-  const int64_t e = size_of(dtype);
-  return {p, rows > 0 ? ((rows - 1) * stride + cols) * e : 0, e, output, cols * e, stride * e};
-}
-
-bool rows_fit(int64_t rows, int64_t cols, int64_t stride) {
-  return rows >= 0 && cols >= 1 && stride >= cols && stride <= kMaxBytes / 4 &&
-         (rows == 0 || rows <= kMaxBytes / 4 / stride);
-}
-
-// Whether two arrays share a byte.  Rows at the same distances may lie between
-// each other's: column slices of one wide buffer.
-bool overlap(const Array& a, const Array& b) {
-  const uintptr_t p = (uintptr_t)a.p, q = (uintptr_t)b.p;
-  if (!(p < q + (uintptr_t)b.bytes && q < p + (uintptr_t)a.bytes)) return false;
-  if (a.pitch == 0 || a.pitch != b.pitch) return true;
-  const int64_t to_b = p <= q ? (int64_t)((q - p) % (uintptr_t)a.pitch)
-                              : (a.pitch - (int64_t)((p - q) % (uintptr_t)a.pitch)) % a.pitch;
-  return to_b < a.width || to_b + b.width > a.pitch;
-}
-
-// NULL arrays are absent ones.  `over`: the index of an output that may lie
-// exactly on the input with index `under` (a gradient on its logits).
-template <int N>
-int check_arrays(const Array (&a)[N], int under, int over, bool same_stride) {
-  for (const Array& v : a)
-    if ((uintptr_t)v.p & (uintptr_t)(v.align - 1)) return SIM_ERR_ALIGN;
-  for (int i = 0; i < N; i++) {
-    if (!a[i].p || !a[i].output || a[i].bytes == 0) continue;
-    for (int j = 0; j < N; j++) {
-      if (j == i || !a[j].p || a[j].bytes == 0) continue;
-      if (i == over && j == under && a[i].p == a[j].p && same_stride) continue;
-      if (overlap(a[i], a[j])) return SIM_ERR_ALIAS;
-    }
-  }
-  return SIM_OK;
-}
-
-// Too many rows for a launch are the caller's error.  It is always a call's
-// first launch that has too many: the others are only made for few rows, or
-// with as many threads as the first.
-int hip_status(hipError_t e) {
-  return e == hipSuccess ? SIM_OK : e == hipErrorInvalidConfiguration ? SIM_ERR_INVALID_ARG : SIM_ERR_HIP;
-}
+// a gradient (array 1) may lie on its logits (array 0)
+constexpr Over kGradOnLogits[] = {{1, 0}};
 
 int check_route(int64_t tokens, int experts, int topk, int dtype) {
   if (!float_dtype(dtype)) return SIM_ERR_INVALID_ARG;
@@ -116,13 +58,6 @@ int64_t distill_work_bytes(int64_t rows, int64_t cols, int dtype) {
   return std::max<int64_t>(step, parts > 1 ? parts : 0) * 4 * rows * 4;
 }
 
-int check_work(const void* work, size_t have, int64_t need) {
-  if (need == 0) return SIM_OK;
-  if (!work) return SIM_ERR_INVALID_ARG;
-  if ((uintptr_t)work & 3u) return SIM_ERR_ALIGN;
-  return have < (size_t)need ? SIM_ERR_NOMEM : SIM_OK;
-}
-
 }  // namespace
 }  // namespace simar
 
@@ -156,7 +91,7 @@ int sim_route(const void* logits, int64_t row_stride, int dtype, const uint8_t* 
                        {counts, ((int64_t)experts + 1) * 4, 4, true},
                        {prob_sums, (int64_t)experts * 4, 4, true},
                        {need ? work : nullptr, need, 4, true}};
-  if ((rc = check_arrays(all, -1, -1, false))) return rc;
+  if ((rc = check_arrays(all))) return rc;
   if ((rc = library_device())) return rc;
   const int wg = route_workgroups(tokens, experts, dtype);
   const Turn turn = route_sums_itself(wg, experts) ? library_turn((hipStream_t)stream) : Turn{};
@@ -185,7 +120,7 @@ int sim_route_grad(const void* logits, int64_t row_stride, int dtype, const uint
                        {counts, ((int64_t)experts + 1) * 4, 4, false},
                        {prob_sums, (int64_t)experts * 4, 4, false},
                        {loss, 4, 4, true}};
-  if ((rc = check_arrays(all, 0, 1, row_stride == drow_stride))) return rc;
+  if ((rc = check_arrays(all, kGradOnLogits))) return rc;
   if ((rc = library_device())) return rc;
   const RouteGradArgs a{logits, row_stride, keep, tokens, experts, topk, normalize != 0, chosen, dweights, counts,
                         prob_sums, coef, dlogits, drow_stride, loss};
@@ -219,7 +154,7 @@ int sim_distill_step(const void* logits, int64_t row_stride, int dtype, int64_t 
                        {row_scale, rows * 4, 4, false},
                        {loss, rows * 4, 4, true},
                        {need ? work : nullptr, need, 4, true}};
-  if ((rc = check_arrays(all, 0, 1, row_stride == drow_stride))) return rc;
+  if ((rc = check_arrays(all, kGradOnLogits))) return rc;
   if ((rc = library_device())) return rc;
   DistillArgs a{};
   a.x = logits;
@@ -265,7 +200,7 @@ int sim_distill_parts(const void* logits, int64_t row_stride, int dtype, int64_t
                        {teacher, rows * topk * size_of(teacher_dtype), size_of(teacher_dtype), false},
                        {parts, rows * 16, 4, true},
                        {need ? work : nullptr, need, 4, true}};
-  if ((rc = check_arrays(all, -1, -1, false))) return rc;
+  if ((rc = check_arrays(all))) return rc;
   if ((rc = library_device())) return rc;
   DistillArgs a{};
   a.x = logits;
@@ -302,7 +237,7 @@ int sim_distill_join(const float* parts, int nparts, int64_t rows, int64_t vocab
                        {teacher, rows * topk * size_of(teacher_dtype), size_of(teacher_dtype), false},
                        {loss, rows * 4, 4, true},
                        {norm, rows * 8, 4, true}};
-  if ((rc = check_arrays(all, -1, -1, false))) return rc;
+  if ((rc = check_arrays(all))) return rc;
   if ((rc = library_device())) return rc;
   DistillArgs a{};
   a.rows = rows;
@@ -333,7 +268,7 @@ int sim_distill_grad(const void* logits, int64_t row_stride, int dtype, int64_t 
                        {teacher, rows * topk * size_of(teacher_dtype), size_of(teacher_dtype), false},
                        {norm, rows * 8, 4, false},
                        {row_scale, rows * 4, 4, false}};
-  if ((rc = check_arrays(all, 0, 1, row_stride == drow_stride))) return rc;
+  if ((rc = check_arrays(all, kGradOnLogits))) return rc;
   if ((rc = library_device())) return rc;
   DistillArgs a{};
   a.x = logits;

@@ -112,10 +112,10 @@ static PyTypeObject PreparedCallType = {
     .tp_call = PreparedCall_call,
 };
 
-/* ---- the routing and loss entry points ------------------------------------
+/* ---- the entry points that work on one rank's data ------------------------------------
  * bind(name, address) sets an entry point once; the function of that name
- * then takes the C function's arguments (pointers as integers or None) and
- * returns its status. */
+ * then takes the C function's arguments (pointers as integers, bytes objects or
+ * None) and returns its status. */
 #define ENTRY(name) static __typeof__(sim_##name)* name##_fn
 ENTRY(route);
 ENTRY(route_grad);
@@ -123,8 +123,19 @@ ENTRY(distill_step);
 ENTRY(distill_parts);
 ENTRY(distill_join);
 ENTRY(distill_grad);
+ENTRY(norm);
+ENTRY(norm_grad);
+ENTRY(dispatch);
+ENTRY(combine);
+ENTRY(combine_grad);
+ENTRY(clip_norm);
+ENTRY(clip);
 
-static void* as_pointer(PyObject* o) { return o == Py_None ? NULL : PyLong_AsVoidPtr(o); }
+/* (an array of the host: the bytes object that tensors() made) */
+static void* as_pointer(PyObject* o) {
+  if (o == Py_None) return NULL;
+  return PyBytes_Check(o) ? (void*)PyBytes_AS_STRING(o) : PyLong_AsVoidPtr(o);
+}
 static int as_int(PyObject* o) {
   const long v = PyLong_AsLong(o);
   if (v != (int)v && !PyErr_Occurred()) PyErr_SetString(PyExc_OverflowError, "argument does not fit an int");
@@ -183,6 +194,39 @@ WRAP(distill_grad, 18,
      void* norm = P(12); void* rs = P(13); float coef = F(14); void* dx = P(15); int64_t dld = L(16); void* s = P(17);
      , ARGS(x, ld, dt, rows, cols, first, vocab, ids, z, zdt, topk, tau, norm, rs, coef, dx, dld, s))
 
+WRAP(norm, 17,
+     void* x = P(0); int64_t ld = L(1); int dt = I(2); void* res = P(3); int64_t rld = L(4); int64_t rows = L(5);
+     int64_t cols = L(6); void* g = P(7); int gdt = I(8); float eps = F(9); void* sum = P(10); int64_t sld = L(11);
+     void* out = P(12); int64_t old = L(13); void* sc = P(14); int group = I(15); void* s = P(16);
+     , ARGS(x, ld, dt, res, rld, rows, cols, g, gdt, eps, sum, sld, out, old, sc, group, s))
+WRAP(norm_grad, 18,
+     void* h = P(0); int64_t ld = L(1); int dt = I(2); int64_t rows = L(3); int64_t cols = L(4); void* g = P(5);
+     int gdt = I(6); float eps = F(7); void* dy = P(8); int64_t dyld = L(9); void* ds = P(10); int64_t dsld = L(11);
+     void* dx = P(12); int64_t dxld = L(13); void* dg = P(14); void* work = P(15); size_t bytes = Z(16); void* s = P(17);
+     , ARGS(h, ld, dt, rows, cols, g, gdt, eps, dy, dyld, ds, dsld, dx, dxld, dg, work, bytes, s))
+WRAP(dispatch, 17,
+     void* x = P(0); int64_t ld = L(1); int64_t rb = L(2); void* sc = P(3); int64_t groups = L(4); void* chosen = P(5);
+     int64_t tokens = L(6); int topk = I(7); int experts = I(8); void* rows = P(9); int64_t rld = L(10);
+     void* rsc = P(11); void* place = P(12); void* off = P(13); void* work = P(14); size_t bytes = Z(15); void* s = P(16);
+     , ARGS(x, ld, rb, sc, groups, chosen, tokens, topk, experts, rows, rld, rsc, place, off, work, bytes, s))
+WRAP(combine, 12,
+     void* rows = P(0); int64_t ld = L(1); int dt = I(2); int64_t nrows = L(3); int64_t cols = L(4); void* place = P(5);
+     void* w = P(6); int64_t tokens = L(7); int topk = I(8); void* out = P(9); int64_t old = L(10); void* s = P(11);
+     , ARGS(rows, ld, dt, nrows, cols, place, w, tokens, topk, out, old, s))
+WRAP(combine_grad, 15,
+     void* dy = P(0); int64_t dyld = L(1); int dt = I(2); void* rows = P(3); int64_t ld = L(4); int64_t nrows = L(5);
+     int64_t cols = L(6); void* place = P(7); void* w = P(8); int64_t tokens = L(9); int topk = I(10);
+     void* dr = P(11); int64_t drld = L(12); void* dw = P(13); void* s = P(14);
+     , ARGS(dy, dyld, dt, rows, ld, nrows, cols, place, w, tokens, topk, dr, drld, dw, s))
+WRAP(clip_norm, 8,
+     void* g = P(0); void* c = P(1); void* d = P(2); int n_t = I(3); void* norm = P(4); void* work = P(5);
+     size_t bytes = Z(6); void* s = P(7);
+     , ARGS(g, c, d, n_t, norm, work, bytes, s))
+WRAP(clip, 12,
+     void* g = P(0); void* o = P(1); void* c = P(2); void* d = P(3); int n_t = I(4); void* parts = P(5);
+     int nparts = I(6); float most = F(7); void* norm = P(8); void* work = P(9); size_t bytes = Z(10); void* s = P(11);
+     , ARGS(g, o, c, d, n_t, parts, nparts, most, norm, work, bytes, s))
+
 static PyObject* py_bind(PyObject* self, PyObject* args) {
   (void)self;
   const char* name;
@@ -191,6 +235,7 @@ static PyObject* py_bind(PyObject* self, PyObject* args) {
 #define SET(entry) \
   if (!strcmp(name, #entry)) { entry##_fn = (__typeof__(sim_##entry)*)(uintptr_t)at; Py_RETURN_NONE; }
   SET(route) SET(route_grad) SET(distill_step) SET(distill_parts) SET(distill_join) SET(distill_grad)
+  SET(norm) SET(norm_grad) SET(dispatch) SET(combine) SET(combine_grad) SET(clip_norm) SET(clip)
   PyErr_Format(PyExc_ValueError, "no entry point %s", name);
   return NULL;
 }
@@ -200,7 +245,7 @@ static PyObject* py_bind(PyObject* self, PyObject* args) {
  * methods.  types(...) sets the logit types once: code i + 1 is entry i. */
 #define TYPES 3
 static PyObject* logit_type[TYPES];
-static PyObject *s_dtype, *s_shape, *s_device, *s_contiguous, *s_data_ptr, *s_stride;
+static PyObject *s_dtype, *s_shape, *s_device, *s_contiguous, *s_data_ptr, *s_stride, *s_esize, *s_numel;
 
 static PyObject* py_types(PyObject* self, PyObject* args) {
   (void)self;
@@ -282,7 +327,7 @@ static PyObject* py_rows(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     ok = PyLong_AsLongLong(PyTuple_GET_ITEM(a[2], 2)) == rows && PyLong_AsLongLong(PyTuple_GET_ITEM(a[2], 3)) == cols &&
          PyLong_AsLong(PyTuple_GET_ITEM(a[2], 4)) == code && PyLong_AsLong(PyTuple_GET_ITEM(a[2], 5)) == dev;
     if (PyErr_Occurred()) return NULL;
-    if (!ok) return PyErr_Format(PyExc_ValueError, "%S must have the logits' shape, dtype and device", a[1]);
+    if (!ok) return PyErr_Format(PyExc_ValueError, "%S must have the first tensor's shape, dtype and device", a[1]);
   }
   if (!(v = PyObject_CallMethodNoArgs(a[0], s_data_ptr))) return NULL;
   return Py_BuildValue("(NLLLil)", v, ld, rows, cols, code, dev);
@@ -384,6 +429,101 @@ static PyObject* py_slots(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return Py_BuildValue("(NNiL)", ids, teacher, code, shape[1]);
 }
 
+/* raw(tensor, what, dtype): (pointer, bytes from row to row, rows, bytes of a
+ * row, device index) of a 2-D device tensor of any type with contiguous rows;
+ * dtype: the one it must have, or None. */
+static PyObject* py_raw(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 3) {
+    PyErr_SetString(PyExc_TypeError, "raw(tensor, what, dtype)");
+    return NULL;
+  }
+  long long rows = 0, cols = 0, ld = 0, step = 0;
+  PyObject* v = PyObject_GetAttr(a[0], s_shape);
+  if (!v) return NULL;
+  int ok = pair_of(v, &rows, &cols);
+  Py_DECREF(v);
+  const long dev = ok ? number(a[0], s_device) : -1;
+  if (PyErr_Occurred()) return NULL;
+  if (dev < 0) return PyErr_Format(PyExc_ValueError, "%S must be a 2-D device tensor", a[1]);
+  if (!(v = PyObject_CallMethodNoArgs(a[0], s_stride))) return NULL;
+  ok = pair_of(v, &ld, &step);
+  Py_DECREF(v);
+  if (PyErr_Occurred()) return NULL;
+  if (!ok || (step != 1 && cols > 1)) return PyErr_Format(PyExc_ValueError, "%S's rows must be contiguous", a[1]);
+  if (rows <= 1) ld = cols;
+  if (a[2] != Py_None) {
+    if (!(v = PyObject_GetAttr(a[0], s_dtype))) return NULL;
+    ok = v == a[2];
+    Py_DECREF(v);
+    if (!ok) return PyErr_Format(PyExc_ValueError, "%S must be of type %S", a[1], a[2]);
+  }
+  const long e = number(a[0], s_esize);
+  if (PyErr_Occurred()) return NULL;
+  if (!(v = PyObject_CallMethodNoArgs(a[0], s_data_ptr))) return NULL;
+  return Py_BuildValue("(NLLLl)", v, ld * e, rows, cols * e, dev);
+}
+
+/* tensors(sequence, what, device, like): (pointers, counts, type codes), each an
+ * array of the host in a bytes object, of contiguous tensors on that device;
+ * like: None, or such a tuple whose counts and types they must have. */
+static PyObject* py_tensors(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 4) {
+    PyErr_SetString(PyExc_TypeError, "tensors(sequence, what, device, like)");
+    return NULL;
+  }
+  const long dev = PyLong_AsLong(a[2]);
+  if (PyErr_Occurred()) return NULL;
+  PyObject* seq = PySequence_Fast(a[0], "a sequence of tensors");
+  if (!seq) return NULL;
+  const Py_ssize_t count = PySequence_Fast_GET_SIZE(seq);
+  PyObject* ptrs = PyBytes_FromStringAndSize(NULL, count * (Py_ssize_t)sizeof(void*));
+  PyObject* counts = PyBytes_FromStringAndSize(NULL, count * (Py_ssize_t)sizeof(int64_t));
+  PyObject* types = PyBytes_FromStringAndSize(NULL, count * (Py_ssize_t)sizeof(int));
+  int ok = ptrs && counts && types;
+  for (Py_ssize_t i = 0; ok && i < count && i < PySequence_Fast_GET_SIZE(seq); i++) {
+    PyObject* t = PySequence_Fast_GET_ITEM(seq, i);
+    Py_INCREF(t);
+    const int code = code_of(t);
+    const long on = code >= 0 ? number(t, s_device) : -1;
+    PyObject* v = PyErr_Occurred() ? NULL : PyObject_CallMethodNoArgs(t, s_contiguous);
+    const int whole = v ? PyObject_IsTrue(v) : 0;
+    Py_XDECREF(v);
+    if (!PyErr_Occurred() && (code == 0 || on != dev || !whole))
+      PyErr_Format(PyExc_ValueError, "%S[%zd] must be a contiguous tensor of one of the float types on cuda:%ld", a[1], i, dev);
+    v = PyErr_Occurred() ? NULL : PyObject_CallMethodNoArgs(t, s_data_ptr);
+    if (v) {
+      ((void**)PyBytes_AS_STRING(ptrs))[i] = PyLong_AsVoidPtr(v);
+      Py_DECREF(v);
+      const long elements = number(t, s_numel);
+      ((int64_t*)PyBytes_AS_STRING(counts))[i] = elements;
+      ((int*)PyBytes_AS_STRING(types))[i] = code;
+    }
+    Py_DECREF(t);
+    ok = !PyErr_Occurred();
+  }
+  if (ok && PySequence_Fast_GET_SIZE(seq) != count) {
+    PyErr_Format(PyExc_RuntimeError, "%S changed while it was read", a[1]);
+    ok = 0;
+  }
+  Py_DECREF(seq);
+  if (ok && a[3] != Py_None) {
+    const int has = PyTuple_Check(a[3]) && PyTuple_GET_SIZE(a[3]) == 3;
+    const int c = has ? PyObject_RichCompareBool(counts, PyTuple_GET_ITEM(a[3], 1), Py_EQ) : 0;
+    const int d = has && c > 0 ? PyObject_RichCompareBool(types, PyTuple_GET_ITEM(a[3], 2), Py_EQ) : 0;
+    if (!PyErr_Occurred() && d <= 0) PyErr_Format(PyExc_ValueError, "%S must have the gradients' sizes and types", a[1]);
+    ok = !PyErr_Occurred();
+  }
+  if (!ok) {
+    Py_XDECREF(ptrs);
+    Py_XDECREF(counts);
+    Py_XDECREF(types);
+    return NULL;
+  }
+  return Py_BuildValue("(NNN)", ptrs, counts, types);
+}
+
 #define METHOD(name, f, doc) {name, (PyCFunction)(void (*)(void))f, METH_FASTCALL, doc}
 static PyMethodDef pycall_methods[] = {
     {"bind", py_bind, METH_VARARGS, "bind(name, address): set an entry point"},
@@ -397,6 +537,15 @@ static PyMethodDef pycall_methods[] = {
     METHOD("distill_parts", py_distill_parts, "sim_distill_parts"),
     METHOD("distill_join", py_distill_join, "sim_distill_join"),
     METHOD("distill_grad", py_distill_grad, "sim_distill_grad"),
+    METHOD("raw", py_raw, "raw(tensor, what, dtype): pointer, row pitch, rows, row bytes, device"),
+    METHOD("tensors", py_tensors, "tensors(sequence, what, device, like): pointers, counts, type codes"),
+    METHOD("norm", py_norm, "sim_norm"),
+    METHOD("norm_grad", py_norm_grad, "sim_norm_grad"),
+    METHOD("dispatch", py_dispatch, "sim_dispatch"),
+    METHOD("combine", py_combine, "sim_combine"),
+    METHOD("combine_grad", py_combine_grad, "sim_combine_grad"),
+    METHOD("clip_norm", py_clip_norm, "sim_clip_norm"),
+    METHOD("clip", py_clip, "sim_clip"),
     {NULL, NULL, 0, NULL},
 };
 
@@ -412,9 +561,13 @@ PyMODINIT_FUNC PyInit__pycall(void) {
   s_contiguous = PyUnicode_InternFromString("is_contiguous");
   s_data_ptr = PyUnicode_InternFromString("data_ptr");
   s_stride = PyUnicode_InternFromString("stride");
+  s_esize = PyUnicode_InternFromString("element_size");
+  s_numel = PyUnicode_InternFromString("numel");
   s_ids = PyUnicode_InternFromString("ids");
   s_teacher = PyUnicode_InternFromString("teacher");
-  if (!s_dtype || !s_shape || !s_device || !s_contiguous || !s_data_ptr || !s_stride || !s_ids || !s_teacher) return NULL;
+  if (!s_dtype || !s_shape || !s_device || !s_contiguous || !s_data_ptr || !s_stride || !s_esize || !s_numel || !s_ids ||
+      !s_teacher)
+    return NULL;
   PyObject* m = PyModule_Create(&pycall_module);
   if (!m) return NULL;
   Py_INCREF(&PreparedCallType);

@@ -552,6 +552,116 @@ int sim_distill_grad(const void* logits, int64_t row_stride, int dtype, int64_t 
                      int topk, float temperature, const float* norm, const float* row_scale, float coef,
                      void* dlogits, int64_t drow_stride, void* stream);
 
+/* ---- around the experts, and before the optimizer ---------------------------
+ * What such a training step does between its routing, its products and its
+ * collectives:
+ *
+ *   all-reduced activation -> sim_norm -> sim_route -> sim_dispatch
+ *       -> the experts' products -> sim_combine -> the residual path
+ *   and back: sim_combine_grad -> the products' gradients -> sim_combine
+ *       (without weights: the gradient of sim_dispatch) -> sim_norm_grad
+ *   reduced gradients -> sim_clip -> the optimizer; where a rank holds a part
+ *       of them: sim_clip_norm -> sim_all_gather -> sim_clip
+ *
+ * The conventions are those of routing and losses: rows whose starts lie
+ * *_stride elements (of moved rows: *_pitch bytes) apart, no alignment but that
+ * of single elements, fp32 (or wider) statistics and sums in an order that
+ * depends on the sizes alone, the caller's scratch in `work`, no library
+ * memory.  Outputs may not overlap anything but where it is said.  0 rows or
+ * tokens are a no-op, except that dgain, offsets and norm are written.
+ */
+#define SIM_NORM_MAX_COLUMNS 32768
+#define SIM_CLIP_MAX_TENSORS 65536
+
+/* Root-mean-square norm of rows of h = x + residual (residual NULL: h = x):
+ *   r = 1 / sqrt(mean of h^2 + eps),   y = gain * h * r
+ * h is held in fp32; sum (NULL: not written; it needs a residual) gets it
+ * rounded to `dtype`, y is taken of the unrounded one.  gain[columns] is of
+ * gain_dtype (NULL: all 1, gain_dtype still a valid one).
+ *   scales NULL   out gets y, rounded to `dtype`
+ *   scales given  out gets 8-bit floats (e4m3: OCP, finite, largest 448) whose
+ *                 rows lie out_stride bytes apart, with
+ *                 scales[t][g] = the largest |y| of the row's columns
+ *                 [g group, (g + 1) group) / 448,  out = y / scale, rounded to
+ *                 nearest even; group is 32, 64 or 128, or 0: one scale for a
+ *                 row.  A group of zeros has scale 0.
+ * sum and out may each lie exactly on x or residual (same address and stride;
+ * out only in `dtype`).  eps lies in [1e-30, 1e30]; the sum of squares is held
+ * in fp32 (values past 1e19 overflow it: r is 0).  A NaN makes its row's y (in
+ * 8 bits: every scale of the row) NaN; an infinity makes r 0, its own y NaN (in
+ * 8 bits: its scale NaN) and the row's others 0. */
+int sim_norm(const void* x, int64_t x_stride, int dtype, const void* residual, int64_t residual_stride, int64_t rows,
+             int64_t columns, const void* gain, int gain_dtype, float eps, void* sum, int64_t sum_stride, void* out,
+             int64_t out_stride, float* scales, int group, void* stream);
+
+/* Gradient of y = gain * h * r for h and gain, from dy and (NULL: none) the
+ * gradient dsum that reaches h by another way:
+ *   dx    = r (gain dy - h r mean(gain dy h r)) + dsum      (rounded to `dtype`;
+ *           the gradient of both x and residual)
+ *   dgain = the sum of dy h r over the rows                 (fp32, NULL: not wanted)
+ * dx may lie exactly on h, dy or dsum. */
+int sim_norm_grad_work(int64_t rows, int64_t columns, int dtype, size_t* bytes);
+int sim_norm_grad(const void* h, int64_t h_stride, int dtype, int64_t rows, int64_t columns, const void* gain,
+                  int gain_dtype, float eps, const void* dy, int64_t dy_stride, const void* dsum, int64_t dsum_stride,
+                  void* dx, int64_t dx_stride, float* dgain, void* work, size_t work_bytes, void* stream);
+
+/* Tokens sorted by their experts.  chosen[tokens][topk] is sim_route's; an
+ * index outside [0, experts) is an empty slot.  The slots that are not empty
+ * are numbered by expert, those of one expert by token and slot:
+ *   place[t][j]    the number of slot (t, j); -1 where it is empty
+ *   offsets[e]     the number of expert e's first slot; offsets[experts]: of all
+ *   rows[place[t][j]]        = x[t]          (row_bytes bytes, any type)
+ *   row_scales[place[t][j]]  = scales[t]     (groups fp32 values; groups 0: none)
+ * rows and row_scales have tokens * topk rows; those from offsets[experts] on
+ * are left as they were.  row_bytes 0 and groups 0: the places alone.
+ * topk <= SIM_ROUTE_MAX_TOPK, experts <= SIM_ROUTE_MAX_EXPERTS, tokens * topk
+ * below 2^31. */
+int sim_dispatch_work(int64_t tokens, int topk, int experts, size_t* bytes);
+int sim_dispatch(const void* x, int64_t x_pitch, int64_t row_bytes, const float* scales, int64_t groups,
+                 const int32_t* chosen, int64_t tokens, int topk, int experts, void* rows, int64_t rows_pitch,
+                 float* row_scales, int32_t* place, int32_t* offsets, void* work, size_t work_bytes, void* stream);
+
+/* The experts' rows back to their tokens:
+ *   out[t] = the sum over j of weights[t][j] * rows[place[t][j]]
+ * in fp32 in the order of j, rounded once.  weights NULL: all 1, which is the
+ * gradient of sim_dispatch for x.  A place outside [0, nrows) is an empty slot
+ * (whatever its weight holds); a token without any gets zeros. */
+int sim_combine(const void* rows, int64_t rows_stride, int dtype, int64_t nrows, int64_t columns, const int32_t* place,
+                const float* weights, int64_t tokens, int topk, void* out, int64_t out_stride, void* stream);
+
+/* Its gradient:
+ *   drows[place[t][j]] = weights[t][j] * dy[t]               (NULL: not wanted)
+ *   dweights[t][j]     = the sum over the columns of dy[t] * rows[place[t][j]]
+ *                        (NULL: not wanted; 0 for an empty slot)
+ * No two slots may have the same place (sim_dispatch's are different; of equal
+ * ones, drows gets one slot's row).  Rows that no place names are left as they
+ * were.  drows may lie exactly on rows. */
+int sim_combine_grad(const void* dy, int64_t dy_stride, int dtype, const void* rows, int64_t rows_stride,
+                     int64_t nrows, int64_t columns, const int32_t* place, const float* weights, int64_t tokens,
+                     int topk, void* drows, int64_t drows_stride, float* dweights, void* stream);
+
+/* The norm over `ntensors` gradients: grads[i] are counts[i] contiguous elements
+ * of dtypes[i] (SIM_FP32, SIM_FP16 or SIM_BF16).  The four arrays themselves are
+ * host memory, read before the call returns.
+ *   sim_clip_norm  norm[0] = sqrt(the sum of all elements' squares), summed in
+ *                  fp64
+ *   sim_clip       outs[i] = grads[i] * min(1, max_norm / norm), rounded once;
+ *                  outs NULL: in place, where a factor of 1 writes nothing.
+ *                  norm[0] is the norm; with parts[nparts] (the norms of all
+ *                  ranks' own gradients, as sim_all_gather leaves them) it is
+ *                  sqrt(the sum of their squares), and work is not needed.
+ * A NaN norm makes everything NaN; an infinite one (also: a norm past fp32's
+ * range) makes finite gradients 0 and infinite ones NaN, by the formula.
+ * max_norm is not negative; +inf: nothing is scaled.  No output may overlap
+ * another tensor (outs[i] may be grads[i]), norm, parts or work.  work is
+ * 8-byte aligned. */
+int sim_clip_work(const int64_t* counts, const int* dtypes, int ntensors, size_t* bytes);
+int sim_clip_norm(const void* const* grads, const int64_t* counts, const int* dtypes, int ntensors, float* norm,
+                  void* work, size_t work_bytes, void* stream);
+int sim_clip(const void* const* grads, void* const* outs, const int64_t* counts, const int* dtypes, int ntensors,
+             const float* parts, int nparts, float max_norm, float* norm, void* work, size_t work_bytes,
+             void* stream);
+
 /* ---- test hooks --------------------------------------------------------- */
 enum {
   SIM_DEBUG_EPOCH = 0,         /* set the LL epoch counter (next call uses value+1) */
