@@ -13,6 +13,8 @@
 namespace simar {
 namespace {
 
+// (a launch has fewer than 2^32 threads, a workgroup for a piece 256)
+constexpr int64_t kMaxPieces = ((int64_t)1 << 24) - 1;
 constexpr int64_t kMaxColumns = (int64_t)1 << 30;
 
 bool eps_fits(float eps) { return eps >= 1e-30f && eps <= 1e30f; }
@@ -43,6 +45,13 @@ int64_t dispatch_work_bytes(int64_t tokens, int topk, int experts) {
   return (int64_t)dispatch_chunks(tokens * topk, &chunk) * experts * 4;
 }
 
+// Up to so many pieces the workgroups that scale them each add up the squares'
+// sums; with more, that costs them more than a launch for it.
+#ifndef X_JOIN
+#define X_JOIN 2048
+#endif
+constexpr int64_t kJoinPieces = X_JOIN;
+
 // ---- lists of tensors ---------------------------------------------------------
 int check_list(const void* const* grads, const int64_t* counts, const int* dtypes, int n) {
   if (n < 0 || n > SIM_CLIP_MAX_TENSORS) return SIM_ERR_INVALID_ARG;
@@ -50,7 +59,7 @@ int check_list(const void* const* grads, const int64_t* counts, const int* dtype
   int64_t all = 0;
   for (int i = 0; i < n; i++) {
     if (!float_dtype(dtypes[i]) || counts[i] < 0 || counts[i] > kMaxBytes / 4) return SIM_ERR_INVALID_ARG;
-    if ((all += counts[i]) > kMaxBytes / 4) return SIM_ERR_INVALID_ARG;
+    if ((all += counts[i]) > kMaxBytes / 4 || clip_pieces(counts[i], dtypes[i]) > kMaxPieces) return SIM_ERR_INVALID_ARG;
     if (counts[i] > 0 && !grads[i]) return SIM_ERR_INVALID_ARG;
   }
   for (int i = 0; i < n; i++)
@@ -65,8 +74,8 @@ void take(ClipList& l, int& i, const void* const* grads, void* const* outs, cons
   int64_t pieces = 0;
   for (; i < n && l.tensors < kClipTensors; i++) {
     if (counts[i] == 0) continue;
-    const int64_t p = clip_pieces(counts[i]);
-    if (l.tensors > 0 && pieces + p > INT32_MAX) break;
+    const int64_t p = clip_pieces(counts[i], dtypes[i]);
+    if (l.tensors > 0 && pieces + p > kMaxPieces) break;
     const int t = l.tensors++;
     l.first[t] = (uint32_t)pieces;
     l.in[t] = grads ? grads[i] : nullptr;
@@ -79,14 +88,16 @@ void take(ClipList& l, int& i, const void* const* grads, void* const* outs, cons
 }
 struct Sizes {
   int launches, squares;
+  int64_t pieces;
 };
 Sizes sizes_of(const int64_t* counts, const int* dtypes, int n) {
-  Sizes s{0, 0};
+  Sizes s{0, 0, 0};
   for (int i = 0; i < n;) {
     ClipList l;
     take(l, i, nullptr, nullptr, counts, dtypes, n);
     if (l.tensors == 0) break;
     s.launches++;
+    s.pieces += l.pieces;
     s.squares += clip_workgroups(l.pieces);
   }
   return s;
@@ -291,7 +302,9 @@ int sim_clip_work(const int64_t* counts, const int* dtypes, int ntensors, size_t
   if (ntensors < 0 || ntensors > SIM_CLIP_MAX_TENSORS || !bytes) return SIM_ERR_INVALID_ARG;
   if (ntensors > 0 && (!counts || !dtypes)) return SIM_ERR_INVALID_ARG;
   for (int i = 0; i < ntensors; i++)
-    if (!float_dtype(dtypes[i]) || counts[i] < 0 || counts[i] > kMaxBytes / 4) return SIM_ERR_INVALID_ARG;
+    if (!float_dtype(dtypes[i]) || counts[i] < 0 || counts[i] > kMaxBytes / 4 ||
+        clip_pieces(counts[i], dtypes[i]) > kMaxPieces)
+      return SIM_ERR_INVALID_ARG;
   *bytes = (size_t)clip_work_bytes(sizes_of(counts, dtypes, ntensors));
   return SIM_OK;
 }
@@ -363,8 +376,8 @@ int sim_clip(const void* const* grads, void* const* outs, const int64_t* counts,
   hipError_t e = hipSuccess;
   ClipNorm n{squares, parts ? 0 : sizes.squares, parts, nparts, max_norm, norm, in_place};
   if (!parts && (e = squares_of_list(grads, counts, dtypes, ntensors, squares, s)) != hipSuccess) return hip_status(e);
-  if (sizes.launches != 1) {
-    // the norm by itself, read by every launch that scales
+  if (sizes.launches != 1 || sizes.pieces > kJoinPieces) {
+    // the norm by itself, read by every workgroup that scales
     if ((e = launch_clip_join(n, s)) != hipSuccess) return hip_status(e);
     n = ClipNorm{nullptr, 0, norm, 1, max_norm, nullptr, in_place};
   }

@@ -2,19 +2,19 @@
 // largest norm (gfx950).
 //
 // norm = sqrt(sum g^2) over all elements of all tensors, rounded to fp32;
-// g' = g * min(1, max_norm / norm).  Squares are summed in 64 bits: fp32 and bf16 gradients of
-// 1e-25 or 1e25 are within their types' range, their squares are not within
-// fp32's.  Tensors are cut into pieces of kClipPiece elements; a workgroup takes a
-// run of pieces, and the workgroups' sums are added up in their order, so that
-// the same list gives the same bits.
-#include <algorithm>
-
+// g' = g * min(1, max_norm / norm).  The sums are held in 64 bits: fp32 and bf16
+// gradients of 1e-25 or 1e25 are within their types' range, their squares are
+// not within fp32's.  Tensors are cut into pieces of 16 KiB, and the workgroups'
+// sums are added up in their order, so that the same list gives the same bits.
 #include "launch.h"
 #include "layer.h"
 #include "loss_device.h"
 
 namespace simar {
 namespace {
+
+// 16-byte vectors of a piece, and of one of a workgroup's threads
+constexpr int kVectors = kClipPieceBytes / 16, kEach = kVectors / kBlock;
 
 __device__ __forceinline__ double wave_sum64(double v) {
   for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
@@ -31,109 +31,117 @@ __device__ __forceinline__ double block_sum64(double v) {
   return sum;
 }
 
-// this workgroup's run of pieces
-struct Run {
+// Which tensor a piece is of: every lane holds two tensors' first pieces, and the
+// number of those that are not after the piece is one more than its index.
+struct Tensors {
+  static_assert(kClipTensors <= 128, "two tensors per lane");
   uint32_t lo, hi;
-  __device__ __forceinline__ explicit Run(const ClipList& l)
-      : lo((uint32_t)((uint64_t)l.pieces * blockIdx.x / gridDim.x)),
-        hi((uint32_t)((uint64_t)l.pieces * (blockIdx.x + 1) / gridDim.x)) {}
-};
-// the last tensor whose first piece is not after `piece` (tensors without
-// elements have no piece: they share their first with the next one)
-__device__ __forceinline__ int tensor_of(const ClipList& l, uint32_t piece) {
-  int lo = 0, hi = l.tensors;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (l.first[mid] <= piece) lo = mid;
-    else hi = mid;
+  __device__ __forceinline__ explicit Tensors(const ClipList& l) {
+    const int lane = threadIdx.x & 63;
+    lo = lane < l.tensors ? l.first[lane] : 0xffffffffu;
+    hi = lane + 64 < l.tensors ? l.first[lane + 64] : 0xffffffffu;
   }
-  return lo;
-}
+  __device__ __forceinline__ int of(uint32_t piece) const {
+    return __popcll(__ballot(lo <= piece)) + __popcll(__ballot(hi <= piece)) - 1;
+  }
+};
+// a piece: its tensor, its first byte and its elements
+struct Piece {
+  int t, n, dtype;
+  int64_t byte;
+  __device__ __forceinline__ Piece(const ClipList& l, const Tensors& all, uint32_t piece) : t(all.of(piece)) {
+    dtype = l.dtype[t];
+    const int size = dtype == SIM_FP32 ? 4 : 2, most = kClipPieceBytes / size;
+    byte = (int64_t)(piece - l.first[t]) * kClipPieceBytes;
+    const int64_t left = l.count[t] - byte / size;
+    n = (int)(left < most ? left : most);
+  }
+};
 
-// f(vector) for the whole vectors and f1(element) for what is left, of the
-// elements [lo, hi); U vectors of a thread are under way at once
-constexpr int kFlight = 8;
+// A vector's squares, in fp32 where that is exact enough: a sum from 2^-90 on
+// has lost nothing to underflow that it could see.  (In 64 bits throughout the
+// conversions bound the kernel.)
+template <int DT>
+__device__ __forceinline__ void add_squares(u32x4 v, double& sum) {
+  constexpr int V = epv<DT>();
+  float f[V], s = 0.0f;
+  unpack<DT>(v, f);
+#pragma unroll
+  for (int t = 0; t < V; t++) s = __builtin_fmaf(f[t], f[t], s);
+  if (DT == SIM_FP16 || (s >= 0x1p-90f && s < __builtin_inff())) {
+    sum += (double)s;
+  } else {
+#pragma unroll
+    for (int t = 0; t < V; t++) sum = __builtin_fma((double)f[t], (double)f[t], sum);
+  }
+}
+template <int DT>
+__device__ __forceinline__ void squares_of(const char* in, int n, double& sum) {
+  constexpr int V = epv<DT>();
+  if (n == kVectors * V) {
+    u32x4 v[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; i++) v[i] = ld_row_lane<DT, true>(in, 0, (i * kBlock + threadIdx.x) * V);
+#pragma unroll
+    for (int i = 0; i < kEach; i++) add_squares<DT>(v[i], sum);
+  } else {
+    for (int i = threadIdx.x; i < n / V; i += kBlock) add_squares<DT>(ld_row<DT>(in, (int64_t)i * V), sum);
+    const int i = n / V * V + threadIdx.x;
+    if (i < n) {
+      const double f = (double)load_elem<DT>(in, i);
+      sum = __builtin_fma(f, f, sum);
+    }
+  }
+}
 
 template <int DT>
-__device__ __forceinline__ double squares_of(const char* in, int n) {
+__device__ __forceinline__ u32x4 scaled(u32x4 v, float c) {
   constexpr int V = epv<DT>();
-  double sum = 0.0;
-  const int nv = n / V;
-  for (int v0 = threadIdx.x; v0 < nv; v0 += kBlock * kFlight) {
-    u32x4 v[kFlight];
+  float f[V];
+  unpack<DT>(v, f);
 #pragma unroll
-    for (int i = 0; i < kFlight; i++) {
-      v[i] = u32x4{0, 0, 0, 0};
-      if (v0 + i * kBlock < nv) v[i] = ld_row<DT>(in, (int64_t)(v0 + i * kBlock) * V);
-    }
-#pragma unroll
-    for (int i = 0; i < kFlight; i++) {
-      float f[V];
-      unpack<DT>(v[i], f);
-      if constexpr (DT == SIM_FP16) {
-        // (the squares of eight halves are within fp32's range)
-        float s = 0.0f;
-#pragma unroll
-        for (int t = 0; t < V; t++) s = __builtin_fmaf(f[t], f[t], s);
-        sum += (double)s;
-      } else {
-#pragma unroll
-        for (int t = 0; t < V; t++) sum = __builtin_fma((double)f[t], (double)f[t], sum);
-      }
-    }
-  }
-  const int i = nv * V + threadIdx.x;
-  if (i < n) {
-    const double f = (double)load_elem<DT>(in, i);
-    sum = __builtin_fma(f, f, sum);
-  }
-  return sum;
+  for (int t = 0; t < V; t++) f[t] *= c;
+  return pack_rounded<DT>(f);
 }
-
 template <int DT>
 __device__ __forceinline__ void scale_to(const char* in, char* out, int n, float c) {
   constexpr int V = epv<DT>();
-  const int nv = n / V;
-  for (int v0 = threadIdx.x; v0 < nv; v0 += kBlock * kFlight) {
-    u32x4 v[kFlight];
+  if (n == kVectors * V) {
+    u32x4 v[kEach];
 #pragma unroll
-    for (int i = 0; i < kFlight; i++)
-      if (v0 + i * kBlock < nv) v[i] = ld_row<DT>(in, (int64_t)(v0 + i * kBlock) * V);
+    for (int i = 0; i < kEach; i++) v[i] = ld_row_lane<DT, true>(in, 0, (i * kBlock + threadIdx.x) * V);
 #pragma unroll
-    for (int i = 0; i < kFlight; i++) {
-      if (v0 + i * kBlock >= nv) continue;
-      float f[V];
-      unpack<DT>(v[i], f);
-#pragma unroll
-      for (int t = 0; t < V; t++) f[t] *= c;
-      st_row<DT>(out, (int64_t)(v0 + i * kBlock) * V, pack_rounded<DT>(f));
-    }
+    for (int i = 0; i < kEach; i++) st_row_lane<DT, true>(out, 0, (i * kBlock + threadIdx.x) * V, scaled<DT>(v[i], c));
+  } else {
+    for (int i = threadIdx.x; i < n / V; i += kBlock)
+      st_row<DT>(out, (int64_t)i * V, scaled<DT>(ld_row<DT>(in, (int64_t)i * V), c));
+    const int i = n / V * V + threadIdx.x;
+    if (i < n) store_elem<DT>(out, i, load_elem<DT>(in, i) * c);
   }
-  const int i = nv * V + threadIdx.x;
-  if (i < n) store_elem<DT>(out, i, load_elem<DT>(in, i) * c);
 }
 
-__global__ void __launch_bounds__(kBlock) k_clip_squares(ClipList l, double* squares) {
-  const Run run(l);
+// Four waves per SIMD, in both passes: with eight the reads and writes of more
+// pieces interleave in memory (809 M bf16 748 us a call, 772).
+#define SIMAR_CLIP_WAVES __attribute__((amdgpu_waves_per_eu(4, 4)))
+__global__ void __launch_bounds__(kBlock) SIMAR_CLIP_WAVES k_clip_squares(ClipList l, double* squares) {
+  const Tensors all(l);
   double sum = 0.0;
-  int t = tensor_of(l, run.lo);
-  for (uint32_t piece = run.lo; piece < run.hi; piece++) {
-    while (t + 1 < l.tensors && l.first[t + 1] <= piece) t++;
-    const int64_t at = (int64_t)(piece - l.first[t]) * kClipPiece;
-    const int n = (int)(l.count[t] - at < kClipPiece ? l.count[t] - at : kClipPiece);
-    const int dt = l.dtype[t];
-    if (dt == SIM_FP32) sum += squares_of<SIM_FP32>((const char*)l.in[t] + at * 4, n);
-    else if (dt == SIM_FP16) sum += squares_of<SIM_FP16>((const char*)l.in[t] + at * 2, n);
-    else sum += squares_of<SIM_BF16>((const char*)l.in[t] + at * 2, n);
+  for (uint32_t piece = blockIdx.x; piece < l.pieces; piece += gridDim.x) {
+    const Piece p(l, all, piece);
+    const char* in = (const char*)l.in[p.t] + p.byte;
+    if (p.dtype == SIM_FP32) squares_of<SIM_FP32>(in, p.n, sum);
+    else if (p.dtype == SIM_FP16) squares_of<SIM_FP16>(in, p.n, sum);
+    else squares_of<SIM_BF16>(in, p.n, sum);
   }
   sum = block_sum64(sum);
   if (threadIdx.x == 0) squares[blockIdx.x] = sum;
 }
 
 // the norm of all, in every thread
-__device__ __forceinline__ double norm_of(const ClipNorm& n) {
+__device__ __forceinline__ float norm_of(const ClipNorm& n) {
   double sum = 0.0;
   if (n.parts) {
+    if (n.nparts == 1) return fabsf(n.parts[0]);
     for (int i = threadIdx.x; i < n.nparts; i += kBlock) {
       const double p = (double)n.parts[i];
       sum = __builtin_fma(p, p, sum);
@@ -141,32 +149,28 @@ __device__ __forceinline__ double norm_of(const ClipNorm& n) {
   } else {
     for (int i = threadIdx.x; i < n.nsquares; i += kBlock) sum += n.squares[i];
   }
-  return sqrt(block_sum64(sum));
+  return (float)sqrt(block_sum64(sum));
 }
 
 __global__ void __launch_bounds__(kBlock) k_clip_join(ClipNorm n) {
-  const double norm = norm_of(n);
-  if (threadIdx.x == 0) n.norm[0] = (float)norm;
+  const float norm = norm_of(n);
+  if (threadIdx.x == 0) n.norm[0] = norm;
 }
 
-__global__ void __launch_bounds__(kBlock) k_clip_scale(ClipList l, ClipNorm n) {
-  const float norm = (float)norm_of(n);
+__global__ void __launch_bounds__(kBlock) SIMAR_CLIP_WAVES k_clip_scale(ClipList l, ClipNorm n) {
+  const Tensors all(l);
+  const float norm = norm_of(n);
   if (n.norm && blockIdx.x == 0 && threadIdx.x == 0) n.norm[0] = norm;
   // (a NaN norm makes everything NaN)
   const float c = norm <= n.max_norm ? 1.0f : (float)((double)n.max_norm / (double)norm);
   if (n.in_place && c == 1.0f) return;
-  const Run run(l);
-  int t = tensor_of(l, run.lo);
-  for (uint32_t piece = run.lo; piece < run.hi; piece++) {
-    while (t + 1 < l.tensors && l.first[t + 1] <= piece) t++;
-    const int64_t at = (int64_t)(piece - l.first[t]) * kClipPiece;
-    const int m = (int)(l.count[t] - at < kClipPiece ? l.count[t] - at : kClipPiece);
-    const int dt = l.dtype[t];
-    const char* in = (const char*)l.in[t];
-    char* out = (char*)l.out[t];
-    if (dt == SIM_FP32) scale_to<SIM_FP32>(in + at * 4, out + at * 4, m, c);
-    else if (dt == SIM_FP16) scale_to<SIM_FP16>(in + at * 2, out + at * 2, m, c);
-    else scale_to<SIM_BF16>(in + at * 2, out + at * 2, m, c);
+  for (uint32_t piece = blockIdx.x; piece < l.pieces; piece += gridDim.x) {
+    const Piece p(l, all, piece);
+    const char* in = (const char*)l.in[p.t] + p.byte;
+    char* out = (char*)l.out[p.t] + p.byte;
+    if (p.dtype == SIM_FP32) scale_to<SIM_FP32>(in, out, p.n, c);
+    else if (p.dtype == SIM_FP16) scale_to<SIM_FP16>(in, out, p.n, c);
+    else scale_to<SIM_BF16>(in, out, p.n, c);
   }
 }
 
@@ -177,7 +181,7 @@ hipError_t launch_clip_squares(const ClipList& l, double* squares, hipStream_t s
 }
 hipError_t launch_clip_join(const ClipNorm& n, hipStream_t s) { return launch<k_clip_join>(dim3(1), dim3(kBlock), s, n); }
 hipError_t launch_clip_scale(const ClipList& l, const ClipNorm& n, hipStream_t s) {
-  return launch<k_clip_scale>(dim3(std::max(1, clip_workgroups(l.pieces))), dim3(kBlock), s, l, n);
+  return launch<k_clip_scale>(dim3(l.pieces), dim3(kBlock), s, l, n);
 }
 
 }  // namespace simar

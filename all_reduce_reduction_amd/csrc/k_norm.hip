@@ -16,27 +16,25 @@
 namespace simar {
 namespace {
 
-// e4m3 of V floats of at most 448
-template <int V>
-__device__ __forceinline__ void to_e4m3(const float (&x)[V], uint32_t (&w)[V / 4]) {
-#pragma unroll
-  for (int i = 0; i < V / 4; i++) {
-    int v = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i], x[4 * i + 1], 0, false);
-    w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i + 2], x[4 * i + 3], v, true);
-  }
-}
-template <int DT, bool TINY>
-__device__ __forceinline__ void store_e4m3(void* row, const RowPart<DT, TINY>& p, const float (&x)[epv<DT>()]) {
+constexpr float kE4m3Max = 448.0f;
+
+// e4m3 of V floats of at most 448 (and its rounding error), four to a word
+template <int DT, Where K>
+__device__ __forceinline__ void store_e4m3(void* row, const RowPart<DT, K>& p, const float (&x)[epv<DT>()]) {
   constexpr int V = epv<DT>();
   typedef uint32_t Words __attribute__((ext_vector_type(V / 4), aligned(1)));
   uint32_t w[V / 4];
-  to_e4m3(x, w);
-  uint8_t* at = (uint8_t*)row + p.column(0);
-  if (p.own(0) && p.own(V - 1)) {
+#pragma unroll
+  for (int i = 0; i < V / 4; i++) {
+    const int v = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i], x[4 * i + 1], 0, false);
+    w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i + 2], x[4 * i + 3], v, true);
+  }
+  uint8_t* at = (uint8_t*)row + p.at();
+  if (K == kInside || (K == kEnd && p.t.skip == 0)) {
     Words v;
     if constexpr (V == 8) v = Words{w[0], w[1]};
     else v = Words{w[0]};
-    *(__attribute__((address_space(1))) Words*)at = v;
+    __builtin_nontemporal_store(v, (__attribute__((address_space(1))) Words*)at);
   } else {
 #pragma unroll
     for (int i = 0; i < V; i++)
@@ -44,7 +42,7 @@ __device__ __forceinline__ void store_e4m3(void* row, const RowPart<DT, TINY>& p
   }
 }
 
-// the largest of `lanes` (4 to 32) neighbouring lanes
+// the largest of `lanes` (4, 8, 16 or 32) neighbouring lanes
 __device__ __forceinline__ float max_of(float v, int lanes) {
   v = fmaxf(v, dpp<kDppPair>(v));
   v = fmaxf(v, dpp<kDppQuad>(v));
@@ -53,156 +51,163 @@ __device__ __forceinline__ float max_of(float v, int lanes) {
   if (lanes >= 32) v = across_rows(v, [](float a, float b) { return fmaxf(a, b); });
   return v;
 }
-
-// factors of g h on its way to e4m3: q = e4m3(g h * up * inv).  A largest value
-// near the type's smallest ones is scaled up first, so that 448 over it is finite.
-struct Quant {
-  float up, inv;
-  __device__ __forceinline__ explicit Quant(float top) {
-    up = top < 0x1p-80f ? 0x1p80f : 1.0f;
-    inv = top > 0.0f ? 448.0f / (top * up) : 0.0f;
-  }
-};
-
-// NT threads hold a row, R vectors each; four rows share a workgroup where a
-// wave holds one.
-template <int DT, int NT, int R, bool TINY>
-__global__ void __launch_bounds__(NT < 256 ? 256 : NT) k_norm(NormArgs a) {
-  constexpr int V = epv<DT>(), W = NT / 64, ROWS = NT < 256 ? 256 / NT : 1;
-  __shared__ float sum_s[2][W], top_s[2][W];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = NT == 64 ? 0 : tid >> 6, l = NT == 64 ? lane : tid;
-  const uint32_t cols = (uint32_t)a.cols;
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * ROWS + (NT == 64 ? tid >> 6 : 0); row < a.rows;
-       row += (int64_t)gridDim.x * ROWS, turn ^= 1) {
-    const char* x = (const char*)a.x + row * a.x_stride * Ty<DT>::E;
-    float h[R][V], g[R][V];
-    u32x4 v[R];
+template <int V>
+__device__ __forceinline__ float largest(const float (&x)[V]) {
+  float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < R; i++) v[i] = RowPart<DT, TINY>((i * NT + l) * V, cols).load(x);
+  for (int t = 0; t < V; t++) m = fmaxf(m, fabsf(x[t]));
+  return m;
+}
+
+// g h on its way to e4m3.  448 / m by the hardware's reciprocal (1 ulp): the
+// largest value becomes 448 within 2 ulp, which rounds to 448.  Near the type's
+// smallest values m and g h are scaled up first, so that 448 / m is finite and m
+// no denormal number, which the reciprocal would take for 0.
+template <int V>
+__device__ __forceinline__ void quantise(float (&x)[V], float m) {
+  if (__builtin_expect(m < 0x1p-100f, 0)) {
+#pragma unroll
+    for (int t = 0; t < V; t++) x[t] *= 0x1p100f;
+    m *= 0x1p100f;
+  }
+  const float f = m > 0.0f ? kE4m3Max * __builtin_amdgcn_rcpf(m) : 0.0f;
+#pragma unroll
+  for (int t = 0; t < V; t++) x[t] *= f;
+}
+
+// L lanes (8, 16, 32 or 64; several rows share a workgroup of 256 threads) or, with
+// L = 0, a workgroup take a row, R vectors per thread.
+template <int DT, int L, int R, bool TINY>
+__global__ void __launch_bounds__(L ? 256 : 1024) k_norm(NormArgs a) {
+  constexpr int V = epv<DT>(), G = L ? L : 64;
+  // With one vector g h stays in registers; with more the gain is loaded again, so
+  // that two workgroups have room (16,384 x 8,192 bf16 151 us, 157.5 held).
+  constexpr bool HOLD = R == 1;
+  __shared__ float sum_s[2][16], top_s[2][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int waves = blockDim.x >> 6;
+  const RowVectors<DT, R, TINY> vectors{L ? threadIdx.x % G : threadIdx.x, L ? L : blockDim.x, (uint32_t)a.cols};
+  const bool exact = vectors.exact(), one_scale = a.scales && a.group == 0;
+  // (a group of more columns than the row has is the row)
+  const int scale_lanes = L && a.group / V > L ? L : a.group / V;
+  int turn = 0;
+  for (int64_t row = L ? (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G : (int64_t)blockIdx.x; row < a.rows;
+       row += L ? (int64_t)gridDim.x * (256 / G) : (int64_t)gridDim.x, turn ^= 1) {
+    const char* x = (const char*)a.x + row * a.x_stride * Ty<DT>::E;
+    float h[R][V], gh[HOLD ? R : 1][V];
+    u32x4 v[R], w[R];
+    vectors([&](auto i, auto p) __attribute__((always_inline)) { v[i] = p.load(x); });
     if (a.residual) {
       const char* res = (const char*)a.residual + row * a.residual_stride * Ty<DT>::E;
-      u32x4 w[R];
-#pragma unroll
-      for (int i = 0; i < R; i++) w[i] = RowPart<DT, TINY>((i * NT + l) * V, cols).load(res);
-#pragma unroll
-      for (int i = 0; i < R; i++) load_gain(a.gain, a.gain_dtype, RowPart<DT, TINY>((i * NT + l) * V, cols), g[i]);
-#pragma unroll
-      for (int i = 0; i < R; i++) {
-        float f[V];
-        unpack<DT>(v[i], h[i]);
-        unpack<DT>(w[i], f);
-#pragma unroll
-        for (int t = 0; t < V; t++) h[i][t] += f[t];
-      }
+      vectors([&](auto i, auto p) __attribute__((always_inline)) { w[i] = p.load(res); });
     } else {
 #pragma unroll
-      for (int i = 0; i < R; i++) load_gain(a.gain, a.gain_dtype, RowPart<DT, TINY>((i * NT + l) * V, cols), g[i]);
-#pragma unroll
-      for (int i = 0; i < R; i++) unpack<DT>(v[i], h[i]);
+      for (int i = 0; i < R; i++) w[i] = u32x4{0, 0, 0, 0};
     }
+    if constexpr (HOLD)
+      vectors([&](auto i, auto p) __attribute__((always_inline)) { load_gain(a.gain, a.gain_dtype, p, gh[i]); });
     float sum = 0.0f, top = 0.0f;
+    vectors([&](auto i, auto p) __attribute__((always_inline)) {
+      float f[V];
+      unpack<DT>(v[i], h[i]);
+      unpack<DT>(w[i], f);
 #pragma unroll
-    for (int i = 0; i < R; i++) {
-      const RowPart<DT, TINY> p((i * NT + l) * V, cols);
+      for (int t = 0; t < V; t++) h[i][t] += f[t];
+      if (i == R - 1 && !exact) p.mask(h[i]);
 #pragma unroll
-      for (int t = 0; t < V; t++) {
-        const float f = p.own(t) ? h[i][t] : 0.0f;
-        sum = __builtin_fmaf(f, f, sum);
-        g[i][t] *= h[i][t];
+      for (int t = 0; t < V; t++) sum = __builtin_fmaf(h[i][t], h[i][t], sum);
+      if constexpr (HOLD) {
+#pragma unroll
+        for (int t = 0; t < V; t++) gh[i][t] *= h[i][t];
       }
-    }
-    if (a.scales && a.group == 0) {
+    });
+    const auto gained = [&](auto i, auto p, float (&x)[V]) __attribute__((always_inline)) {
+      if constexpr (!HOLD) load_gain(a.gain, a.gain_dtype, p, x);
 #pragma unroll
-      for (int i = 0; i < R; i++) {
-        const RowPart<DT, TINY> p((i * NT + l) * V, cols);
-#pragma unroll
-        for (int t = 0; t < V; t++) top = fmaxf(top, p.own(t) ? fabsf(g[i][t]) : 0.0f);
-      }
-      top = wave_max(top);
+      for (int t = 0; t < V; t++) x[t] = HOLD ? gh[HOLD ? decltype(i)::value : 0][t] : x[t] * h[i][t];
+    };
+    sum = group_sum<G>(sum);
+    if (one_scale) {
+      vectors([&](auto i, auto p) __attribute__((always_inline)) {
+        float x[V];
+        gained(i, p, x);
+        top = fmaxf(top, largest(x));
+      });
+      top = group_max<G>(top);
     }
-    sum = wave_sum(sum);
-    if constexpr (W > 1) {
+    if (!L && waves > 1) {
       if (lane == 0) {
         sum_s[turn][wave] = sum;
         top_s[turn][wave] = top;
       }
       __syncthreads();
-      sum = wave_sum(lane < W ? sum_s[turn][lane] : 0.0f);
-      if (a.scales && a.group == 0) top = wave_max(lane < W ? top_s[turn][lane] : 0.0f);
+      sum = group_sum<16>((lane & 15) < waves ? sum_s[turn][lane & 15] : 0.0f);
+      if (one_scale) top = group_max<16>((lane & 15) < waves ? top_s[turn][lane & 15] : 0.0f);
     }
-    const float r = 1.0f / __builtin_sqrtf(sum / (float)cols + a.eps);
+    const float r = 1.0f / __builtin_sqrtf(sum / (float)a.cols + a.eps);
     if (a.sum) {
       char* to = (char*)a.sum + row * a.sum_stride * Ty<DT>::E;
-#pragma unroll
-      for (int i = 0; i < R; i++) {
-        const RowPart<DT, TINY> p((i * NT + l) * V, cols);
+      vectors([&](auto i, auto p) __attribute__((always_inline)) {
         if (p.any()) p.store(to, h[i]);
-      }
+      });
     }
     if (!a.scales) {
       char* to = (char*)a.out + row * a.out_stride * Ty<DT>::E;
+      vectors([&](auto i, auto p) __attribute__((always_inline)) {
+        float x[V];
+        gained(i, p, x);
 #pragma unroll
-      for (int i = 0; i < R; i++) {
-        const RowPart<DT, TINY> p((i * NT + l) * V, cols);
-#pragma unroll
-        for (int t = 0; t < V; t++) g[i][t] *= r;
-        if (p.any()) p.store(to, g[i]);
-      }
+        for (int t = 0; t < V; t++) x[t] *= r;
+        if (p.any()) p.store(to, x);
+      });
       continue;
     }
     char* to = (char*)a.out + row * a.out_stride;
     float* scales = a.scales + row * a.groups;
-#pragma unroll
-    for (int i = 0; i < R; i++) {
-      const RowPart<DT, TINY> p((i * NT + l) * V, cols);
-      float m = top;
+    const float unit = r * (1.0f / kE4m3Max);
+    vectors([&](auto i, auto p) __attribute__((always_inline)) {
+      float x[V], m = top;
+      gained(i, p, x);
       if (a.group) {
-        m = 0.0f;
-#pragma unroll
-        for (int t = 0; t < V; t++) m = fmaxf(m, p.own(t) ? fabsf(g[i][t]) : 0.0f);
-        m = max_of(m, a.group / V);
-        if (p.any() && p.col % (uint32_t)a.group == 0) scales[p.col / (uint32_t)a.group] = m * r / 448.0f;
+        m = max_of(largest(x), scale_lanes);
+        if (p.any() && p.col % (uint32_t)a.group == 0) scales[p.col / (uint32_t)a.group] = m * unit;
       } else if (p.col == 0) {
-        scales[0] = m * r / 448.0f;
+        scales[0] = m * unit;
       }
-      const Quant q(m);
-#pragma unroll
-      for (int t = 0; t < V; t++) g[i][t] = g[i][t] * q.up * q.inv;
-      if (p.any()) store_e4m3(to, p, g[i]);
-    }
+      quantise(x, m);
+      if (p.any()) store_e4m3(to, p, x);
+    });
   }
 }
 
-template <int DT, int NT, int R, bool TINY = false>
-hipError_t go(const NormArgs& a, hipStream_t s) {
-  constexpr int ROWS = NT < 256 ? 256 / NT : 1;
-  const int64_t wg = (a.rows + ROWS - 1) / ROWS;
+template <int DT, int L, int R, bool TINY = false>
+hipError_t go(const NormArgs& a, int threads, hipStream_t s) {
+  if (!TINY && !row_vectors_fit(a.cols, epv<DT>(), threads, R)) return hipErrorInvalidValue;
+  const int64_t each = L ? 256 / L : 1, wg = (a.rows + each - 1) / each;
   const int64_t most = (int64_t)1 << 21;  // (a launch has fewer than 2^32 threads)
-  return launch<k_norm<DT, NT, R, TINY>>(dim3((unsigned)(wg < most ? wg : most)), dim3(NT < 256 ? 256 : NT), s, a);
+  return launch<k_norm<DT, L, R, TINY>>(dim3((unsigned)(wg < most ? wg : most)), dim3(L ? 256 : threads), s, a);
 }
 
 template <int DT>
 hipError_t pick(const NormArgs& a, hipStream_t s) {
   constexpr int V = epv<DT>();
   const int64_t nv = ((int64_t)a.cols + V - 1) / V;
-  if (a.cols < V) return go<DT, 64, 1, true>(a, s);
-  if (nv <= 64) return go<DT, 64, 1>(a, s);
-  if (nv <= 128) return go<DT, 64, 2>(a, s);
-  if (a.rows >= 4 * library_cus()) {
-    if (nv <= 256) return go<DT, 256, 1>(a, s);
-    if (nv <= 512) return go<DT, 256, 2>(a, s);
-    if (nv <= 768) return go<DT, 256, 3>(a, s);
-    if (nv <= 1024) return go<DT, 256, 4>(a, s);
-    if constexpr (V == 4)
-      if (nv <= 2048) return go<DT, 256, 8>(a, s);
-  }
-  if (nv <= 256) return go<DT, 256, 1>(a, s);
-  if (nv <= 1024) return go<DT, 1024, 1>(a, s);
-  if (nv <= 2048) return go<DT, 1024, 2>(a, s);
-  if (nv <= 4096) return go<DT, 1024, 4>(a, s);
-  if constexpr (V == 4) return go<DT, 1024, 8>(a, s);
+  if (a.cols < V) return go<DT, 8, 1, true>(a, 8, s);
+  if (nv <= 8) return go<DT, 8, 1>(a, 8, s);
+  if (nv <= 16) return go<DT, 16, 1>(a, 16, s);
+  if (nv <= 32) return go<DT, 32, 1>(a, 32, s);
+  if (nv <= 64) return go<DT, 64, 1>(a, 64, s);
+  if (nv <= 128) return go<DT, 64, 2>(a, 64, s);
+  // Two vectors per thread leave room for another row's workgroup on the same
+  // compute unit; a row by itself is done sooner with one (16,384 x 8,192 bf16
+  // 156 us, 225 with one; 1 x 8,192 5.7 us, 6.0 with two).
+#ifndef X_F
+#define X_F 1
+#endif
+  if (nv <= 1024 && a.rows <= X_F * library_cus()) return go<DT, 0, 1>(a, row_threads(nv, 1), s);
+  if (nv <= 2048) return go<DT, 0, 2>(a, row_threads(nv, 2), s);
+  if (nv <= 4096) return go<DT, 0, 4>(a, row_threads(nv, 4), s);
+  if constexpr (V == 4) return go<DT, 0, 8>(a, row_threads(nv, 8), s);
   return hipErrorInvalidValue;  // (rows of more than SIM_NORM_MAX_COLUMNS are refused before)
 }
 

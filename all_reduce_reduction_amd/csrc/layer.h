@@ -105,8 +105,8 @@ struct CombineGradArgs {
   float* dweights;       // NULL: not wanted
 };
 
-// Tensors are cut into pieces of so many elements.
-constexpr int kClipPiece = 16384;
+// Tensors are cut into pieces.
+constexpr int kClipPieceBytes = 16384;
 // Tensors of one launch: the kernel's argument block stays below 4 KiB.
 constexpr int kClipTensors = 120;
 struct ClipList {
@@ -130,9 +130,26 @@ struct ClipNorm {
 };
 
 // layer_sizes.cpp
+// Threads of a row, and 16-byte vectors of each.  The least threads, in whole
+// waves, that hold a row: only the last vector of a thread may then lie past the
+// row's end.
+inline int row_threads(int64_t vectors, int per_thread) {
+  return (int)((vectors + 64 * per_thread - 1) / (64 * per_thread)) * 64;
+}
+inline bool row_vectors_fit(int64_t cols, int per_vector, int threads, int per_thread) {
+  return (int64_t)threads * per_thread * per_vector >= cols &&
+         (int64_t)threads * (per_thread - 1) * per_vector <= cols;
+}
+// A gradient's rows: `lanes` lanes of a workgroup of kNormShortThreads (0: a whole
+// workgroup of `threads`) take a row, per_thread vectors each.
+constexpr int kNormShortThreads = 512;
+struct NormGradShape {
+  int lanes, per_thread, threads;
+};
+NormGradShape norm_grad_shape(int64_t cols, int per_vector);
 int norm_grad_workgroups(int64_t rows, int64_t cols, int dtype);
 int dispatch_chunks(int64_t slots, int64_t* chunk);  // 0: one launch for all slots
-int64_t clip_pieces(int64_t count);
+int64_t clip_pieces(int64_t count, int dtype);
 int clip_workgroups(uint32_t pieces);
 
 hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t s);

@@ -31,7 +31,7 @@ static bool whole(const ClipList& l) {
   int64_t pieces = 0;
   for (int t = 0; t < l.tensors; t++) {
     if (l.first[t] != pieces || l.count[t] <= 0) return false;
-    pieces += clip_pieces(l.count[t]);
+    pieces += clip_pieces(l.count[t], l.dtype[t]);
   }
   return l.tensors >= 1 && l.tensors <= kClipTensors && pieces == l.pieces;
 }
