@@ -552,7 +552,7 @@ if torch is not None:
     _FLOATS = tuple(_TORCH_CODE)
 
 _ENTRIES = ("route", "route_grad", "distill_step", "distill_parts", "distill_join", "distill_grad", "norm", "norm_grad",
-            "dispatch", "combine", "combine_grad", "clip_norm", "clip")
+            "dispatch", "combine", "combine_grad", "clip_work", "clip_norm", "clip")
 
 
 def _vec_py(t, what, dtypes, device, *shape):
@@ -590,6 +590,24 @@ def _slots_py(ids, teacher, dtypes, rows, device):
             _TORCH_CODE[teacher.dtype], k)
 
 
+def _like_py(t, what, like):
+    """The first two of _rows' for a tensor like another one; of None, None and the columns."""
+    return (None, like[3]) if t is None else _rows_py(t, what, like)[:2]
+
+
+def _gain_py(gain, columns, device):
+    """(pointer, type code) of a norm's gain (None: all 1)."""
+    if gain is None:
+        return None, 1
+    return _vec_py(gain, "gain", _FLOATS, device, columns), _TORCH_CODE[gain.dtype]
+
+
+def _clip_work_py(counts, dtypes, n):
+    nb = ctypes.c_size_t(0)
+    rc = lib.sim_clip_work(counts, dtypes, n, ctypes.byref(nb))
+    return rc or nb.value
+
+
 def _raw_py(t, what, dtype):
     """(pointer, bytes from row to row, rows, bytes of a row, device index) of a 2-D device tensor of any type whose
     rows are contiguous; dtype: the one it must have, or None."""
@@ -618,18 +636,20 @@ def _tensors_py(ts, what, device, like):
     return got
 
 
-if hasattr(_pycall, "tensors") and torch is not None:
+if hasattr(_pycall, "clip_work") and torch is not None:
     # arguments converted and tensors checked in C: of a small call's 7.3 us on the host, ctypes and the same checks
     # in Python took about 3
     for _name in _ENTRIES:
         _pycall.bind(_name, ctypes.cast(lib["sim_" + _name], ctypes.c_void_p).value)
     _pycall.types(*_FLOATS)
     _entry, _vec, _rows, _slots = _pycall, _pycall.pointer, _pycall.rows, _pycall.slots
-    _raw, _tensors = _pycall.raw, _pycall.tensors
+    _raw, _tensors, _like, _gain = _pycall.raw, _pycall.tensors, _pycall.like, _pycall.gain
+    _clip_bytes = _pycall.clip_work
 else:
     import types as _types
     _entry, _vec = _types.SimpleNamespace(**{n: getattr(lib, "sim_" + n) for n in _ENTRIES}), _vec_py
-    _rows, _slots, _raw, _tensors = _rows_py, _slots_py, _raw_py, _tensors_py
+    _rows, _slots, _raw, _tensors, _like, _gain = _rows_py, _slots_py, _raw_py, _tensors_py, _like_py, _gain_py
+    _clip_bytes = _clip_work_py
 
 
 def _on(stream, device):
@@ -785,13 +805,6 @@ def _here(device):
         raise ValueError(f"tensors must be on cuda:{_device}, the device that sim_init chose")
 
 
-def _gain(gain, columns, device):
-    """(pointer, type code) of a norm's gain (None: all 1)."""
-    if gain is None:
-        return None, 1
-    return _vec(gain, "gain", _FLOATS, device, columns), _TORCH_CODE[gain.dtype]
-
-
 def norm(x, gain=None, residual=None, eps: float = 1e-6, out=None, stream=None):
     """Root-mean-square norm of the rows of x (+ residual): (y, x + residual; without a residual None); ``sim_norm`` in
     include/simar.h says what each holds.  out: the same two, to write into (each may be x or residual)."""
@@ -801,11 +814,12 @@ def norm(x, gain=None, residual=None, eps: float = 1e-6, out=None, stream=None):
         out = (_empty((n, c), x.dtype, dev, stream),
                None if residual is None else _empty((n, c), x.dtype, dev, stream))
     y, total = out
-    yp, yld, *_ = _rows(y, "y", mine)
-    rp, rld, *_ = (None, c) if residual is None else _rows(residual, "residual", mine)
-    tp, tld, *_ = (None, c) if total is None else _rows(total, "total", mine)
-    _check(_entry.norm(ptr, ld, dt, rp, rld, n, c, *_gain(gain, c, dev), eps, tp, tld, yp, yld, None, 0,
-                       _on(stream, dev)), "sim_norm")
+    yp, yld = _like(y, "y", mine)
+    rp, rld = _like(residual, "residual", mine)
+    tp, tld = _like(total, "total", mine)
+    gp, gdt = _gain(gain, c, dev)
+    _check(_entry.norm(ptr, ld, dt, rp, rld, n, c, gp, gdt, eps, tp, tld, yp, yld, None, 0, _on(stream, dev)),
+           "sim_norm")
     return out
 
 
@@ -822,11 +836,12 @@ def norm_quant(x, gain=None, residual=None, eps: float = 1e-6, group: int = 128,
                None if residual is None else _empty((n, c), x.dtype, dev, stream))
     q, scales, total = out
     qp, qld, qn, qc, qdev = _raw(q, "q", _E4M3)
-    if (qn, qc, qdev) != (n, c, dev):
+    if qn != n or qc != c or qdev != dev:
         raise ValueError("q must have x's shape and device")
-    rp, rld, *_ = (None, c) if residual is None else _rows(residual, "residual", mine)
-    tp, tld, *_ = (None, c) if total is None else _rows(total, "total", mine)
-    _check(_entry.norm(ptr, ld, dt, rp, rld, n, c, *_gain(gain, c, dev), eps, tp, tld, qp, qld,
+    rp, rld = _like(residual, "residual", mine)
+    tp, tld = _like(total, "total", mine)
+    gp, gdt = _gain(gain, c, dev)
+    _check(_entry.norm(ptr, ld, dt, rp, rld, n, c, gp, gdt, eps, tp, tld, qp, qld,
                        _vec(scales, "scales", _F32, dev, n, groups), 0 if group == c else group,
                        _on(stream, dev)), "sim_norm")
     return out
@@ -841,12 +856,13 @@ def norm_grad(total, gain, dout, dtotal=None, eps: float = 1e-6, out=None, strea
     if out is None:
         out = (_empty((n, c), total.dtype, dev, stream), _empty(c, torch.float32, dev, stream))
     dx, dgain = out
-    dp, dld, *_ = _rows(dx, "dx", mine)
-    op, old, *_ = _rows(dout, "dout", mine)
-    tp, tld, *_ = (None, c) if dtotal is None else _rows(dtotal, "dtotal", mine)
+    dp, dld = _like(dx, "dx", mine)
+    op, old = _like(dout, "dout", mine)
+    tp, tld = _like(dtotal, "dtotal", mine)
+    gp, gdt = _gain(gain, c, dev)
     nb = 0 if dgain is None else sim_norm_grad_work(n, c, dt)
     w, wp = _work(nb, dev, stream)
-    _check(_entry.norm_grad(ptr, ld, dt, n, c, *_gain(gain, c, dev), eps, op, old, tp, tld, dp, dld,
+    _check(_entry.norm_grad(ptr, ld, dt, n, c, gp, gdt, eps, op, old, tp, tld, dp, dld,
                             _vec(dgain, "dgain", _F32, dev, c), wp, nb, _on(stream, dev)), "sim_norm_grad")
     return out
 
@@ -868,7 +884,7 @@ def dispatch(x, chosen, experts: int, scales=None, out=None, stream=None):
                None if scales is None else _empty((n * k, groups), torch.float32, dev, stream))
     rows, place, offsets, row_scales = out
     rp, rpitch, rn, rnb, rdev = _raw(rows, "rows", x.dtype)
-    if (rn, rnb, rdev) != (n * k, nb, dev):
+    if rn != n * k or rnb != nb or rdev != dev:
         raise ValueError("rows must be [tokens * topk, columns] on x's device")
     if (scales is None) != (row_scales is None):
         raise ValueError("scales and the rows' scales: both or neither")
@@ -892,7 +908,7 @@ def combine(rows, place, weights=None, out=None, stream=None):
     n, k = place.shape
     if out is None:
         out = _empty((n, c), rows.dtype, dev, stream)
-    op, old, *_ = _rows(out, "out", (None, None, n, c, dt, dev))
+    op, old = _like(out, "out", (None, None, n, c, dt, dev))
     _check(_entry.combine(ptr, ld, dt, m, c, _vec(place, "place", _I32, dev, n, k),
                           _vec(weights, "weights", _F32, dev, n, k), n, k, op, old, _on(stream, dev)), "sim_combine")
     return out
@@ -909,8 +925,8 @@ def combine_grad(dout, rows, place, weights=None, out=None, stream=None):
     into (drows may be the rows; either may be None: not wanted)."""
     dp, dld, n, c, dt, dev = _rows(dout, "dout", None)
     _here(dev)
-    rp, rld, m, *_ = theirs = _rows(rows, "rows", None)
-    if theirs[3:] != (c, dt, dev):
+    rp, rld, m, rc, rdt, rdev = theirs = _rows(rows, "rows", None)
+    if rc != c or rdt != dt or rdev != dev:
         raise ValueError("rows must have dout's columns, dtype and device")
     if place.dim() != 2:
         raise ValueError("place must be [tokens, topk]")
@@ -918,7 +934,7 @@ def combine_grad(dout, rows, place, weights=None, out=None, stream=None):
     if out is None:
         out = (_empty((m, c), rows.dtype, dev, stream), _empty((n, k), torch.float32, dev, stream))
     drows, dweights = out
-    gp, gld, *_ = (None, c) if drows is None else _rows(drows, "drows", theirs)
+    gp, gld = _like(drows, "drows", theirs)
     _check(_entry.combine_grad(dp, dld, dt, rp, rld, m, c, _vec(place, "place", _I32, dev, n, k),
                                _vec(weights, "weights", _F32, dev, n, k), n, k, gp, gld,
                                _vec(dweights, "dweights", _F32, dev, n, k), _on(stream, dev)), "sim_combine_grad")
@@ -935,9 +951,10 @@ def _list_device(grads):
 
 def _clip_work(lists, n, device, stream):
     """Scratch of a norm over a list: (tensor, pointer, bytes)."""
-    nb = ctypes.c_size_t(0)
-    _check(lib.sim_clip_work(lists[1], lists[2], n, ctypes.byref(nb)), "sim_clip_work")
-    return (*_work(nb.value, device, stream), nb.value)
+    nb = _clip_bytes(lists[1], lists[2], n)
+    if nb < 0:
+        raise SimError(nb, "sim_clip_work")
+    return (*_work(nb, device, stream), nb)
 
 
 def grad_norm(grads, out=None, stream=None):

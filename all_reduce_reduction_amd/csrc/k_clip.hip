@@ -81,7 +81,7 @@ __device__ __forceinline__ void squares_of(const char* in, int n, double& sum) {
   if (n == kVectors * V) {
     u32x4 v[kEach];
 #pragma unroll
-    for (int i = 0; i < kEach; i++) v[i] = ld_row_lane<DT, true>(in, 0, (i * kBlock + threadIdx.x) * V);
+    for (int i = 0; i < kEach; i++) v[i] = ld_row_lane<DT, false>(in, 0, (i * kBlock + threadIdx.x) * V);
 #pragma unroll
     for (int i = 0; i < kEach; i++) add_squares<DT>(v[i], sum);
   } else {
@@ -103,13 +103,11 @@ __device__ __forceinline__ u32x4 scaled(u32x4 v, float c) {
   for (int t = 0; t < V; t++) f[t] *= c;
   return pack_rounded<DT>(f);
 }
+// A whole piece's vectors are given, the others' read.
 template <int DT>
-__device__ __forceinline__ void scale_to(const char* in, char* out, int n, float c) {
+__device__ __forceinline__ void scale_to(const char* in, char* out, int n, float c, const u32x4 (&v)[kEach]) {
   constexpr int V = epv<DT>();
   if (n == kVectors * V) {
-    u32x4 v[kEach];
-#pragma unroll
-    for (int i = 0; i < kEach; i++) v[i] = ld_row_lane<DT, true>(in, 0, (i * kBlock + threadIdx.x) * V);
 #pragma unroll
     for (int i = 0; i < kEach; i++) st_row_lane<DT, true>(out, 0, (i * kBlock + threadIdx.x) * V, scaled<DT>(v[i], c));
   } else {
@@ -157,21 +155,27 @@ __global__ void __launch_bounds__(kBlock) k_clip_join(ClipNorm n) {
   if (threadIdx.x == 0) n.norm[0] = norm;
 }
 
+// A workgroup scales one piece, whose vectors are on their way while the norm is
+// found.  The last pieces come first: they are what the squares' pass, which reads
+// without the streaming hint, left in the caches (235 MB of bf16 111 us, 115 with
+// the hint and from the front).
 __global__ void __launch_bounds__(kBlock) SIMAR_CLIP_WAVES k_clip_scale(ClipList l, ClipNorm n) {
-  const Tensors all(l);
+  const Piece p(l, Tensors(l), gridDim.x - 1 - blockIdx.x);
+  const char* in = (const char*)l.in[p.t] + p.byte;
+  char* out = (char*)l.out[p.t] + p.byte;
+  u32x4 v[kEach] = {};
+  if (p.n * (p.dtype == SIM_FP32 ? 4 : 2) == kClipPieceBytes) {
+#pragma unroll
+    for (int i = 0; i < kEach; i++) v[i] = ld_row_lane<SIM_BF16, true>(in, 0, (i * kBlock + threadIdx.x) * 8);
+  }
   const float norm = norm_of(n);
   if (n.norm && blockIdx.x == 0 && threadIdx.x == 0) n.norm[0] = norm;
   // (a NaN norm makes everything NaN)
   const float c = norm <= n.max_norm ? 1.0f : (float)((double)n.max_norm / (double)norm);
   if (n.in_place && c == 1.0f) return;
-  for (uint32_t piece = blockIdx.x; piece < l.pieces; piece += gridDim.x) {
-    const Piece p(l, all, piece);
-    const char* in = (const char*)l.in[p.t] + p.byte;
-    char* out = (char*)l.out[p.t] + p.byte;
-    if (p.dtype == SIM_FP32) scale_to<SIM_FP32>(in, out, p.n, c);
-    else if (p.dtype == SIM_FP16) scale_to<SIM_FP16>(in, out, p.n, c);
-    else scale_to<SIM_BF16>(in, out, p.n, c);
-  }
+  if (p.dtype == SIM_FP32) scale_to<SIM_FP32>(in, out, p.n, c, v);
+  else if (p.dtype == SIM_FP16) scale_to<SIM_FP16>(in, out, p.n, c, v);
+  else scale_to<SIM_BF16>(in, out, p.n, c, v);
 }
 
 }  // namespace

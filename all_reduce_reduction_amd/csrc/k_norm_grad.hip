@@ -13,13 +13,13 @@
 namespace simar {
 namespace {
 
-// A row's vectors of a thread.  With one each, the next row's are asked for before
-// this one's are used; with four or more the gain and dsum are loaded where they
+// A row's vectors of a thread.  With eight elements each, the next row's are asked
+// for before this one's are used; with four vectors or more the gain and dsum are loaded where they
 // are needed, as they do not fit in the registers beside the others.
 template <int DT, int R>
 __global__ void __launch_bounds__(1024) k_norm_grad(NormGradArgs a) {
   constexpr int V = epv<DT>();
-  constexpr bool AHEAD = R == 1, HOLD = R <= 2;
+  constexpr bool AHEAD = R * V <= 8, HOLD = R <= 2;
   __shared__ float ss_s[2][16], dot_s[2][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const RowVectors<DT, R, false> vectors{threadIdx.x, blockDim.x, (uint32_t)a.cols};
@@ -273,7 +273,8 @@ hipError_t pick(const NormGradArgs& a, hipStream_t s) {
   if (f.lanes == 16) return go_short<DT, 16, 1>(a, s);
   if (f.lanes == 32) return go_short<DT, 32, 1>(a, s);
   if (f.lanes == 64) return f.per_thread == 1 ? go_short<DT, 64, 1>(a, s) : go_short<DT, 64, 2>(a, s);
-  if (f.per_thread == 1) return go<DT, 1>(a, f.threads, s);
+  if constexpr (V == 8)
+    if (f.per_thread == 1) return go<DT, 1>(a, f.threads, s);
   if (f.per_thread == 2) return go<DT, 2>(a, f.threads, s);
   if (f.per_thread == 4) return go<DT, 4>(a, f.threads, s);
   if constexpr (V == 4) return go<DT, 8>(a, f.threads, s);

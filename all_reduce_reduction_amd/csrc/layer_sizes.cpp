@@ -10,7 +10,8 @@ namespace simar {
 NormGradShape norm_grad_shape(int64_t cols, int per_vector) {
   const int64_t nv = (cols + per_vector - 1) / per_vector;
   if (nv <= 128) return {nv <= 8 ? 8 : nv <= 16 ? 16 : nv <= 32 ? 32 : 64, nv <= 64 ? 1 : 2, kNormShortThreads};
-  const int r = nv <= 1024 ? 1 : nv <= 2048 ? 2 : nv <= 4096 ? 4 : 8;
+  // (eight elements where a workgroup has the threads for it)
+  const int r = nv <= 1024 && per_vector == 8 ? 1 : nv <= 2048 ? 2 : nv <= 4096 ? 4 : 8;
   return {0, r, row_threads(nv, r)};
 }
 int norm_grad_workgroups(int64_t rows, int64_t cols, int dtype) {

@@ -128,6 +128,7 @@ ENTRY(norm_grad);
 ENTRY(dispatch);
 ENTRY(combine);
 ENTRY(combine_grad);
+ENTRY(clip_work);
 ENTRY(clip_norm);
 ENTRY(clip);
 
@@ -235,7 +236,7 @@ static PyObject* py_bind(PyObject* self, PyObject* args) {
 #define SET(entry) \
   if (!strcmp(name, #entry)) { entry##_fn = (__typeof__(sim_##entry)*)(uintptr_t)at; Py_RETURN_NONE; }
   SET(route) SET(route_grad) SET(distill_step) SET(distill_parts) SET(distill_join) SET(distill_grad)
-  SET(norm) SET(norm_grad) SET(dispatch) SET(combine) SET(combine_grad) SET(clip_norm) SET(clip)
+  SET(norm) SET(norm_grad) SET(dispatch) SET(combine) SET(combine_grad) SET(clip_work) SET(clip_norm) SET(clip)
   PyErr_Format(PyExc_ValueError, "no entry point %s", name);
   return NULL;
 }
@@ -290,12 +291,24 @@ static int pair_of(PyObject* v, long long* a, long long* b) {
 /* rows(tensor, what, like): (pointer, row stride, rows, columns, type code,
  * device index) of a 2-D device tensor with contiguous rows; like: None, or
  * the tuple of a tensor whose shape, type and device it must have. */
+static PyObject* rows_of(PyObject* const* a, int brief);
 static PyObject* py_rows(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
-  if (n != 3) {
-    PyErr_SetString(PyExc_TypeError, "rows(tensor, what, like)");
+  if (n == 3) return rows_of(a, 0);
+  PyErr_SetString(PyExc_TypeError, "rows(tensor, what, like)");
+  return NULL;
+}
+/* like(tensor, what, like): the first two of rows()'s; of None, None and the
+ * columns */
+static PyObject* py_like(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 3 || !PyTuple_Check(a[2]) || PyTuple_GET_SIZE(a[2]) != 6) {
+    PyErr_SetString(PyExc_TypeError, "like(tensor, what, a tuple that rows() returned)");
     return NULL;
   }
+  return a[0] == Py_None ? Py_BuildValue("(OO)", Py_None, PyTuple_GET_ITEM(a[2], 3)) : rows_of(a, 1);
+}
+static PyObject* rows_of(PyObject* const* a, int brief) {
   long long rows = 0, cols = 0, ld = 0, step = 0;
   PyObject* v = PyObject_GetAttr(a[0], s_shape);
   if (!v) return NULL;
@@ -330,7 +343,7 @@ static PyObject* py_rows(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     if (!ok) return PyErr_Format(PyExc_ValueError, "%S must have the first tensor's shape, dtype and device", a[1]);
   }
   if (!(v = PyObject_CallMethodNoArgs(a[0], s_data_ptr))) return NULL;
-  return Py_BuildValue("(NLLLil)", v, ld, rows, cols, code, dev);
+  return brief ? Py_BuildValue("(NL)", v, ld) : Py_BuildValue("(NLLLil)", v, ld, rows, cols, code, dev);
 }
 
 /* whether a tensor is contiguous, on that device, of that shape and one of
@@ -397,6 +410,28 @@ static PyObject* py_pointer(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   const long dev = PyLong_AsLong(a[3]);
   if (PyErr_Occurred()) return NULL;
   return pointer_of(a[0], a[1], PySequence_Fast_ITEMS(a[2]), PyTuple_GET_SIZE(a[2]), dev, shape, n - 4);
+}
+
+/* gain(tensor, columns, device index): (pointer, type code) of a contiguous
+ * tensor of that many floats; of None, None and fp32's code */
+static PyObject* s_gain;
+static PyObject* py_gain(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 3) {
+    PyErr_SetString(PyExc_TypeError, "gain(tensor, columns, device)");
+    return NULL;
+  }
+  if (a[0] == Py_None) return Py_BuildValue("(Oi)", Py_None, 1);
+  const long long shape[1] = {PyLong_AsLongLong(a[1])};
+  const long dev = PyLong_AsLong(a[2]);
+  if (PyErr_Occurred()) return NULL;
+  PyObject* at = pointer_of(a[0], s_gain, logit_type, TYPES, dev, shape, 1);
+  const int code = at ? code_of(a[0]) : -1;
+  if (code < 0) {
+    Py_XDECREF(at);
+    return NULL;
+  }
+  return Py_BuildValue("(Ni)", at, code);
 }
 
 /* slots(ids, teacher, ids' types, rows, device index): (ids pointer, teacher
@@ -524,6 +559,18 @@ static PyObject* py_tensors(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return Py_BuildValue("(NNN)", ptrs, counts, types);
 }
 
+/* clip_work(counts, type codes, number): sim_clip_work's bytes, or its status */
+static PyObject* py_clip_work(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (!ready((const void*)clip_work_fn, n, 3)) return NULL;
+  void *counts = P(0), *types = P(1);
+  const int tensors = I(2);
+  if (PyErr_Occurred()) return NULL;
+  size_t bytes = 0;
+  const int rc = clip_work_fn(counts, types, tensors, &bytes);
+  return rc ? PyLong_FromLong(rc) : PyLong_FromSize_t(bytes);
+}
+
 #define METHOD(name, f, doc) {name, (PyCFunction)(void (*)(void))f, METH_FASTCALL, doc}
 static PyMethodDef pycall_methods[] = {
     {"bind", py_bind, METH_VARARGS, "bind(name, address): set an entry point"},
@@ -537,6 +584,9 @@ static PyMethodDef pycall_methods[] = {
     METHOD("distill_parts", py_distill_parts, "sim_distill_parts"),
     METHOD("distill_join", py_distill_join, "sim_distill_join"),
     METHOD("distill_grad", py_distill_grad, "sim_distill_grad"),
+    METHOD("like", py_like, "like(tensor, what, like): pointer, row stride"),
+    METHOD("gain", py_gain, "gain(tensor, columns, device): pointer, type code"),
+    METHOD("clip_work", py_clip_work, "clip_work(counts, types, number): sim_clip_work's bytes, or its status"),
     METHOD("raw", py_raw, "raw(tensor, what, dtype): pointer, row pitch, rows, row bytes, device"),
     METHOD("tensors", py_tensors, "tensors(sequence, what, device, like): pointers, counts, type codes"),
     METHOD("norm", py_norm, "sim_norm"),
@@ -561,11 +611,12 @@ PyMODINIT_FUNC PyInit__pycall(void) {
   s_contiguous = PyUnicode_InternFromString("is_contiguous");
   s_data_ptr = PyUnicode_InternFromString("data_ptr");
   s_stride = PyUnicode_InternFromString("stride");
+  s_gain = PyUnicode_InternFromString("gain");
   s_esize = PyUnicode_InternFromString("element_size");
   s_numel = PyUnicode_InternFromString("numel");
   s_ids = PyUnicode_InternFromString("ids");
   s_teacher = PyUnicode_InternFromString("teacher");
-  if (!s_dtype || !s_shape || !s_device || !s_contiguous || !s_data_ptr || !s_stride || !s_esize || !s_numel || !s_ids ||
+  if (!s_dtype || !s_shape || !s_device || !s_contiguous || !s_data_ptr || !s_stride || !s_esize || !s_numel || !s_gain || !s_ids ||
       !s_teacher)
     return NULL;
   PyObject* m = PyModule_Create(&pycall_module);

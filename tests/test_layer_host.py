@@ -77,20 +77,20 @@ def test_norm_checks(checks):
 
 def test_norm_grad_checks(checks):
     need = ctypes.c_size_t()
-    assert checks.sim_norm_grad_work(7, 100, BF16, ctypes.byref(need)) == 0 and need.value == 7 * 100 * 4
+    assert checks.sim_norm_grad_work(7, 2000, BF16, ctypes.byref(need)) == 0 and need.value == 7 * 2000 * 4
     assert checks.sim_norm_grad_work(1, 100, BF16, ctypes.byref(need)) == 0 and need.value == 0
     for bad in ((-1, 100, BF16), (7, 0, BF16), (7, 40000, BF16), (7, 100, 0)):
         assert checks.sim_norm_grad_work(*bad, ctypes.byref(need)) == INVALID
     assert checks.sim_norm_grad_work(7, 100, BF16, None) == INVALID
-    good = dict(h=A, h_stride=100, dtype=BF16, rows=7, columns=100, gain=B, gain_dtype=BF16, eps=1e-6, dy=C, dy_stride=100,
-                dsum=D, dsum_stride=100, dx=E, dx_stride=100, dgain=F, work=F + 0x1000, work_bytes=2800, stream=None)
+    good = dict(h=A, h_stride=2000, dtype=BF16, rows=7, columns=2000, gain=B, gain_dtype=BF16, eps=1e-6, dy=C, dy_stride=2000,
+                dsum=D, dsum_stride=2000, dx=E, dx_stride=2000, dgain=F, work=F + 0x10000, work_bytes=56000, stream=None)
     for change in ({}, dict(dsum=None), dict(gain=None), dict(dgain=None, work=None, work_bytes=0), dict(dx=A), dict(dx=C),
                    dict(dx=D), dict(rows=1, work=None, work_bytes=0), dict(rows=0, h=None, dy=None, dx=None, work=None)):
         run(checks, "sim_norm_grad", good, change, 0)
     for change, status in ((dict(h=None), INVALID), (dict(dy=None), INVALID), (dict(dx=None), INVALID), (dict(work=None), INVALID),
-                           (dict(work_bytes=2799), NOMEM), (dict(work=F + 0x1002), ALIGN), (dict(dgain=F + 1), ALIGN),
+                           (dict(work_bytes=55999), NOMEM), (dict(work=F + 0x10002), ALIGN), (dict(dgain=F + 1), ALIGN),
                            (dict(dx=B), ALIAS), (dict(dgain=A), ALIAS), (dict(dgain=E), ALIAS), (dict(work=F), ALIAS),
-                           (dict(dx=A, dx_stride=101), ALIAS), (dict(dx=C + 2), ALIAS), (dict(dy_stride=5), INVALID),
+                           (dict(dx=A, dx_stride=2001), ALIAS), (dict(dx=C + 2), ALIAS), (dict(dy_stride=5), INVALID),
                            (dict(dsum_stride=5), INVALID), (dict(eps=0.0), INVALID), (dict(dtype=7), INVALID)):
         run(checks, "sim_norm_grad", good, change, status)
 
