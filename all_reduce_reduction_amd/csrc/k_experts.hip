@@ -514,6 +514,33 @@ __global__ void __launch_bounds__(W > 1 ? 64 * W : 256) k_combine_grad(CombineGr
   }
 }
 
+// The rows' gradient by itself: a wave takes part of a token's columns, as where
+// rows are only moved.
+template <int DT>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(6, 6))) k_combine_grad_rows(CombineGradArgs a, int parts) {
+  constexpr int V = epv<DT>();
+  const int lane = threadIdx.x & 63;
+  const int64_t step = (int64_t)gridDim.x * 4;
+  for (int64_t unit = (int64_t)blockIdx.x * 4 + wave_uniform(threadIdx.x >> 6); unit < a.tokens * parts; unit += step) {
+    const int64_t token = unit / parts;
+    const TokenSlots s(a.place, a.weights, token, a.topk, a.nrows);
+    const RowPart<DT, kEnd> p(((uint32_t)(unit - token * parts) * 64 + lane) * V, (uint32_t)a.cols);
+    if (!p.any()) continue;
+    float d[V];
+    unpack<DT>(p.load((const char*)a.dy + token * a.dy_stride * Ty<DT>::E), d);
+    for (uint64_t m = s.mask; m;) {
+      const int j = take(m);
+      const float w = lane_value(s.weight, j);
+      char* row = (char*)a.drows + (int64_t)lane_value(s.place, j) * a.drows_stride * Ty<DT>::E;
+      asm volatile("" : "+s"(row));
+      float f[V];
+#pragma unroll
+      for (int t = 0; t < V; t++) f[t] = w * d[t];
+      p.template store<false>(row, f);
+    }
+  }
+}
+
 // ---- launches ---------------------------------------------------------------------------
 unsigned grid_of(int64_t units, int per) {
   return (unsigned)std::min<int64_t>((units + per - 1) / per, (int64_t)1 << 22);
@@ -542,6 +569,19 @@ hipError_t combine_grad(const CombineGradArgs& a, hipStream_t s) {
   const uintptr_t starts = (uintptr_t)a.dy | (uintptr_t)a.rows | (uintptr_t)(a.dy_stride * Ty<DT>::E) |
                            (uintptr_t)(a.rows_stride * Ty<DT>::E);
   const bool stream = starts % 64 == 0;
+  // Where the rows are more than the caches hold, memory that reads and then writes
+  // is faster than memory that does both at once, by more than dy's second reading
+  // costs (16,384 tokens of 8 KiB, 8 slots: 406 us, 452 in one launch; 4,096
+  // tokens 110, 123; 2,048 tokens 59.5, 55.8; 16,384 tokens, 2 slots 139, 135).
+  if (a.drows && a.dweights && a.topk >= 4 && nv > 64 && a.tokens * a.topk * a.cols * Ty<DT>::E > (int64_t)192 << 20) {
+    CombineGradArgs b = a;
+    b.drows = nullptr;
+    const hipError_t e = stream ? launch<k_combine_grad<DT, 1, kEnd, true>>(dim3(grid_of(a.tokens, 4)), dim3(256), s, b)
+                                : launch<k_combine_grad<DT, 1, kEnd, false>>(dim3(grid_of(a.tokens, 4)), dim3(256), s, b);
+    if (e != hipSuccess) return e;
+    const int parts = (int)((nv + 63) / 64);
+    return launch<k_combine_grad_rows<DT>>(dim3(grid_of(a.tokens * parts, 4)), dim3(256), s, a, parts);
+  }
   if (nv <= 64 || a.tokens >= 16 * library_cus()) {
     const dim3 grid(grid_of(a.tokens, 4));
     return stream ? launch<k_combine_grad<DT, 1, kEnd, true>>(grid, dim3(256), s, a)

@@ -40,9 +40,10 @@ struct RowPart {
       return ld_row_lane<DT, STREAM>(row, 0, at());
     }
   }
+  template <bool STREAM = true>
   __device__ __forceinline__ void store(void* row, const float (&x)[V]) const {
     if (K == kInside || (K == kEnd && t.skip == 0)) {
-      st_row_lane<DT, true>(row, 0, at(), pack_rounded<DT>(x));
+      st_row_lane<DT, STREAM>(row, 0, at(), pack_rounded<DT>(x));
     } else {
 #pragma unroll
       for (int i = 0; i < V; i++)

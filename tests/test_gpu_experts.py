@@ -181,6 +181,34 @@ def test_combine_grad_sizes(lib, t, k, c, dtype):
         assert torch.equal(alone, out[0]) and torch.equal(dw, out[1])
 
 
+@pytest.mark.parametrize("t,k,c,dtype", [(6500, 8, 2051, torch.bfloat16), (13000, 4, 1025, torch.float32), (3400, 32, 1030, torch.float16)])
+def test_combine_grad_of_more_rows_than_the_caches_hold(lib, t, k, c, dtype):
+    """There the weights' gradient and the rows' are found one after the other."""
+    g = torch.Generator("cuda").manual_seed(t)
+    chosen = torch.randint(-1, 40, (t, k), device="cuda", generator=g, dtype=torch.int32)
+    _, place, offsets, _ = lib.dispatch(torch.empty(t, 1, device="cuda"), chosen, 40)
+    n = int(offsets[40])
+    rows = torch.randn(t * k, c, device="cuda", generator=g).to(dtype)
+    dy = torch.randn(t, c, device="cuda", generator=g).to(dtype)
+    w = torch.rand(t, k, device="cuda", generator=g)
+    out = (torch.full((t * k, c), 7.0, dtype=dtype, device="cuda"), torch.empty(t, k, device="cuda"))
+    lib.combine_grad(dy, rows, place, w, out=out)
+    full = place.reshape(-1) >= 0
+    at, token = place.reshape(-1)[full].long(), torch.arange(t * k, device="cuda")[full] // k
+    want = torch.full_like(out[0], 7.0)
+    want[at] = (w.reshape(-1)[full][:, None] * dy[token].float()).to(dtype)  # one product, rounded once more
+    assert torch.equal(out[0], want)
+    for a in range(0, n, 8000):
+        i, d = at[a:a + 8000], dy[token[a:a + 8000]].double()
+        terms = d * rows[i].double()
+        oracle.assert_within(out[1].reshape(-1)[full][a:a + 8000].cpu(), terms.sum(1).cpu(),
+                             (40 + c / 256) * oracle.U * terms.abs().sum(1).cpu() + 1e-37, "dweights")
+    assert not out[1].reshape(-1)[~full].any()
+    dw = torch.empty_like(out[1])
+    lib.combine_grad(dy, rows, place, w, out=(rows, dw))
+    assert torch.equal(rows[:n], out[0][:n]) and torch.equal(dw, out[1])
+
+
 def test_places_outside_the_rows_are_empty_slots(lib):
     rows = torch.randn(6, 70)
     place = torch.tensor([[0, 6, -1], [2 ** 31 - 1, -2 ** 31, 5], [7, 100, -7]], dtype=torch.int32)
