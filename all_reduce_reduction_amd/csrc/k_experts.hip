@@ -89,32 +89,28 @@ __device__ __forceinline__ void copy_row(const char* from, int64_t bytes, char* 
     } else if (l < bytes) {
       v[0] = (uint8_t)from[b];
     }
-    for (int j = lane >> 4; mask >> (j & ~3); j += 4) {
-      const int32_t at = __shfl(place, j);
-      if (at < 0) continue;
-      if (!whole) {
-        if (l < bytes) to[at * pitch + b] = (char)v[0];
-      } else if (l * 16 < bytes) {
-        st_any<STREAM>(to, at * pitch + b, v);
-      }
+    for (int j0 = 0; mask >> j0; j0 += 4) {
+      const int32_t row = __shfl(place, j0 + (lane >> 4));
+      if (row >= 0 && whole && l * 16 < bytes) st_any<STREAM>(to, row * pitch + b, v);
+      if (row >= 0 && !whole && l < bytes) to[row * pitch + b] = (char)v[0];
     }
     return;
   }
   const int64_t b = (int64_t)part * kPartBytes + lane * 16;
-  if (b >= bytes) return;
-  // (the last 16 bytes end with the row)
+  // (the last 16 bytes end with the row; lanes past it keep running, as the others
+  // read their places)
   const int64_t at = b + 16 <= bytes ? b : bytes - 16;
   const u32x4 v = ld_any(from, at);
   while (mask) {
     char* row = to + (int64_t)lane_value(place, take(mask)) * pitch;
     asm volatile("" : "+s"(row));
-    st_any<STREAM>(row, at, v);
+    if (b < bytes) st_any<STREAM>(row, at, v);
   }
 }
-// parts of a token's row
+// a part of a token's row, and of its scales
 template <bool STREAM>
 __device__ __forceinline__ void move_token(const DispatchArgs& a, int64_t token, int32_t place, int part) {
-  if (a.row_bytes)
+  if ((int64_t)part * kPartBytes < a.row_bytes)
     copy_row<STREAM>((const char*)a.x + token * a.x_pitch, a.row_bytes, (char*)a.rows, a.rows_pitch, place, part);
   if (a.scales && (int64_t)part * kPartBytes < a.scale_bytes)
     copy_row<STREAM>((const char*)a.scales + token * a.scale_bytes, a.scale_bytes, (char*)a.row_scales, a.scale_bytes, place, part);
@@ -533,7 +529,6 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(6, 6))
     const int64_t token = unit / parts;
     const TokenSlots s(a.place, a.weights, token, a.topk, a.nrows);
     const RowPart<DT, kEnd> p(((uint32_t)(unit - token * parts) * 64 + lane) * V, (uint32_t)a.cols);
-    if (!p.any()) continue;
     float d[V];
     unpack<DT>(p.load((const char*)a.dy + token * a.dy_stride * Ty<DT>::E), d);
     for (uint64_t m = s.mask; m;) {
@@ -544,7 +539,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(6, 6))
       float f[V];
 #pragma unroll
       for (int t = 0; t < V; t++) f[t] = w * d[t];
-      p.template store<false>(row, f);
+      if (p.any()) p.template store<false>(row, f);
     }
   }
 }

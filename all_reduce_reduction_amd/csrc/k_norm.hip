@@ -205,7 +205,7 @@ hipError_t pick(const NormArgs& a, hipStream_t s) {
   if (nv <= 64) return go<DT, 64, 1>(a, 64, s);
   if (nv <= 128) return go<DT, 64, 2>(a, 64, s);
   // Two vectors per thread leave room for another row's workgroup on the same
-  // compute unit (16,384 x 8,192 bf16 156 us, 219 with one; a few rows by
+  // compute unit (16,384 x 8,192 bf16 157 us, 219 with one; a few rows by
   // themselves take the same with either, 1 x 8,192 3.7 us).
   if (nv <= 2048) return go<DT, 0, 2>(a, row_threads(nv, 2), s);
   if (nv <= 4096) return go<DT, 0, 4>(a, row_threads(nv, 4), s);

@@ -633,9 +633,10 @@ int sim_combine(const void* rows, int64_t rows_stride, int dtype, int64_t nrows,
  *   drows[place[t][j]] = weights[t][j] * dy[t]               (NULL: not wanted)
  *   dweights[t][j]     = the sum over the columns of dy[t] * rows[place[t][j]]
  *                        (NULL: not wanted; 0 for an empty slot)
- * No two slots may have the same place (sim_dispatch's are different; of equal
- * ones, drows gets one slot's row).  Rows that no place names are left as they
- * were.  drows may lie exactly on rows. */
+ * No two slots may have the same place (sim_dispatch's are different; of slots
+ * with equal ones that row of drows, and in place their dweights too, hold
+ * anything).  Rows that no place names are left as they were.  drows may lie
+ * exactly on rows. */
 int sim_combine_grad(const void* dy, int64_t dy_stride, int dtype, const void* rows, int64_t rows_stride,
                      int64_t nrows, int64_t columns, const int32_t* place, const float* weights, int64_t tokens,
                      int topk, void* drows, int64_t drows_stride, float* dweights, void* stream);

@@ -144,6 +144,19 @@ def test_parts_of_several_ranks(lib, p):
     assert abs(norm.item() - 5.0) < 1e-6 and all(torch.allclose(t, torch.full_like(t, 0.2)) for t in many)
 
 
+def test_parts_of_many_ranks_and_of_one(lib):
+    parts = torch.rand(1000, generator=torch.Generator().manual_seed(1))
+    want = (parts.double() ** 2).sum().sqrt()
+    g = torch.ones(5, device="cuda")
+    norm = lib.clip_grads([g], 1.0, parts=parts.cuda())
+    oracle.assert_within(norm.reshape(()), want, 8 * oracle.U * want, "norm")
+    oracle.assert_within(g, torch.full((5,), 1.0).double() / want, 12 * oracle.U / want, "gradient")
+    for n in (3, 0):  # one rank's norm is all of it, whatever it is
+        g = [torch.ones(5, device="cuda") for _ in range(n)]
+        assert lib.clip_grads(g, 1.0, parts=torch.tensor([4.0], device="cuda")).item() == 4.0
+        assert all((t == 0.25).all() for t in g)
+
+
 def test_the_same_bits_every_time(lib):
     grads = [g.cuda() for g in make([500001, 77, 40000], DTYPES, 20)]
     a, b = ([torch.empty_like(g) for g in grads] for _ in range(2))

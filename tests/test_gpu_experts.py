@@ -78,6 +78,33 @@ def test_dispatch_row_lengths(lib, t, c):
     check_dispatch(lib, x.view(oracle.E4M3), choose(t, 8, 40, c), 40, scales=torch.rand(t, -(-c // 128)))
 
 
+@pytest.mark.parametrize("t", [37, 700])
+@pytest.mark.parametrize("c,groups", [(8, 300), (700, 900), (3000, 1), (1, 65), (2049, 2049)])
+def test_scales_of_any_length_beside_rows_of_any_length(lib, t, c, groups):
+    x = torch.randint(0, 256, (t, c), generator=torch.Generator().manual_seed(c), dtype=torch.uint8)
+    check_dispatch(lib, x, choose(t, 8, 40, groups), 40, scales=torch.rand(t, groups))
+
+
+@pytest.mark.parametrize("t", [37, 700])
+def test_the_places_alone(lib, t):
+    chosen = choose(t, 8, 40, t)
+    rows, place, offsets, _ = lib.dispatch(torch.empty(t, 0, device="cuda"), chosen.cuda(), 40)
+    want = oracle.places(chosen, 40)
+    assert rows.shape == (t * 8, 0) and torch.equal(place.cpu(), want[0]) and torch.equal(offsets.cpu(), want[1])
+
+
+def test_no_slot_has_an_expert(lib):
+    t, k = 30, 3
+    place = torch.full((t, k), -1, dtype=torch.int32, device="cuda")
+    w = torch.full((t, k), NAN, device="cuda")
+    for c in (5, 64, 2000):
+        rows = torch.full((t * k, c), NAN, device="cuda")
+        assert not lib.combine(rows, place, w).any()
+        keep = torch.full_like(rows, 7.0)
+        _, dw = lib.combine_grad(torch.ones(t, c, device="cuda"), rows, place, w, out=(keep, torch.empty(t, k, device="cuda")))
+        assert (keep == 7).all() and not dw.any()
+
+
 @pytest.mark.parametrize("t", [100, 3000])
 def test_all_to_one_expert_none_and_the_last(lib, t):
     x = torch.randn(t, 24)
