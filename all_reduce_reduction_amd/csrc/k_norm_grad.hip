@@ -126,9 +126,7 @@ __global__ void __launch_bounds__(1024) k_norm_grad(NormGradArgs a) {
   // (one workgroup's share is the whole sum)
   float* to = a.workgroups > 1 ? a.partial + (int64_t)blockIdx.x * a.cols : a.dgain;
   vectors([&](auto i, auto p) __attribute__((always_inline)) {
-#pragma unroll
-    for (int t = 0; t < V; t++)
-      if (p.any() && p.own(t)) to[p.at() + t] = acc[i][t];
+    if (p.any()) p.store_floats(to, acc[i]);
   });
 }
 

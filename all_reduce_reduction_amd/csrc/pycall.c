@@ -288,6 +288,25 @@ static int pair_of(PyObject* v, long long* a, long long* b) {
   return two && !PyErr_Occurred();
 }
 
+/* the elements from row to row of a tensor with contiguous rows; 0: it has none,
+ * or an error.  (A tensor's strides cost more than whether it is contiguous.) */
+static int row_step(PyObject* t, long long rows, long long cols, long long* ld) {
+  PyObject* v = PyObject_CallMethodNoArgs(t, s_contiguous);
+  if (!v) return 0;
+  const int whole = PyObject_IsTrue(v);
+  Py_DECREF(v);
+  if (whole < 0) return 0;
+  *ld = cols;
+  if (whole) return 1;
+  long long step = 0;
+  if (!(v = PyObject_CallMethodNoArgs(t, s_stride))) return 0;
+  const int ok = pair_of(v, ld, &step);
+  Py_DECREF(v);
+  if (!ok || PyErr_Occurred() || (step != 1 && cols > 1)) return 0;
+  if (rows <= 1) *ld = cols;
+  return 1;
+}
+
 /* rows(tensor, what, like): (pointer, row stride, rows, columns, type code,
  * device index) of a 2-D device tensor with contiguous rows; like: None, or
  * the tuple of a tensor whose shape, type and device it must have. */
@@ -309,7 +328,7 @@ static PyObject* py_like(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return a[0] == Py_None ? Py_BuildValue("(OO)", Py_None, PyTuple_GET_ITEM(a[2], 3)) : rows_of(a, 1);
 }
 static PyObject* rows_of(PyObject* const* a, int brief) {
-  long long rows = 0, cols = 0, ld = 0, step = 0;
+  long long rows = 0, cols = 0, ld = 0;
   PyObject* v = PyObject_GetAttr(a[0], s_shape);
   if (!v) return NULL;
   int ok = pair_of(v, &rows, &cols);
@@ -317,12 +336,10 @@ static PyObject* rows_of(PyObject* const* a, int brief) {
   const long dev = ok ? number(a[0], s_device) : -1;
   if (PyErr_Occurred()) return NULL;
   if (dev < 0) return PyErr_Format(PyExc_ValueError, "%S must be a 2-D device tensor", a[1]);
-  if (!(v = PyObject_CallMethodNoArgs(a[0], s_stride))) return NULL;
-  ok = pair_of(v, &ld, &step);
-  Py_DECREF(v);
-  if (PyErr_Occurred()) return NULL;
-  if (!ok || (step != 1 && cols > 1)) return PyErr_Format(PyExc_ValueError, "%S's rows must be contiguous", a[1]);
-  if (rows <= 1) ld = cols;
+  if (!row_step(a[0], rows, cols, &ld)) {
+    if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "%S's rows must be contiguous", a[1]);
+    return NULL;
+  }
   const int code = code_of(a[0]);
   if (code < 0) return NULL;
   if (code == 0) {
@@ -473,7 +490,7 @@ static PyObject* py_raw(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     PyErr_SetString(PyExc_TypeError, "raw(tensor, what, dtype)");
     return NULL;
   }
-  long long rows = 0, cols = 0, ld = 0, step = 0;
+  long long rows = 0, cols = 0, ld = 0;
   PyObject* v = PyObject_GetAttr(a[0], s_shape);
   if (!v) return NULL;
   int ok = pair_of(v, &rows, &cols);
@@ -481,12 +498,10 @@ static PyObject* py_raw(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   const long dev = ok ? number(a[0], s_device) : -1;
   if (PyErr_Occurred()) return NULL;
   if (dev < 0) return PyErr_Format(PyExc_ValueError, "%S must be a 2-D device tensor", a[1]);
-  if (!(v = PyObject_CallMethodNoArgs(a[0], s_stride))) return NULL;
-  ok = pair_of(v, &ld, &step);
-  Py_DECREF(v);
-  if (PyErr_Occurred()) return NULL;
-  if (!ok || (step != 1 && cols > 1)) return PyErr_Format(PyExc_ValueError, "%S's rows must be contiguous", a[1]);
-  if (rows <= 1) ld = cols;
+  if (!row_step(a[0], rows, cols, &ld)) {
+    if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "%S's rows must be contiguous", a[1]);
+    return NULL;
+  }
   if (a[2] != Py_None) {
     if (!(v = PyObject_GetAttr(a[0], s_dtype))) return NULL;
     ok = v == a[2];

@@ -50,6 +50,20 @@ struct RowPart {
         if (own(i)) store_elem<DT>(row, (int64_t)at() + i, x[i]);
     }
   }
+  // this thread's elements of a row of floats
+  __device__ __forceinline__ void store_floats(float* row, const float (&x)[V]) const {
+    if (K == kInside || (K == kEnd && t.skip == 0)) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const float f[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
+        st_row<SIM_FP32>(row, (int64_t)at() + i, pack<SIM_FP32>(f));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i++)
+        if (own(i)) row[at() + i] = x[i];
+    }
+  }
   // others' elements as zeros
   __device__ __forceinline__ void mask(float (&x)[V]) const {
 #pragma unroll
