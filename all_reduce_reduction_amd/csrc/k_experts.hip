@@ -15,7 +15,7 @@
 // costs a load.
 //
 // Bound by memory, and by how it takes rows in no order: 16,384 tokens and 8 slots,
-// combine of 8 KiB rows 203 us (1,209 MB at 5.9 TB/s; a copy of as many bytes 182),
+// combine of 8 KiB rows 198 us (1,209 MB at 6.1 TB/s; a copy of as many bytes 182),
 // its gradient 406 (weights 185, rows 221; 2,283 MB, 343), dispatch of 4 KiB rows 127
 // (places 12, rows 115; 624 MB, 94).  Writes alone that fill memory from its start
 // reach 6.7 TB/s when every wave writes once, 5.5 when it writes eight times, 4.5 to
@@ -355,12 +355,13 @@ __device__ __forceinline__ void add_rows(const CombineArgs& a, const TokenSlots&
     for (int t = 0; t < V; t++) acc[t] = __builtin_fmaf(w[i], f[t], acc[t]);
   }
 }
-// A wave takes part of a token's columns, 64 vectors.  MANY slots: with eight
-// loads of a wave under way four waves per SIMD are enough, and more would only
-// interleave more rows in memory (16,384 tokens of 8 KiB, 8 slots 203 us, 214 with
-// eight waves; 2 slots 73 us, 65 with eight).
-template <int DT, bool MANY>
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, MANY ? 4 : 8))) k_combine(CombineArgs a, int parts) {
+// A wave takes part of a token's columns, 64 vectors.  With many loads of a wave
+// under way WAVES per SIMD are enough, and more would only interleave more rows in
+// memory (16,384 tokens of 8 KiB, 8 slots: three 198 us, four 204, eight 214; 4,096
+// of 16 KiB, 6 slots: three 74 us, four 70.5, eight 73; 16,384 of 8 KiB, 2 slots:
+// four 73 us, eight 65).
+template <int DT, int WAVES>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES < 8 ? WAVES : 4, WAVES))) k_combine(CombineArgs a, int parts) {
   constexpr int V = epv<DT>();
   const int lane = threadIdx.x & 63;
   const int64_t step = (int64_t)gridDim.x * 4;
@@ -558,8 +559,9 @@ hipError_t combine(const CombineArgs& a, hipStream_t s) {
   if (nv <= 32) return launch<k_combine_short<DT, 32, false>>(dim3(grid_of(a.tokens, 8)), dim3(256), s, a);
   const int parts = (int)((nv + 63) / 64);
   const dim3 grid(grid_of(a.tokens * parts, 4));
-  return a.topk > 4 ? launch<k_combine<DT, true>>(grid, dim3(256), s, a, parts)
-                    : launch<k_combine<DT, false>>(grid, dim3(256), s, a, parts);
+  if (a.topk >= 8) return launch<k_combine<DT, 3>>(grid, dim3(256), s, a, parts);
+  if (a.topk > 4) return launch<k_combine<DT, 4>>(grid, dim3(256), s, a, parts);
+  return launch<k_combine<DT, 8>>(grid, dim3(256), s, a, parts);
 }
 template <int DT>
 hipError_t combine_grad(const CombineGradArgs& a, hipStream_t s) {

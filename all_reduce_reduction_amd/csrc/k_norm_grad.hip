@@ -7,7 +7,7 @@
 // dgain in registers from the first row to the last; the workgroups' shares are
 // added up by a second launch, in the workgroups' order.
 //
-// Bound by memory that reads and writes at once: 186 us for 16,384 rows x 8,192
+// Bound by memory that reads and writes at once: 184 us for 16,384 rows x 8,192
 // bf16 with dsum (1,074 MB; a copy of as many bytes 161), of which the second launch
 // and its gap are 6; 1,003 rows x 2,261 fp32 12 us, where a workgroup's two rows
 // follow each other.
