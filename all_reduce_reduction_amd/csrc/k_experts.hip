@@ -568,25 +568,25 @@ hipError_t combine_grad(const CombineGradArgs& a, hipStream_t s) {
   constexpr int V = epv<DT>();
   const int64_t nv = (a.cols + V - 1) / V;
   if (a.cols < V) return launch<k_combine_grad<DT, 1, kTiny, false>>(dim3(grid_of(a.tokens, 4)), dim3(256), s, a);
+  // Where the rows are more than the caches hold, memory that reads and then writes
+  // is faster than memory that does both at once, by more than dy's second reading
+  // costs (16,384 tokens of 8 KiB, 8 slots: 406 us, 452 in one launch; 4,096
+  // tokens 110, 123; 2,048 tokens 59.5, 55.8; 16,384 tokens, 2 slots 139, 135).
+  if (a.drows && a.dweights && a.topk >= 4 && nv > 64 &&
+      (double)a.tokens * a.topk * (double)a.cols * Ty<DT>::E > (double)(192 << 20)) {
+    CombineGradArgs b = a;
+    b.drows = nullptr;
+    const hipError_t e = combine_grad<DT>(b, s);
+    if (e != hipSuccess) return e;
+    const int parts = (int)((nv + 63) / 64);
+    return launch<k_combine_grad_rows<DT>>(dim3(grid_of(a.tokens * parts, 4)), dim3(256), s, a, parts);
+  }
   // Rows that start inside a line share it: streaming loads would fetch it twice
   // (333 tokens x 2,263 fp32, 6 slots 9.9 us, 13.0 streaming; 4,096 x 5,120 bf16,
   // 4 slots 78, 74 streaming).
   const uintptr_t starts = (uintptr_t)a.dy | (uintptr_t)a.rows | (uintptr_t)(a.dy_stride * Ty<DT>::E) |
                            (uintptr_t)(a.rows_stride * Ty<DT>::E);
   const bool stream = starts % 64 == 0;
-  // Where the rows are more than the caches hold, memory that reads and then writes
-  // is faster than memory that does both at once, by more than dy's second reading
-  // costs (16,384 tokens of 8 KiB, 8 slots: 406 us, 452 in one launch; 4,096
-  // tokens 110, 123; 2,048 tokens 59.5, 55.8; 16,384 tokens, 2 slots 139, 135).
-  if (a.drows && a.dweights && a.topk >= 4 && nv > 64 && a.tokens * a.topk * a.cols * Ty<DT>::E > (int64_t)192 << 20) {
-    CombineGradArgs b = a;
-    b.drows = nullptr;
-    const hipError_t e = stream ? launch<k_combine_grad<DT, 1, kEnd, true>>(dim3(grid_of(a.tokens, 4)), dim3(256), s, b)
-                                : launch<k_combine_grad<DT, 1, kEnd, false>>(dim3(grid_of(a.tokens, 4)), dim3(256), s, b);
-    if (e != hipSuccess) return e;
-    const int parts = (int)((nv + 63) / 64);
-    return launch<k_combine_grad_rows<DT>>(dim3(grid_of(a.tokens * parts, 4)), dim3(256), s, a, parts);
-  }
   if (nv <= 64 || a.tokens >= 16 * library_cus()) {
     const dim3 grid(grid_of(a.tokens, 4));
     return stream ? launch<k_combine_grad<DT, 1, kEnd, true>>(grid, dim3(256), s, a)
