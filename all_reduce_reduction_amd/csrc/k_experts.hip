@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(256) k_dispatch_few(DispatchArgs a, int groups
   move_token<true>(a, token, place, part);
 }
 
-// ---- many slots: counts, places, rows -----------------------------------------------
+// ---- more slots: counts, places, rows -----------------------------------------------
 __global__ void __launch_bounds__(256) k_dispatch_count(DispatchArgs a) {
   constexpr int N = 4;
   __shared__ uint32_t count_s[SIM_ROUTE_MAX_EXPERTS];
@@ -217,51 +217,73 @@ __global__ void __launch_bounds__(256) k_dispatch_count(DispatchArgs a) {
   for (int e = threadIdx.x; e < a.experts; e += 256) a.counts[(int64_t)blockIdx.x * a.experts + e] = count_s[e];
 }
 
-// A chunk's places.  The experts' starts and the counts of the chunks before
-// come from all chunks' counts; within the chunk each wave takes a run of slots,
-// 64 at a time, and a slot's place is its wave's next one of its expert plus the
-// number of lanes below it with the same expert.
+// A chunk's places.  The experts' starts and the slots before the chunk come from
+// all chunks' counts, or with SELF from all slots themselves; within the chunk each
+// wave takes a run of slots, 64 at a time, and a slot's place is its wave's next one
+// of its expert plus the number of lanes below it with the same expert.
 constexpr int kPlaceThreads = 1024, kPlaceWaves = kPlaceThreads / 64;
+template <bool SELF>
 __global__ void __launch_bounds__(kPlaceThreads) k_dispatch_place(DispatchArgs a) {
-  constexpr int N = 8;
+  constexpr int N = 16;  // loads of a thread under way
   __shared__ uint32_t next_s[kPlaceWaves * SIM_ROUTE_MAX_EXPERTS];
   __shared__ uint32_t total_s[SIM_ROUTE_MAX_EXPERTS], before_s[SIM_ROUTE_MAX_EXPERTS];
   __shared__ uint32_t wave_s[kPlaceWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_uniform(tid >> 6);
   const int experts = a.experts, mine = (int)blockIdx.x;
+  const int64_t slots = a.tokens * a.topk, run = a.chunk / kPlaceWaves;
+  const int64_t lo = mine * a.chunk + wave * run;
+  const int64_t hi = lo + run < slots ? lo + run : slots;
+  // the wave's first 64 slots, asked for first
+  const uint32_t first_e = lo + lane < hi ? expert_of(a, lo + lane) : (uint32_t)experts;
   uint32_t* next = next_s + wave * experts;
   for (int e = tid; e < experts; e += kPlaceThreads) total_s[e] = before_s[e] = 0;
   for (int e = lane; e < experts; e += 64) next[e] = 0;
   __syncthreads();
-  // this chunk's slots, counted per wave
-  const int64_t slots = a.tokens * a.topk, run = a.chunk / kPlaceWaves;
-  const int64_t lo = mine * a.chunk + wave * run;
-  const int64_t hi = lo + run < slots ? lo + run : slots;
-  for (int64_t i = lo + lane; i < hi; i += 64) {
-    const uint32_t e = expert_of(a, i);
-    if (e < (uint32_t)experts) atomicAdd(&next[e], 1u);
-  }
-  // as many chunks at once as there are threads for their experts
-  const int at_once = kPlaceThreads / experts;
-  const int from = tid / experts;
-  if (from < at_once) {
-    const int e = tid - from * experts;
-    uint32_t total = 0, before = 0;
-    for (int c0 = from; c0 < a.chunks; c0 += at_once * N) {
-      uint32_t n[N];
+  if constexpr (SELF) {
+    const int start = (int)(mine * a.chunk);
+    for (int i0 = tid; i0 < slots; i0 += kPlaceThreads * N) {
+      int32_t c[N];
 #pragma unroll
       for (int i = 0; i < N; i++) {
-        n[i] = 0;
-        if (c0 + i * at_once < a.chunks) n[i] = a.counts[(int64_t)(c0 + i * at_once) * experts + e];
+        c[i] = -1;
+        if (i0 + i * kPlaceThreads < slots) c[i] = a.chosen[i0 + i * kPlaceThreads];
       }
 #pragma unroll
       for (int i = 0; i < N; i++) {
-        total += n[i];
-        before += c0 + i * at_once < mine ? n[i] : 0;
+        if ((uint32_t)c[i] >= (uint32_t)experts) continue;
+        atomicAdd(&total_s[c[i]], 1u);
+        if (i0 + i * kPlaceThreads < start) atomicAdd(&before_s[c[i]], 1u);
       }
     }
-    atomicAdd(&total_s[e], total);
-    atomicAdd(&before_s[e], before);
+  } else {
+    // as many chunks at once as there are threads for their experts
+    const int at_once = kPlaceThreads / experts;
+    const int from = tid / experts;
+    if (from < at_once) {
+      const int e = tid - from * experts;
+      uint32_t total = 0, before = 0;
+      for (int c0 = from; c0 < a.chunks; c0 += at_once * N) {
+        uint32_t n[N];
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+          n[i] = 0;
+          if (c0 + i * at_once < a.chunks) n[i] = a.counts[(int64_t)(c0 + i * at_once) * experts + e];
+        }
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+          total += n[i];
+          before += c0 + i * at_once < mine ? n[i] : 0;
+        }
+      }
+      atomicAdd(&total_s[e], total);
+      atomicAdd(&before_s[e], before);
+    }
+  }
+  // this chunk's slots, counted per wave
+  if (first_e < (uint32_t)experts) atomicAdd(&next[first_e], 1u);
+  for (int64_t i = lo + 64 + lane; i < hi; i += 64) {
+    const uint32_t e = expert_of(a, i);
+    if (e < (uint32_t)experts) atomicAdd(&next[e], 1u);
   }
   __syncthreads();
   // the experts' starts: a scan of the totals, one expert per thread
@@ -286,7 +308,7 @@ __global__ void __launch_bounds__(kPlaceThreads) k_dispatch_place(DispatchArgs a
   __syncthreads();
   for (int64_t i0 = lo; i0 < hi; i0 += 64) {
     const int64_t i = i0 + lane;
-    const uint32_t e = i < hi ? expert_of(a, i) : (uint32_t)experts;
+    const uint32_t e = i0 == lo ? first_e : i < hi ? expert_of(a, i) : (uint32_t)experts;
     // the lanes with the same expert
     uint64_t same = ~0ull;
     for (int b = 0; (experts >> b) != 0; b++) {
@@ -607,9 +629,14 @@ hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
     const int groups = (parts + 3) / 4;
     return launch<k_dispatch_few>(dim3((unsigned)(a.tokens * groups + 1)), dim3(256), s, a, groups);
   }
-  hipError_t e = launch<k_dispatch_count>(dim3(a.chunks), dim3(256), s, a);
-  if (e != hipSuccess) return e;
-  e = launch<k_dispatch_place>(dim3(a.chunks), dim3(kPlaceThreads), s, a);
+  hipError_t e;
+  if (a.counts) {
+    e = launch<k_dispatch_count>(dim3(a.chunks), dim3(256), s, a);
+    if (e != hipSuccess) return e;
+    e = launch<k_dispatch_place<false>>(dim3(a.chunks), dim3(kPlaceThreads), s, a);
+  } else {
+    e = launch<k_dispatch_place<true>>(dim3(a.chunks), dim3(kPlaceThreads), s, a);
+  }
   if (e != hipSuccess || (a.row_bytes == 0 && !a.scales)) return e;
   // Streaming stores, but not where what is written is far more than the caches
   // hold: 16,384 tokens of 4 KiB to 8 places 130 us, 134 streaming; 1,000 of 4 KiB

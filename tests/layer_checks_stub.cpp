@@ -23,7 +23,8 @@ hipError_t launch_norm_grad(const NormGradArgs& a, int, hipStream_t) {
 }
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t) {
   return made(a.chunks == 0 ? a.tokens * a.topk <= 4096
-                            : a.counts && a.chunk % 1024 == 0 && a.chunks * a.chunk >= a.tokens * a.topk);
+                            : (a.counts || !dispatch_counts(a.tokens * a.topk, a.experts)) && a.chunk % 1024 == 0 &&
+                                  a.chunks * a.chunk >= a.tokens * a.topk);
 }
 hipError_t launch_combine(const CombineArgs& a, int, hipStream_t) { return made(a.rows || a.nrows == 0); }
 hipError_t launch_combine_grad(const CombineGradArgs& a, int, hipStream_t) { return made(a.drows || a.dweights); }

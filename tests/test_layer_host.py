@@ -98,16 +98,16 @@ def test_norm_grad_checks(checks):
 def test_dispatch_checks(checks):
     need = ctypes.c_size_t()
     assert checks.sim_dispatch_work(512, 8, 256, ctypes.byref(need)) == 0 and need.value == 0
-    assert checks.sim_dispatch_work(513, 8, 256, ctypes.byref(need)) == 0 and need.value > 0 and need.value % (256 * 4) == 0
+    assert checks.sim_dispatch_work(20000, 8, 256, ctypes.byref(need)) == 0 and need.value > 0 and need.value % (256 * 4) == 0
     for bad in ((-1, 8, 8), (1, 0, 8), (1, 33, 64), (1, 1, 0), (1, 1, 1025), (2 ** 28, 8, 8)):
         assert checks.sim_dispatch_work(*bad, ctypes.byref(need)) == INVALID
-    assert checks.sim_dispatch_work(2000, 4, 16, ctypes.byref(need)) == 0
+    assert checks.sim_dispatch_work(40000, 4, 16, ctypes.byref(need)) == 0
     many = need.value
     good = dict(x=A, x_pitch=200, row_bytes=200, scales=None, groups=0, chosen=B, tokens=10, topk=4, experts=16, rows=C,
                 rows_pitch=200, row_scales=None, place=D, offsets=E, work=None, work_bytes=0, stream=None)
     for change in ({}, dict(x=A + 1, rows=C + 3), dict(row_bytes=0, x=None, rows=None, x_pitch=0, rows_pitch=0),
                    dict(scales=F, groups=3, row_scales=F + 0x1000), dict(tokens=0, x=None, rows=None, chosen=None, place=None),
-                   dict(tokens=2000, work=F, work_bytes=many), dict(x_pitch=600, rows=A + 200, rows_pitch=600),
+                   dict(tokens=40000, work=F, work_bytes=many), dict(x_pitch=600, rows=A + 200, rows_pitch=600),
                    dict(experts=1024, topk=32)):
         run(checks, "sim_dispatch", good, change, 0)
     for change, status in ((dict(tokens=-1), INVALID), (dict(topk=0), INVALID), (dict(topk=33), INVALID), (dict(experts=0), INVALID),
@@ -115,8 +115,8 @@ def test_dispatch_checks(checks):
                            (dict(rows_pitch=199), INVALID), (dict(row_bytes=-1), INVALID), (dict(x=None), INVALID),
                            (dict(rows=None), INVALID), (dict(chosen=None), INVALID), (dict(place=None), INVALID),
                            (dict(offsets=None), INVALID), (dict(groups=3, scales=F), INVALID), (dict(groups=-1), INVALID),
-                           (dict(groups=3, row_scales=F), INVALID), (dict(tokens=2000), INVALID),
-                           (dict(tokens=2000, work=F, work_bytes=many - 1), NOMEM), (dict(chosen=B + 2), ALIGN),
+                           (dict(groups=3, row_scales=F), INVALID), (dict(tokens=40000), INVALID),
+                           (dict(tokens=40000, work=F, work_bytes=many - 1), NOMEM), (dict(chosen=B + 2), ALIGN),
                            (dict(place=D + 1), ALIGN), (dict(offsets=E + 2), ALIGN), (dict(rows=A), ALIAS), (dict(place=B), ALIAS),
                            (dict(offsets=D), ALIAS), (dict(rows=D), ALIAS), (dict(x=C + 7999), ALIAS),
                            (dict(scales=F, groups=3, row_scales=F + 8), ALIAS)):
