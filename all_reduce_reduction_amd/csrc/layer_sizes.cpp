@@ -36,11 +36,11 @@ int dispatch_chunks(int64_t slots, int64_t* chunk) {
   return (int)((slots + *chunk - 1) / *chunk);
 }
 
-// Up to 8,192 slots every chunk's workgroup counts all of them (5,120 slots of 64
-// experts: 10.7 us a call, 12.7 with a launch that counts; 8,192: 13.2, 14.2), but
-// not for so few experts that its counters are in each other's way (16,384 slots of
-// 4 experts: 21 us, 12.6).
-bool dispatch_counts(int64_t slots, int experts) { return slots > 8192 || experts < 32; }
+// Up to so many slots every chunk's workgroup counts all of them.  5,120 slots of 64
+// experts: 11.0 us a call, 12.9 with a launch that counts; 8,192 of 4: 10.2, 12.9;
+// 16,384 of 256: 10.1, 12.9, but of 4, whose counters are in each other's way, 14.8,
+// 12.9; 32,768 of 256: 13.6, 13.1.
+bool dispatch_counts(int64_t slots, int experts) { return slots > (experts >= 32 ? 16384 : 8192); }
 
 int64_t clip_pieces(int64_t count, int dtype) {
   const int64_t each = kClipPieceBytes / (dtype == SIM_FP32 ? 4 : 2);

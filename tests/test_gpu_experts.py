@@ -57,11 +57,12 @@ def check_dispatch(lib, x, chosen, e, scales=None, **more):
     return out
 
 
-# (tokens, slots, experts, columns): one token, few and many slots on both sides of 4,096 and 8,192, few and many
-# experts there, chunks that end inside
+# (tokens, slots, experts, columns): one token, few and many slots on both sides of 4,096, 8,192 and 16,384, few and
+# many experts there, chunks that end inside
 SIZES = [(1, 1, 1, 1), (1, 8, 256, 100), (5, 3, 7, 33), (64, 8, 64, 40), (511, 8, 300, 9), (512, 8, 256, 4), (513, 8, 60, 5),
          (1366, 3, 1024, 3), (4097, 1, 2, 7), (129, 32, 1000, 2), (3000, 7, 33, 3), (70, 32, 32, 300), (2500, 16, 96, 2),
-         (1024, 8, 32, 3), (1025, 8, 32, 3), (1000, 8, 31, 3), (700, 9, 1024, 2), (8000, 1, 33, 1)]
+         (1024, 8, 32, 3), (1025, 8, 32, 3), (1000, 8, 31, 3), (700, 9, 1024, 2), (8000, 1, 33, 1),
+         (2048, 8, 32, 1), (2049, 8, 32, 1), (4100, 2, 3, 1)]
 
 
 @pytest.mark.parametrize("t,k,e,c", SIZES)
@@ -107,7 +108,7 @@ def test_no_slot_has_an_expert(lib):
         assert (keep == 7).all() and not dw.any()
 
 
-@pytest.mark.parametrize("t", [100, 3000])
+@pytest.mark.parametrize("t", [100, 2000, 5000])
 def test_all_to_one_expert_none_and_the_last(lib, t):
     x = torch.randn(t, 24)
     for chosen in (torch.full((t, 4), 5), torch.full((t, 4), -1), torch.full((t, 4), 63), torch.full((t, 4), 64)):
