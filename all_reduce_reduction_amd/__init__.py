@@ -131,6 +131,12 @@ except ImportError:  # not built: prepare_allreduce falls back to a ctypes call 
     _pycall = None
 
 
+try:  # tensors' pointers, sizes and types (csrc/pytensor.cpp), built beside it
+    from . import _pytensor
+except ImportError:  # not built, or without torch: the same checks in Python
+    _pytensor = None
+
+
 def _check(status: int, what: str) -> int:
     if status != SIM_OK:
         raise SimError(status, what)
@@ -629,27 +635,29 @@ def _tensors_py(ts, what, device, like):
     for i, t in enumerate(ts):
         if t.dtype not in _TORCH_CODE or t.get_device() != device or not t.is_contiguous():
             raise ValueError(f"{what}[{i}] must be a contiguous tensor of one of the float types on cuda:{device}")
-    got = (_host_array([t.data_ptr() for t in ts], ctypes.c_void_p), _host_array([t.numel() for t in ts], ctypes.c_int64),
-           _host_array([_TORCH_CODE[t.dtype] for t in ts], ctypes.c_int))
-    if like is not None and (list(got[1]) != list(like[1]) or list(got[2]) != list(like[2])):
+    got = tuple(bytes(_host_array(v, c)) for v, c in (([t.data_ptr() for t in ts], ctypes.c_void_p),
+                                                      ([t.numel() for t in ts], ctypes.c_int64),
+                                                      ([_TORCH_CODE[t.dtype] for t in ts], ctypes.c_int)))
+    if like is not None and got[1:] != like[1:]:
         raise ValueError(f"{what} must have the gradients' sizes and types")
     return got
 
 
-if hasattr(_pycall, "clip_work") and torch is not None:
-    # arguments converted and tensors checked in C: of a small call's 7.3 us on the host, ctypes and the same checks
-    # in Python took about 3
+if hasattr(_pycall, "clip_work"):
+    # arguments converted in C: ctypes took a good half of a small call's time on the host
     for _name in _ENTRIES:
         _pycall.bind(_name, ctypes.cast(lib["sim_" + _name], ctypes.c_void_p).value)
-    _pycall.types(*_FLOATS)
-    _entry, _vec, _rows, _slots = _pycall, _pycall.pointer, _pycall.rows, _pycall.slots
-    _raw, _tensors, _like, _gain = _pycall.raw, _pycall.tensors, _pycall.like, _pycall.gain
-    _clip_bytes = _pycall.clip_work
+    _entry, _clip_bytes = _pycall, _pycall.clip_work
 else:
     import types as _types
-    _entry, _vec = _types.SimpleNamespace(**{n: getattr(lib, "sim_" + n) for n in _ENTRIES}), _vec_py
-    _rows, _slots, _raw, _tensors, _like, _gain = _rows_py, _slots_py, _raw_py, _tensors_py, _like_py, _gain_py
-    _clip_bytes = _clip_work_py
+    _entry, _clip_bytes = _types.SimpleNamespace(**{n: getattr(lib, "sim_" + n) for n in _ENTRIES}), _clip_work_py
+if _pytensor is not None:
+    # tensors looked at in C++: five attributes and methods of each took 0.25 us in Python's own calls
+    _rows, _like, _raw, _vec, _tensors = _pytensor.rows, _pytensor.like, _pytensor.raw, _pytensor.pointer, _pytensor.tensors
+    _gain, _slots = _pytensor.gain, _pytensor.slots
+else:
+    _rows, _like, _raw, _vec, _tensors = _rows_py, _like_py, _raw_py, _vec_py, _tensors_py
+    _gain, _slots = _gain_py, _slots_py
 
 
 def _on(stream, device):

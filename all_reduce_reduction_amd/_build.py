@@ -29,7 +29,9 @@ FLAGS = [
 
 
 def sources():
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".hip", ".cpp")))
+    # (pytensor.cpp is the binding's, not the library's)
+    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC)
+                  if f.endswith((".hip", ".cpp")) and f != "pytensor.cpp")
 
 
 def _compile(src: str) -> str:
@@ -82,6 +84,26 @@ def build_pycall(out_dir: str = HERE) -> str:
     return out
 
 
+def build_pytensor(out_dir: str = HERE) -> str:
+    """Compile the tensor extension (_pytensor) against this interpreter's and
+    the installed torch's headers; always rebuilds."""
+    import sysconfig
+    from torch.utils.cpp_extension import include_paths, library_paths
+    import torch
+    cxx = os.environ.get("CXX", "g++")
+    out = os.path.join(out_dir, "_pytensor" + sysconfig.get_config_var("EXT_SUFFIX"))
+    tmp = out + ".tmp"
+    cmd = [cxx, "-O2", "-shared", "-fPIC", "-std=c++17", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_paths()["include"], *(f"-isystem{p}" for p in include_paths()),
+           os.path.join(CSRC, "pytensor.cpp"), "-o", tmp, *(f"-L{p}" for p in library_paths()),
+           "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("pytensor build failed:\n" + r.stdout + r.stderr)
+    os.replace(tmp, out)
+    return out
+
+
 if __name__ == "__main__":
     import argparse
     ap = argparse.ArgumentParser()
@@ -90,3 +112,4 @@ if __name__ == "__main__":
     a = ap.parse_args()
     print(build(out=a.out, build_dir=a.build_dir))
     print(build_pycall())
+    print(build_pytensor())

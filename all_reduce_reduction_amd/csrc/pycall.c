@@ -1,5 +1,5 @@
 /* pycall.c -- the Python object behind prepare_allreduce(), and the direct
- * calls behind the routing and loss helpers (further down).
+ * calls behind the helpers that work on one rank's data (further down).
  *
  * prepare_allreduce() marshals the arguments of one sim_allreduce call
  * once; calling the object it returns makes that C call again.  Through
@@ -241,339 +241,6 @@ static PyObject* py_bind(PyObject* self, PyObject* args) {
   return NULL;
 }
 
-/* ---- tensors -------------------------------------------------------------------
- * What the helpers have to know of a tensor, through its own attributes and
- * methods.  types(...) sets the logit types once: code i + 1 is entry i. */
-#define TYPES 3
-static PyObject* logit_type[TYPES];
-static PyObject *s_dtype, *s_shape, *s_device, *s_contiguous, *s_data_ptr, *s_stride, *s_esize, *s_numel;
-
-static PyObject* py_types(PyObject* self, PyObject* args) {
-  (void)self;
-  PyObject* t[TYPES];
-  if (!PyArg_ParseTuple(args, "OOO", &t[0], &t[1], &t[2])) return NULL;
-  for (int i = 0; i < TYPES; i++) {
-    Py_INCREF(t[i]);
-    Py_XSETREF(logit_type[i], t[i]);
-  }
-  Py_RETURN_NONE;
-}
-
-/* the code of a tensor's type, 0 for any other type, -1 on an error */
-static int code_of(PyObject* t) {
-  PyObject* v = PyObject_GetAttr(t, s_dtype);
-  if (!v) return -1;
-  Py_DECREF(v);  /* types live as long as their module */
-  for (int i = 0; i < TYPES; i++)
-    if (logit_type[i] == v) return i + 1;
-  return 0;
-}
-
-/* a method's result as an integer (-1: look for an error) */
-static long number(PyObject* t, PyObject* method) {
-  PyObject* v = PyObject_CallMethodNoArgs(t, method);
-  if (!v) return -1;
-  const long n = PyLong_AsLong(v);
-  Py_DECREF(v);
-  return n;
-}
-
-/* whether a 2-tuple of integers was read */
-static int pair_of(PyObject* v, long long* a, long long* b) {
-  const int two = PyTuple_Check(v) && PyTuple_GET_SIZE(v) == 2;
-  if (two) {
-    *a = PyLong_AsLongLong(PyTuple_GET_ITEM(v, 0));
-    *b = PyLong_AsLongLong(PyTuple_GET_ITEM(v, 1));
-  }
-  return two && !PyErr_Occurred();
-}
-
-/* the elements from row to row of a tensor with contiguous rows; 0: it has none,
- * or an error.  (A tensor's strides cost more than whether it is contiguous.) */
-static int row_step(PyObject* t, long long rows, long long cols, long long* ld) {
-  PyObject* v = PyObject_CallMethodNoArgs(t, s_contiguous);
-  if (!v) return 0;
-  const int whole = PyObject_IsTrue(v);
-  Py_DECREF(v);
-  if (whole < 0) return 0;
-  *ld = cols;
-  if (whole) return 1;
-  long long step = 0;
-  if (!(v = PyObject_CallMethodNoArgs(t, s_stride))) return 0;
-  const int ok = pair_of(v, ld, &step);
-  Py_DECREF(v);
-  if (!ok || PyErr_Occurred() || (step != 1 && cols > 1)) return 0;
-  if (rows <= 1) *ld = cols;
-  return 1;
-}
-
-/* rows(tensor, what, like): (pointer, row stride, rows, columns, type code,
- * device index) of a 2-D device tensor with contiguous rows; like: None, or
- * the tuple of a tensor whose shape, type and device it must have. */
-static PyObject* rows_of(PyObject* const* a, int brief);
-static PyObject* py_rows(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  (void)self;
-  if (n == 3) return rows_of(a, 0);
-  PyErr_SetString(PyExc_TypeError, "rows(tensor, what, like)");
-  return NULL;
-}
-/* like(tensor, what, like): the first two of rows()'s; of None, None and the
- * columns */
-static PyObject* py_like(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  (void)self;
-  if (n != 3 || !PyTuple_Check(a[2]) || PyTuple_GET_SIZE(a[2]) != 6) {
-    PyErr_SetString(PyExc_TypeError, "like(tensor, what, a tuple that rows() returned)");
-    return NULL;
-  }
-  return a[0] == Py_None ? Py_BuildValue("(OO)", Py_None, PyTuple_GET_ITEM(a[2], 3)) : rows_of(a, 1);
-}
-static PyObject* rows_of(PyObject* const* a, int brief) {
-  long long rows = 0, cols = 0, ld = 0;
-  PyObject* v = PyObject_GetAttr(a[0], s_shape);
-  if (!v) return NULL;
-  int ok = pair_of(v, &rows, &cols);
-  Py_DECREF(v);
-  const long dev = ok ? number(a[0], s_device) : -1;
-  if (PyErr_Occurred()) return NULL;
-  if (dev < 0) return PyErr_Format(PyExc_ValueError, "%S must be a 2-D device tensor", a[1]);
-  if (!row_step(a[0], rows, cols, &ld)) {
-    if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "%S's rows must be contiguous", a[1]);
-    return NULL;
-  }
-  const int code = code_of(a[0]);
-  if (code < 0) return NULL;
-  if (code == 0) {
-    if ((v = PyObject_GetAttr(a[0], s_dtype))) {
-      PyErr_Format(PyExc_ValueError, "unsupported dtype %S", v);
-      Py_DECREF(v);
-    }
-    return NULL;
-  }
-  if (a[2] != Py_None) {
-    if (!PyTuple_Check(a[2]) || PyTuple_GET_SIZE(a[2]) != 6) {
-      PyErr_SetString(PyExc_TypeError, "like: a tuple that rows() returned");
-      return NULL;
-    }
-    ok = PyLong_AsLongLong(PyTuple_GET_ITEM(a[2], 2)) == rows && PyLong_AsLongLong(PyTuple_GET_ITEM(a[2], 3)) == cols &&
-         PyLong_AsLong(PyTuple_GET_ITEM(a[2], 4)) == code && PyLong_AsLong(PyTuple_GET_ITEM(a[2], 5)) == dev;
-    if (PyErr_Occurred()) return NULL;
-    if (!ok) return PyErr_Format(PyExc_ValueError, "%S must have the first tensor's shape, dtype and device", a[1]);
-  }
-  if (!(v = PyObject_CallMethodNoArgs(a[0], s_data_ptr))) return NULL;
-  return brief ? Py_BuildValue("(NL)", v, ld) : Py_BuildValue("(NLLLil)", v, ld, rows, cols, code, dev);
-}
-
-/* whether a tensor is contiguous, on that device, of that shape and one of
- * those types; -1 on an error */
-static int fits(PyObject* t, PyObject* const* types, Py_ssize_t ntypes, long dev, const long long* shape,
-                Py_ssize_t dims) {
-  int ok = 0;
-  PyObject* v = PyObject_GetAttr(t, s_dtype);
-  if (!v) return -1;
-  for (Py_ssize_t i = 0; i < ntypes; i++) ok = ok || types[i] == v;
-  Py_DECREF(v);
-  if (!ok) return 0;
-  if (!(v = PyObject_GetAttr(t, s_shape))) return -1;
-  ok = PyTuple_Check(v) && PyTuple_GET_SIZE(v) == dims;
-  for (Py_ssize_t i = 0; ok && i < dims; i++) ok = PyLong_AsLongLong(PyTuple_GET_ITEM(v, i)) == shape[i];
-  Py_DECREF(v);
-  if (PyErr_Occurred()) return -1;
-  if (!ok) return 0;
-  ok = number(t, s_device) == dev;
-  if (PyErr_Occurred()) return -1;
-  if (!ok) return 0;
-  if (!(v = PyObject_CallMethodNoArgs(t, s_contiguous))) return -1;
-  ok = PyObject_IsTrue(v);
-  Py_DECREF(v);
-  return ok;
-}
-
-/* the pointer of a tensor that fits, or an error that says what it must be */
-static PyObject* pointer_of(PyObject* t, PyObject* what, PyObject* const* types, Py_ssize_t ntypes, long dev,
-                            const long long* shape, Py_ssize_t dims) {
-  const int ok = fits(t, types, ntypes, dev, shape, dims);
-  if (ok < 0) return NULL;
-  if (ok) return PyObject_CallMethodNoArgs(t, s_data_ptr);
-  PyObject *of = PyTuple_New(ntypes), *sizes = PyTuple_New(dims);
-  for (Py_ssize_t i = 0; of && i < ntypes; i++) {
-    Py_INCREF(types[i]);
-    PyTuple_SET_ITEM(of, i, types[i]);
-  }
-  for (Py_ssize_t i = 0; sizes && i < dims; i++) {
-    PyObject* d = PyLong_FromLongLong(shape[i]);
-    if (!d) Py_CLEAR(sizes);
-    else PyTuple_SET_ITEM(sizes, i, d);
-  }
-  if (of && sizes)
-    PyErr_Format(PyExc_ValueError, "%S must be a contiguous tensor %R of one of %R on cuda:%ld", what, sizes, of, dev);
-  Py_XDECREF(of);
-  Py_XDECREF(sizes);
-  return NULL;
-}
-
-/* pointer(tensor, what, types, device index, *shape): the data pointer of a
- * contiguous tensor of that shape and device and one of those types (None
- * for None). */
-#define DIMS 4
-static PyObject* py_pointer(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  (void)self;
-  if (n < 4 || n > 4 + DIMS || !PyTuple_Check(a[2])) {
-    PyErr_SetString(PyExc_TypeError, "pointer(tensor, what, types, device, *shape)");
-    return NULL;
-  }
-  if (a[0] == Py_None) Py_RETURN_NONE;
-  long long shape[DIMS];
-  for (Py_ssize_t i = 4; i < n; i++) shape[i - 4] = PyLong_AsLongLong(a[i]);
-  const long dev = PyLong_AsLong(a[3]);
-  if (PyErr_Occurred()) return NULL;
-  return pointer_of(a[0], a[1], PySequence_Fast_ITEMS(a[2]), PyTuple_GET_SIZE(a[2]), dev, shape, n - 4);
-}
-
-/* gain(tensor, columns, device index): (pointer, type code) of a contiguous
- * tensor of that many floats; of None, None and fp32's code */
-static PyObject* s_gain;
-static PyObject* py_gain(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  (void)self;
-  if (n != 3) {
-    PyErr_SetString(PyExc_TypeError, "gain(tensor, columns, device)");
-    return NULL;
-  }
-  if (a[0] == Py_None) return Py_BuildValue("(Oi)", Py_None, 1);
-  const long long shape[1] = {PyLong_AsLongLong(a[1])};
-  const long dev = PyLong_AsLong(a[2]);
-  if (PyErr_Occurred()) return NULL;
-  PyObject* at = pointer_of(a[0], s_gain, logit_type, TYPES, dev, shape, 1);
-  const int code = at ? code_of(a[0]) : -1;
-  if (code < 0) {
-    Py_XDECREF(at);
-    return NULL;
-  }
-  return Py_BuildValue("(Ni)", at, code);
-}
-
-/* slots(ids, teacher, ids' types, rows, device index): (ids pointer, teacher
- * pointer, the teacher's type code, topk) of contiguous [rows, topk] tensors. */
-static PyObject *s_ids, *s_teacher;
-static PyObject* py_slots(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  (void)self;
-  if (n != 5 || !PyTuple_Check(a[2])) {
-    PyErr_SetString(PyExc_TypeError, "slots(ids, teacher, types, rows, device)");
-    return NULL;
-  }
-  long long had = 0, shape[2] = {PyLong_AsLongLong(a[3]), 0};
-  const long dev = PyLong_AsLong(a[4]);
-  if (PyErr_Occurred()) return NULL;
-  PyObject* v = PyObject_GetAttr(a[0], s_shape);
-  if (!v) return NULL;
-  const int ok = pair_of(v, &had, &shape[1]);
-  Py_DECREF(v);
-  if (PyErr_Occurred()) return NULL;
-  if (!ok) return PyErr_Format(PyExc_ValueError, "ids must be [rows, topk]");
-  PyObject* ids = pointer_of(a[0], s_ids, PySequence_Fast_ITEMS(a[2]), PyTuple_GET_SIZE(a[2]), dev, shape, 2);
-  if (!ids) return NULL;
-  PyObject* teacher = pointer_of(a[1], s_teacher, logit_type, TYPES, dev, shape, 2);
-  const int code = teacher ? code_of(a[1]) : -1;
-  if (code < 0) {
-    Py_DECREF(ids);
-    Py_XDECREF(teacher);
-    return NULL;
-  }
-  return Py_BuildValue("(NNiL)", ids, teacher, code, shape[1]);
-}
-
-/* raw(tensor, what, dtype): (pointer, bytes from row to row, rows, bytes of a
- * row, device index) of a 2-D device tensor of any type with contiguous rows;
- * dtype: the one it must have, or None. */
-static PyObject* py_raw(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  (void)self;
-  if (n != 3) {
-    PyErr_SetString(PyExc_TypeError, "raw(tensor, what, dtype)");
-    return NULL;
-  }
-  long long rows = 0, cols = 0, ld = 0;
-  PyObject* v = PyObject_GetAttr(a[0], s_shape);
-  if (!v) return NULL;
-  int ok = pair_of(v, &rows, &cols);
-  Py_DECREF(v);
-  const long dev = ok ? number(a[0], s_device) : -1;
-  if (PyErr_Occurred()) return NULL;
-  if (dev < 0) return PyErr_Format(PyExc_ValueError, "%S must be a 2-D device tensor", a[1]);
-  if (!row_step(a[0], rows, cols, &ld)) {
-    if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "%S's rows must be contiguous", a[1]);
-    return NULL;
-  }
-  if (a[2] != Py_None) {
-    if (!(v = PyObject_GetAttr(a[0], s_dtype))) return NULL;
-    ok = v == a[2];
-    Py_DECREF(v);
-    if (!ok) return PyErr_Format(PyExc_ValueError, "%S must be of type %S", a[1], a[2]);
-  }
-  const long e = number(a[0], s_esize);
-  if (PyErr_Occurred()) return NULL;
-  if (!(v = PyObject_CallMethodNoArgs(a[0], s_data_ptr))) return NULL;
-  return Py_BuildValue("(NLLLl)", v, ld * e, rows, cols * e, dev);
-}
-
-/* tensors(sequence, what, device, like): (pointers, counts, type codes), each an
- * array of the host in a bytes object, of contiguous tensors on that device;
- * like: None, or such a tuple whose counts and types they must have. */
-static PyObject* py_tensors(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  (void)self;
-  if (n != 4) {
-    PyErr_SetString(PyExc_TypeError, "tensors(sequence, what, device, like)");
-    return NULL;
-  }
-  const long dev = PyLong_AsLong(a[2]);
-  if (PyErr_Occurred()) return NULL;
-  PyObject* seq = PySequence_Fast(a[0], "a sequence of tensors");
-  if (!seq) return NULL;
-  const Py_ssize_t count = PySequence_Fast_GET_SIZE(seq);
-  PyObject* ptrs = PyBytes_FromStringAndSize(NULL, count * (Py_ssize_t)sizeof(void*));
-  PyObject* counts = PyBytes_FromStringAndSize(NULL, count * (Py_ssize_t)sizeof(int64_t));
-  PyObject* types = PyBytes_FromStringAndSize(NULL, count * (Py_ssize_t)sizeof(int));
-  int ok = ptrs && counts && types;
-  for (Py_ssize_t i = 0; ok && i < count && i < PySequence_Fast_GET_SIZE(seq); i++) {
-    PyObject* t = PySequence_Fast_GET_ITEM(seq, i);
-    Py_INCREF(t);
-    const int code = code_of(t);
-    const long on = code >= 0 ? number(t, s_device) : -1;
-    PyObject* v = PyErr_Occurred() ? NULL : PyObject_CallMethodNoArgs(t, s_contiguous);
-    const int whole = v ? PyObject_IsTrue(v) : 0;
-    Py_XDECREF(v);
-    if (!PyErr_Occurred() && (code == 0 || on != dev || !whole))
-      PyErr_Format(PyExc_ValueError, "%S[%zd] must be a contiguous tensor of one of the float types on cuda:%ld", a[1], i, dev);
-    v = PyErr_Occurred() ? NULL : PyObject_CallMethodNoArgs(t, s_data_ptr);
-    if (v) {
-      ((void**)PyBytes_AS_STRING(ptrs))[i] = PyLong_AsVoidPtr(v);
-      Py_DECREF(v);
-      const long elements = number(t, s_numel);
-      ((int64_t*)PyBytes_AS_STRING(counts))[i] = elements;
-      ((int*)PyBytes_AS_STRING(types))[i] = code;
-    }
-    Py_DECREF(t);
-    ok = !PyErr_Occurred();
-  }
-  if (ok && PySequence_Fast_GET_SIZE(seq) != count) {
-    PyErr_Format(PyExc_RuntimeError, "%S changed while it was read", a[1]);
-    ok = 0;
-  }
-  Py_DECREF(seq);
-  if (ok && a[3] != Py_None) {
-    const int has = PyTuple_Check(a[3]) && PyTuple_GET_SIZE(a[3]) == 3;
-    const int c = has ? PyObject_RichCompareBool(counts, PyTuple_GET_ITEM(a[3], 1), Py_EQ) : 0;
-    const int d = has && c > 0 ? PyObject_RichCompareBool(types, PyTuple_GET_ITEM(a[3], 2), Py_EQ) : 0;
-    if (!PyErr_Occurred() && d <= 0) PyErr_Format(PyExc_ValueError, "%S must have the gradients' sizes and types", a[1]);
-    ok = !PyErr_Occurred();
-  }
-  if (!ok) {
-    Py_XDECREF(ptrs);
-    Py_XDECREF(counts);
-    Py_XDECREF(types);
-    return NULL;
-  }
-  return Py_BuildValue("(NNN)", ptrs, counts, types);
-}
-
 /* clip_work(counts, type codes, number): sim_clip_work's bytes, or its status */
 static PyObject* py_clip_work(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
@@ -589,21 +256,13 @@ static PyObject* py_clip_work(PyObject* self, PyObject* const* a, Py_ssize_t n) 
 #define METHOD(name, f, doc) {name, (PyCFunction)(void (*)(void))f, METH_FASTCALL, doc}
 static PyMethodDef pycall_methods[] = {
     {"bind", py_bind, METH_VARARGS, "bind(name, address): set an entry point"},
-    {"types", py_types, METH_VARARGS, "types(fp32, fp16, bf16): set the logit types"},
-    METHOD("rows", py_rows, "rows(tensor, what, like): pointer, row stride, rows, columns, type code, device"),
-    METHOD("pointer", py_pointer, "pointer(tensor, what, types, device, *shape): the checked data pointer"),
-    METHOD("slots", py_slots, "slots(ids, teacher, types, rows, device): pointers, teacher's type code, topk"),
     METHOD("route", py_route, "sim_route"),
     METHOD("route_grad", py_route_grad, "sim_route_grad"),
     METHOD("distill_step", py_distill_step, "sim_distill_step"),
     METHOD("distill_parts", py_distill_parts, "sim_distill_parts"),
     METHOD("distill_join", py_distill_join, "sim_distill_join"),
     METHOD("distill_grad", py_distill_grad, "sim_distill_grad"),
-    METHOD("like", py_like, "like(tensor, what, like): pointer, row stride"),
-    METHOD("gain", py_gain, "gain(tensor, columns, device): pointer, type code"),
     METHOD("clip_work", py_clip_work, "clip_work(counts, types, number): sim_clip_work's bytes, or its status"),
-    METHOD("raw", py_raw, "raw(tensor, what, dtype): pointer, row pitch, rows, row bytes, device"),
-    METHOD("tensors", py_tensors, "tensors(sequence, what, device, like): pointers, counts, type codes"),
     METHOD("norm", py_norm, "sim_norm"),
     METHOD("norm_grad", py_norm_grad, "sim_norm_grad"),
     METHOD("dispatch", py_dispatch, "sim_dispatch"),
@@ -620,20 +279,6 @@ static struct PyModuleDef pycall_module = {
 
 PyMODINIT_FUNC PyInit__pycall(void) {
   if (PyType_Ready(&PreparedCallType) < 0) return NULL;
-  s_dtype = PyUnicode_InternFromString("dtype");
-  s_shape = PyUnicode_InternFromString("shape");
-  s_device = PyUnicode_InternFromString("get_device");
-  s_contiguous = PyUnicode_InternFromString("is_contiguous");
-  s_data_ptr = PyUnicode_InternFromString("data_ptr");
-  s_stride = PyUnicode_InternFromString("stride");
-  s_gain = PyUnicode_InternFromString("gain");
-  s_esize = PyUnicode_InternFromString("element_size");
-  s_numel = PyUnicode_InternFromString("numel");
-  s_ids = PyUnicode_InternFromString("ids");
-  s_teacher = PyUnicode_InternFromString("teacher");
-  if (!s_dtype || !s_shape || !s_device || !s_contiguous || !s_data_ptr || !s_stride || !s_esize || !s_numel || !s_gain || !s_ids ||
-      !s_teacher)
-    return NULL;
   PyObject* m = PyModule_Create(&pycall_module);
   if (!m) return NULL;
   Py_INCREF(&PreparedCallType);

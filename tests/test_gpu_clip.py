@@ -207,6 +207,32 @@ def test_streams_and_graphs(lib):
         assert torch.equal(norm, n) and all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+def test_both_forms_of_the_tensor_checks_agree(lib):
+    """The checks in C++ and their Python forms return or refuse the same, for tensors of any kind."""
+    x = torch.zeros(6, 40, device="cuda")
+    some = [x, x.half(), x.bfloat16(), x[:, 3:9], x[::2], x[:1], x[:0], x[:, :1], x[:, :0], x.t(), x[0], x.int(), x.double(),
+            x.cpu(), x.view(2, 3, 40), x[:, ::2], x.to(torch.float8_e4m3fn), torch.nn.Parameter(x), x.expand(6, 40), x[:1].expand(6, 40)]
+    mine = lib._rows_py(x, "x", None)
+    lists = [[], [x], [x, x.half()], [x.half(), x], [x, x.t()], [x.cpu()], [x.int()], [x[:0], x[1]], (x,), [x.view(-1)]]
+    likes = [None] + [lib._tensors_py(ts, "l", 0, None) for ts in ([], [x], [x, x.half()])]
+    pairs = [(lib._raw, lib._raw_py, [(t, "t", d) for t in some for d in (None, torch.float32, torch.float8_e4m3fn)]),
+             (lib._like, lib._like_py, [(t, "t", mine) for t in some + [None]]),
+             (lib._rows, lib._rows_py, [(t, "t", w) for t in some for w in (None, mine)]),
+             (lib._gain, lib._gain_py, [(t, n, 0) for t in some + [None, x.view(-1)] for n in (40, 240)]),
+             (lib._vec, lib._vec_py, [(t, "t", (torch.float32,), 0, 6, 40) for t in some + [None]]),
+             (lib._tensors, lib._tensors_py, [(ts, "l", 0, w) for ts in lists for w in likes])]
+    for c, py, calls in pairs:
+        assert c is not py
+        for args in calls:
+            got = []
+            for f in (c, py):
+                try:
+                    got.append(f(*args))
+                except ValueError as e:
+                    got.append(type(e))
+            assert got[0] == got[1], (py.__name__, args)
+
+
 def test_refusals(lib):
     a, b = torch.ones(10, device="cuda"), torch.ones(6, 4, device="cuda")
     for f in (lambda: lib.clip_grads([a, b.t()], 1.0), lambda: lib.clip_grads([a, b.cpu()], 1.0), lambda: lib.clip_grads([a.cpu()], 1.0),
