@@ -7,10 +7,10 @@
 // not within fp32's.  Tensors are cut into pieces of 16 KiB, and the workgroups'
 // sums are added up in their order, so that the same list gives the same bits.
 //
-// Bound by memory: 748 us for 809 M bf16 and 33 K fp32 gradients (read, then read and
+// Bound by memory: 747 us for 809 M bf16 and 33 K fp32 gradients (read, then read and
 // written: 4,857 MB at 6.5 TB/s; a copy of as many bytes 730).  2.6 M halves in nine
-// tensors take 7.6 us on the GPU and 13.3 a call: 7 are the helper's look at 18
-// tensors, the rest two launches.
+// tensors take 7.6 us on the GPU and 10.3 a call: 3 are the helper's, the rest two
+// launches.
 #include "launch.h"
 #include "layer.h"
 #include "loss_device.h"

@@ -239,6 +239,23 @@ def test_helpers_refuse_host_tensors():
             f()
 
 
+def test_tensor_extension_is_built_and_survives_what_is_no_tensor():
+    import all_reduce_reduction_amd as sim
+    assert sim._pytensor is not None, "the tensor extension is not built"
+    for call in (lambda: sim._rows(3, "x", None), lambda: sim._raw("x", "x", None), lambda: sim._rows(torch.zeros(2, 2), "x"),
+                 lambda: sim._vec([1], "x", (torch.float32,), 0, 1), lambda: sim._vec(torch.zeros(1), "x", 7, 0, 1),
+                 lambda: sim._gain(1.0, 2, 0), lambda: sim._gain(torch.zeros(2), "two", 0), lambda: sim._like(None, "x", (1, 2)),
+                 lambda: sim._tensors([1, 2], "l", 0, None), lambda: sim._tensors(None, "l", 0, None),
+                 lambda: sim._slots(None, None, (), 1, 0), lambda: sim._slots(torch.zeros(1, 1), 5, (torch.float32,), 1, 0)):
+        with pytest.raises(TypeError):
+            call()
+    meta = torch.zeros(2, 3, device="meta")
+    for call in (lambda: sim._rows(meta, "x", None), lambda: sim._vec(meta, "x", (torch.float32,), 0, 2, 3),
+                 lambda: sim._tensors([meta], "l", 0, None), lambda: sim._rows(torch.zeros(2, 3).to_sparse(), "x", None)):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_limits_match_the_header():
     import re
 
