@@ -531,9 +531,11 @@ __device__ __forceinline__ void grad_rows(const CombineGradArgs& a, const TokenS
     for (int i = 0; i < N; i++) a.dweights[token * a.topk + slot[i]] = dot[i];
   }
 }
-// Where there are too few tokens to fill the GPU with a wave each, eight waves
-// share one (333 tokens x 2,263 fp32, 6 slots: 9.2 us, four 9.9, sixteen 11.3).
-constexpr int kManyWaves = 8;
+// Where there are too few tokens to fill the GPU with a wave each, up to eight waves
+// share one (333 tokens x 2,263 fp32, 6 slots: 9.2 us, four 9.9, sixteen 11.3), but
+// no more than its row has 64 vectors for: the others would only wait (bf16, 1,116
+// tokens x 737, 14 slots, two waves 12.7 us, eight 22.6; 1,500 x 2,048, 4 slots,
+// four waves 11.2, eight 12.8).
 template <int DT, int W, Where K, bool STREAM>
 __global__ void __launch_bounds__(W > 1 ? 64 * W : 256) k_combine_grad(CombineGradArgs a) {
   __shared__ float dot_s[W][8];
@@ -595,6 +597,13 @@ hipError_t combine(const CombineArgs& a, hipStream_t s) {
   if (a.topk > 4) return launch<k_combine<DT, 4>>(grid, dim3(256), s, a, parts);
   return launch<k_combine<DT, 8>>(grid, dim3(256), s, a, parts);
 }
+// W waves share a token
+template <int DT, int W>
+hipError_t combine_grad_shared(const CombineGradArgs& a, bool stream, hipStream_t s) {
+  const dim3 grid(grid_of(a.tokens, 1));
+  return stream ? launch<k_combine_grad<DT, W, kEnd, true>>(grid, dim3(64 * W), s, a)
+                : launch<k_combine_grad<DT, W, kEnd, false>>(grid, dim3(64 * W), s, a);
+}
 template <int DT>
 hipError_t combine_grad(const CombineGradArgs& a, hipStream_t s) {
   constexpr int V = epv<DT>();
@@ -624,9 +633,9 @@ hipError_t combine_grad(const CombineGradArgs& a, hipStream_t s) {
     return stream ? launch<k_combine_grad<DT, 1, kEnd, true>>(grid, dim3(256), s, a)
                   : launch<k_combine_grad<DT, 1, kEnd, false>>(grid, dim3(256), s, a);
   }
-  const dim3 grid(grid_of(a.tokens, 1));
-  return stream ? launch<k_combine_grad<DT, kManyWaves, kEnd, true>>(grid, dim3(64 * kManyWaves), s, a)
-                : launch<k_combine_grad<DT, kManyWaves, kEnd, false>>(grid, dim3(64 * kManyWaves), s, a);
+  if (nv <= 128) return combine_grad_shared<DT, 2>(a, stream, s);
+  if (nv <= 256) return combine_grad_shared<DT, 4>(a, stream, s);
+  return combine_grad_shared<DT, 8>(a, stream, s);
 }
 
 }  // namespace

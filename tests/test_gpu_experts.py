@@ -163,7 +163,8 @@ def test_dispatch_slices(lib, dtype):
     assert not big.float()[:, :3].any() and not big.float()[:, 3 + c:].any() and not big.float()[n:].any()
 
 
-COMBINE = [(1, 1, 1), (1, 8, 8192), (7, 3, 5), (65, 8, 64), (40, 8, 129), (33, 9, 520), (20, 32, 1025), (9, 17, 2049), (5, 4, 5003), (300, 2, 8)]
+COMBINE = [(1, 1, 1), (1, 8, 8192), (7, 3, 5), (65, 8, 64), (40, 8, 129), (33, 9, 520), (20, 32, 1025), (9, 17, 2049), (5, 4, 5003), (300, 2, 8),
+           (19, 11, 500), (23, 14, 1024), (18, 7, 1031), (16, 5, 2048)]
 
 
 def expert_case(t, k, c, dtype, seed, spare=3):
