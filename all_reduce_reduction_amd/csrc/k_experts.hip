@@ -640,13 +640,24 @@ hipError_t combine_grad(const CombineGradArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t s) {
+// Few slots go in one launch while a workgroup reads few of them, once for every 8
+// of its token's slots, and all workgroups together not too many; else in two.
+// A workgroup's own: 512 tokens of 4 KiB, 8 slots, 4,096 read: 8.8 us, 10.3 in two
+// launches; 128, 16 slots, 4,096: 8.5, 9.4; 400, 10 slots, 8,000: 13.4, 10.4; 128, 32
+// slots, 16,384: 22.8, 11.2.  All of them: 1,024 of 8 KiB, 2 slots, 4.2 M: 9.9, 12.0;
+// 1,600 of 4 KiB, 2 slots, 5.1 M: 11.6, 10.9; 4,096, one slot, 16.8 M: 22.7, 14.1.
+constexpr int64_t kFewChunk = 1024, kFewOwn = 6 << 10, kFewReads = 9 << 19;
+hipError_t launch_dispatch(const DispatchArgs& args, hipStream_t s) {
+  DispatchArgs a = args;
   // a wave for each part of a token's row
   const int64_t longest = std::max(std::max(a.row_bytes, a.scales ? a.scale_bytes : 0), (int64_t)1);
   const int parts = (int)((longest + kPartBytes - 1) / kPartBytes);
   if (a.chunks == 0) {
-    const int groups = (parts + 3) / 4;
-    return launch<k_dispatch_few>(dim3((unsigned)(a.tokens * groups + 1)), dim3(256), s, a, groups);
+    const int64_t slots = a.tokens * a.topk, groups = (parts + 3) / 4, own = slots * ((a.topk + 7) / 8);
+    if (own <= kFewOwn && a.tokens * groups * own <= kFewReads)
+      return launch<k_dispatch_few>(dim3((unsigned)(a.tokens * groups + 1)), dim3(256), s, a, (int)groups);
+    a.chunk = kFewChunk;
+    a.chunks = (int)((slots + kFewChunk - 1) / kFewChunk);
   }
   hipError_t e;
   if (a.counts) {

@@ -26,8 +26,9 @@ int norm_grad_workgroups(int64_t rows, int64_t cols, int dtype) {
   return (int)std::max<int64_t>(1, (turns + each - 1) / each);
 }
 
-// Up to so many slots each token's workgroup reads all of them (512 tokens of 4
-// KiB, 8 slots: 9.3 us, 12.8 in three launches; 1,000 tokens, 6 slots: 15.0, 14.6).
+// Up to so many slots each token's workgroup may read all of them (512 tokens of 4
+// KiB, 8 slots: 8.8 us, 10.3 in two launches; 1,000 tokens, 6 slots: 15.0, 14.6 in
+// three).
 constexpr int64_t kFewSlots = 4096;
 int dispatch_chunks(int64_t slots, int64_t* chunk) {
   *chunk = 0;

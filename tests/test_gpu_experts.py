@@ -74,6 +74,22 @@ def test_dispatch_sizes(lib, t, k, e, c, dtype):
     check_dispatch(lib, x, choose(t, k, e, t + k, 0.2 if t % 2 else 0.0), e, scales=torch.rand(t, 3, generator=g) if c % 2 else None)
 
 
+# few slots that many workgroups would read: both sides of where they are placed by a launch of their own
+@pytest.mark.parametrize("t,k,e,c", [(2172, 1, 5, 7), (2173, 1, 5, 7), (48, 32, 9, 300), (49, 32, 9, 300), (341, 9, 30, 5),
+                                     (342, 9, 30, 5), (4096, 1, 1024, 40), (1500, 1, 9, 2122), (1365, 3, 16, 1030),
+                                     (128, 32, 8, 5000), (455, 9, 64, 4500)])
+@pytest.mark.parametrize("dtype", [torch.float32, oracle.E4M3])
+def test_dispatch_of_few_slots_to_be_read_often(lib, t, k, e, c, dtype):
+    g = torch.Generator().manual_seed(t + c)
+    x = torch.randint(0, 256, (t, c), generator=g, dtype=torch.uint8)
+    x = x.float() if dtype == torch.float32 else x.view(dtype)
+    check_dispatch(lib, x, choose(t, k, e, t + k, 0.2 if t % 2 else 0.0), e, scales=torch.rand(t, 3, generator=g) if t % 3 else None)
+    chosen = choose(t, k, e, t, 0.1)
+    rows, place, offsets, _ = lib.dispatch(torch.empty(t, 0, device="cuda"), chosen.cuda(), e)
+    want = oracle.places(chosen, e)
+    assert torch.equal(place.cpu(), want[0]) and torch.equal(offsets.cpu(), want[1])
+
+
 @pytest.mark.parametrize("c", [1, 15, 16, 17, 255, 257, 2047, 2049, 4096, 5000])
 @pytest.mark.parametrize("t", [37, 700])
 def test_dispatch_row_lengths(lib, t, c):
