@@ -65,7 +65,12 @@ def test_quant_sizes(lib, n, c, dtype):
         oracle.check_quant(q, scales, total, x, gain, residual, EPS, group, f"group {group}")
 
 
-@pytest.mark.parametrize("n,c", SIZES + MANY)
+# both sides of where one workgroup takes all rows, and of where each takes one row, two, and up to four
+SHARED = [(64, 300), (65, 300), (4, 1500), (5, 1500), (2, 9000), (3, 9000), (255, 4112), (256, 4112), (513, 2300), (1027, 1100),
+          (120, 10000)]
+
+
+@pytest.mark.parametrize("n,c", SIZES + MANY + SHARED)
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_grad_sizes(lib, n, c, dtype):
     h, dy, ds = rand(n, c, dtype, n + c + 4, 2.0), rand(n, c, dtype, n + c + 5), rand(n, c, dtype, n + c + 6)
