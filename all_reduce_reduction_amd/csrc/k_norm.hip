@@ -5,7 +5,7 @@
 // sum is rounded to the activations' type only as it is written; y is taken of
 // the unrounded one.  In 8 bits, with m the largest |g h| of a scale's columns:
 // scale = m r / 448 and q = e4m3(g h * 448 / m), so that q needs no r and y is
-// not rounded in between.
+// not rounded in between: of 16-bit values q is the nearest code, of two the even one.
 //
 // A row stays in the registers of its lanes (8 to 64) or of its workgroup from its
 // one read to its writes; a workgroup is cut to the row's length in whole waves, so
@@ -65,10 +65,13 @@ __device__ __forceinline__ float largest(const float (&x)[V]) {
   return m;
 }
 
-// g h on its way to e4m3.  448 / m by the hardware's reciprocal (1 ulp): the
-// largest value becomes 448 within 2 ulp, which rounds to 448.  Near the type's
-// smallest values m and g h are scaled up first, so that 448 / m is finite and m
-// no denormal number, which the reciprocal would take for 0.
+// g h on its way to e4m3: g h * 448 / m, rounded once.  Values in 16 bits often lie
+// halfway between two codes exactly, and go to the even one only if the quotient has
+// no error of its own: 448 / m as the hardware's reciprocal (1 ulp) and what it
+// leaves, together off by 2^-44, so that the fused sum is the nearest float and a
+// halfway value stays one.  Near the type's smallest values m and g h are scaled up
+// first, so that 448 / m is finite and m no denormal number, which the reciprocal
+// would take for 0.
 template <int V>
 __device__ __forceinline__ void quantise(float (&x)[V], float m) {
   if (__builtin_expect(m < 0x1p-100f, 0)) {
@@ -76,9 +79,12 @@ __device__ __forceinline__ void quantise(float (&x)[V], float m) {
     for (int t = 0; t < V; t++) x[t] *= 0x1p100f;
     m *= 0x1p100f;
   }
-  const float f = m > 0.0f ? kE4m3Max * __builtin_amdgcn_rcpf(m) : 0.0f;
+  const float inv = __builtin_amdgcn_rcpf(m), f = kE4m3Max * inv;
+  // (a group of zeros stays one; finite values beside an infinite one become 0)
+  const bool sane = m > 0.0f && m < __builtin_inff();
+  const float hi = sane ? f : 0.0f, lo = sane ? __builtin_fmaf(-f, m, kE4m3Max) * inv : 0.0f;
 #pragma unroll
-  for (int t = 0; t < V; t++) x[t] *= f;
+  for (int t = 0; t < V; t++) x[t] = __builtin_fmaf(x[t], hi, x[t] * lo);
 }
 
 // L lanes (8, 16, 32 or 64; several rows share a workgroup of 256 threads) or, with

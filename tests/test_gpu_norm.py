@@ -162,6 +162,48 @@ def test_small_groups_of_small_values(lib, dtype):
         oracle.check_quant(q, s, None, x, None, None, EPS, group)
 
 
+def nearest_codes(t):
+    """e4m3 values nearest to t in 64 bits, of two equally near ones the even one."""
+    e = (torch.frexp(t)[1] - 1).clamp(min=-6)
+    step = torch.exp2(e.double() - 3)
+    return (torch.round(t / step) * step).clamp(-448, 448)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_halfway_between_two_codes(lib, dtype):
+    """g h * 448 / m halfway between two codes becomes the even one.  Every value here is a product of integers of at
+    most 8 bits and a power of two, and so is exact in every type and in the sums of products."""
+    odd = [n + 0.5 for n in range(8, 16)]  # between codes of one power of two
+    t = torch.tensor([448.0] + [v * 2.0 ** k for k in range(-3, 5) for v in odd] + [(n + 0.5) * 2.0 ** -9 for n in range(8)] + [2.0 ** -10])
+    t = torch.cat([t, torch.zeros(128 - len(t))]).repeat(2).double()
+    for top in (448.0, 7.0, 0.875, 224.0, 448.0 * 2 ** -12, 3.5 * 2 ** 20 if dtype != torch.float16 else 3.5 * 2 ** 10):
+        x = t * top / 448
+        keep = x.to(dtype).double() == x  # (what a half's denormal numbers cannot hold is left out)
+        x = torch.where(keep, x, 0.0)
+        want = nearest_codes(torch.where(keep, t, 0.0))
+        x = torch.stack([x, -x]).to(dtype).cuda()
+        for group in (128, 256):
+            for gain in (None, torch.full((len(t),), 4.0, dtype=dtype, device="cuda")):
+                q, _, _ = lib.norm_quant(x, gain, group=group)
+                assert torch.equal(q.cpu().double(), torch.stack([want, -want])), (top, group)
+
+
+@pytest.mark.parametrize("n,c", [(37, 40), (64, 128), (50, 300), (20, 1000), (9, 2500), (8, 8192), (6, 20000)])
+@pytest.mark.parametrize("group", [32, 128, 0])
+def test_codes_of_16_bit_values_are_the_nearest(lib, n, c, group):
+    """Of bf16 values x and gain, g x and m are integers a, b < 2^16 times powers of two, and a halfway value is an odd
+    integer T < 2^5 times one.  448 a / b is equal to T, or relative to it at least 1 / (T b) > 2^-21 away, more than
+    what one rounding to fp32 moves it: the codes are those of the quotient in 64 bits."""
+    x, gain = rand(n, c, torch.bfloat16, n + c), gains(c, torch.bfloat16, c)
+    q, _, _ = lib.norm_quant(x.cuda(), gain.cuda(), eps=EPS, group=group or c)
+    gx = gain.double() * x.double()
+    g = group or c
+    k = -(-c // g)
+    parts = torch.nn.functional.pad(gx, (0, k * g - c)).view(n, k, g)
+    t = (parts * 448 / parts.abs().amax(2, keepdim=True)).view(n, k * g)[:, :c]
+    assert torch.equal(q.cpu().double(), nearest_codes(t))
+
+
 def test_eps_is_all_that_a_row_of_zeros_has(lib):
     x = torch.full((3, 70), 1e-15)
     for eps in (1e-30, 1.0, 1e30):
