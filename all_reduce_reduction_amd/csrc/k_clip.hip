@@ -140,11 +140,10 @@ __global__ void __launch_bounds__(kBlock) SIMAR_CLIP_WAVES k_clip_squares(ClipLi
   if (threadIdx.x == 0) squares[blockIdx.x] = sum;
 }
 
-// the norm of all, in every thread
-__device__ __forceinline__ float norm_of(const ClipNorm& n) {
+// The sum of all squares, in every thread.
+__device__ __forceinline__ double sum_of(const ClipNorm& n) {
   double sum = 0.0;
   if (n.parts) {
-    if (n.nparts == 1) return fabsf(n.parts[0]);
     for (int i = threadIdx.x; i < n.nparts; i += kBlock) {
       const double p = (double)n.parts[i];
       sum = __builtin_fma(p, p, sum);
@@ -152,12 +151,31 @@ __device__ __forceinline__ float norm_of(const ClipNorm& n) {
   } else {
     for (int i = threadIdx.x; i < n.nsquares; i += kBlock) sum += n.squares[i];
   }
-  return (float)sqrt(block_sum64(sum));
+  return block_sum64(sum);
+}
+// The norm that the factor is formed of: a list's own in 64 bits, rounded only as
+// norm[0] (2^-24 of the factor, the same for every element); the ranks' as norm[0]
+// holds it, so that all ranks have the same factor whatever launches their own lists
+// take.  Past fp32's range it is infinite, as norm[0] is.
+__device__ __forceinline__ double norm_of(const ClipNorm& n) {
+  if (n.parts && n.nparts == 1) return (double)fabsf(n.parts[0]);
+  const double norm = sqrt(sum_of(n));
+  const float rounded = (float)norm;
+  return n.parts || rounded == __builtin_inff() ? (double)rounded : norm;
 }
 
 __global__ void __launch_bounds__(kBlock) k_clip_join(ClipNorm n) {
-  const float norm = norm_of(n);
-  if (threadIdx.x == 0) n.norm[0] = norm;
+  if (n.total) {
+    // (every thread has read its squares before the sum is there)
+    const double sum = sum_of(n);
+    if (threadIdx.x == 0) {
+      n.norm[0] = (float)sqrt(sum);
+      n.total[0] = sum;
+    }
+  } else {
+    const double norm = norm_of(n);
+    if (threadIdx.x == 0) n.norm[0] = (float)norm;
+  }
 }
 
 // A workgroup scales one piece, whose vectors are on their way while the norm is
@@ -173,10 +191,10 @@ __global__ void __launch_bounds__(kBlock) SIMAR_CLIP_WAVES k_clip_scale(ClipList
 #pragma unroll
     for (int i = 0; i < kEach; i++) v[i] = ld_row_lane<SIM_BF16, true>(in, 0, (i * kBlock + threadIdx.x) * 8);
   }
-  const float norm = norm_of(n);
-  if (n.norm && blockIdx.x == 0 && threadIdx.x == 0) n.norm[0] = norm;
+  const double norm = norm_of(n);
+  if (n.norm && blockIdx.x == 0 && threadIdx.x == 0) n.norm[0] = (float)norm;
   // (a NaN norm makes everything NaN)
-  const float c = norm <= n.max_norm ? 1.0f : (float)((double)n.max_norm / (double)norm);
+  const float c = norm <= (double)n.max_norm ? 1.0f : (float)((double)n.max_norm / norm);
   if (n.in_place && c == 1.0f) return;
   if (p.dtype == SIM_FP32) scale_to<SIM_FP32>(in, out, p.n, c, v);
   else if (p.dtype == SIM_FP16) scale_to<SIM_FP16>(in, out, p.n, c, v);

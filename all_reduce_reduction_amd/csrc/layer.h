@@ -127,6 +127,7 @@ struct ClipNorm {
   float max_norm;
   float* norm;            // NULL: another launch writes it
   int in_place;
+  double* total;          // NULL, or where launch_clip_join leaves the squares' sum (squares itself, say)
 };
 
 // layer_sizes.cpp

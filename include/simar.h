@@ -651,6 +651,9 @@ int sim_combine_grad(const void* dy, int64_t dy_stride, int dtype, const void* r
  *                  norm[0] is the norm; with parts[nparts] (the norms of all
  *                  ranks' own gradients, as sim_all_gather leaves them) it is
  *                  sqrt(the sum of their squares), and work is not needed.
+ *                  The factor is formed of the norm in 64 bits and rounded to
+ *                  fp32; with parts it is formed of norm[0], so that every rank
+ *                  has the same one.
  * A NaN norm makes everything NaN; an infinite one (also: a norm past fp32's
  * range) makes finite gradients 0 and infinite ones NaN, by the formula.
  * max_norm is not negative; +inf: nothing is scaled.  No output may overlap

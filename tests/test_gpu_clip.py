@@ -157,6 +157,33 @@ def test_parts_of_many_ranks_and_of_one(lib):
         assert all((t == 0.25).all() for t in g)
 
 
+@pytest.mark.parametrize("sizes", [[5000], [700, 4000, 33], [40] * 130, [9000000]], ids=lambda s: f"{len(s)}x{s[0]}")
+def test_the_factor_is_formed_of_the_norm_in_64_bits(lib, sizes):
+    """One rounding of the factor and one of the product, u = 2^-24 each; the sums in 64 bits are off by far less than
+    2^-16 u.  Whatever the norm's own rounding would add is common to all elements."""
+    worst = 0.0
+    for seed in range(100 if sum(sizes) < 10000 else 4):
+        grads = [(torch.rand(n, generator=torch.Generator("cuda").manual_seed(seed), device="cuda") + 0.5) for n in sizes]
+        want = torch.cat([g.double() for g in grads])
+        norm = want.square().sum().sqrt().item()
+        most = torch.tensor(norm / (1.3 + seed / 30)).item()
+        lib.clip_grads(grads, most)
+        want *= torch.tensor(most, dtype=torch.float32).double().item() / norm
+        worst = max(worst, ((torch.cat([g.double() for g in grads]) - want).abs() / want).max().item())
+    assert worst <= (2 + 2.0 ** -16) * oracle.U, worst / oracle.U
+
+
+@pytest.mark.parametrize("tensors,n", [(3, 1000), (130, 50), (1, 40000000)])
+def test_ranks_with_the_same_parts_have_the_same_factor(lib, tensors, n):
+    """Whichever launches a rank's own list takes; factor and norm are those of the fp32 norm[0]."""
+    for seed in range(20):
+        parts = (torch.rand(8, generator=torch.Generator().manual_seed(seed)) + 1.0).cuda()
+        few, own = [torch.ones(16, device="cuda")], [torch.ones(n, device="cuda") for _ in range(tensors)]
+        a, b = lib.clip_grads(few, 0.7, parts=parts), lib.clip_grads(own, 0.7, parts=parts)
+        factor = (torch.tensor(0.7).double() / a.double().cpu()).float()
+        assert torch.equal(a, b) and (few[0].cpu() == factor).all() and all((g == few[0][0]).all() for g in own)
+
+
 def test_the_same_bits_every_time(lib):
     grads = [g.cuda() for g in make([500001, 77, 40000], DTYPES, 20)]
     a, b = ([torch.empty_like(g) for g in grads] for _ in range(2))
