@@ -99,27 +99,44 @@ __device__ __forceinline__ void squares_of(const char* in, int n, double& sum) {
   }
 }
 
+// max_norm / norm as a float c and a power of two, which is 1 unless the quotient is
+// below fp32's normal numbers, where c alone would have lost bits (1e30 clipped to
+// 1e-13: c = 5e-44, of 5 bits) that the product has: then c lies in [1/2, 1).
+struct Factor {
+  float power, c;
+  __device__ __forceinline__ Factor(double norm, float max_norm) : power(1.0f) {
+    // (a NaN norm makes everything NaN)
+    const double q = norm <= (double)max_norm ? 1.0 : (double)max_norm / norm;
+    c = (float)q;
+    if (q > 0.0 && q < 0x1p-126) {
+      const int e = __builtin_amdgcn_frexp_exp(q), k = e < -149 ? -149 : e;
+      power = (float)__builtin_amdgcn_ldexp(1.0, k);
+      c = (float)__builtin_amdgcn_ldexp(q, -k);
+    }
+  }
+  __device__ __forceinline__ float operator()(float g) const { return g * power * c; }
+};
 template <int DT>
-__device__ __forceinline__ u32x4 scaled(u32x4 v, float c) {
+__device__ __forceinline__ u32x4 scaled(u32x4 v, const Factor& by) {
   constexpr int V = epv<DT>();
   float f[V];
   unpack<DT>(v, f);
 #pragma unroll
-  for (int t = 0; t < V; t++) f[t] *= c;
+  for (int t = 0; t < V; t++) f[t] = by(f[t]);
   return pack_rounded<DT>(f);
 }
 // A whole piece's vectors are given, the others' read.
 template <int DT>
-__device__ __forceinline__ void scale_to(const char* in, char* out, int n, float c, const u32x4 (&v)[kEach]) {
+__device__ __forceinline__ void scale_to(const char* in, char* out, int n, const Factor& by, const u32x4 (&v)[kEach]) {
   constexpr int V = epv<DT>();
   if (n == kVectors * V) {
 #pragma unroll
-    for (int i = 0; i < kEach; i++) st_row_lane<DT, true>(out, 0, (i * kBlock + threadIdx.x) * V, scaled<DT>(v[i], c));
+    for (int i = 0; i < kEach; i++) st_row_lane<DT, true>(out, 0, (i * kBlock + threadIdx.x) * V, scaled<DT>(v[i], by));
   } else {
     for (int i = threadIdx.x; i < n / V; i += kBlock)
-      st_row<DT>(out, (int64_t)i * V, scaled<DT>(ld_row<DT>(in, (int64_t)i * V), c));
+      st_row<DT>(out, (int64_t)i * V, scaled<DT>(ld_row<DT>(in, (int64_t)i * V), by));
     const int i = n / V * V + threadIdx.x;
-    if (i < n) store_elem<DT>(out, i, load_elem<DT>(in, i) * c);
+    if (i < n) store_elem<DT>(out, i, by(load_elem<DT>(in, i)));
   }
 }
 
@@ -193,12 +210,11 @@ __global__ void __launch_bounds__(kBlock) SIMAR_CLIP_WAVES k_clip_scale(ClipList
   }
   const double norm = norm_of(n);
   if (n.norm && blockIdx.x == 0 && threadIdx.x == 0) n.norm[0] = (float)norm;
-  // (a NaN norm makes everything NaN)
-  const float c = norm <= (double)n.max_norm ? 1.0f : (float)((double)n.max_norm / norm);
-  if (n.in_place && c == 1.0f) return;
-  if (p.dtype == SIM_FP32) scale_to<SIM_FP32>(in, out, p.n, c, v);
-  else if (p.dtype == SIM_FP16) scale_to<SIM_FP16>(in, out, p.n, c, v);
-  else scale_to<SIM_BF16>(in, out, p.n, c, v);
+  const Factor by(norm, n.max_norm);
+  if (n.in_place && by.power == 1.0f && by.c == 1.0f) return;
+  if (p.dtype == SIM_FP32) scale_to<SIM_FP32>(in, out, p.n, by, v);
+  else if (p.dtype == SIM_FP16) scale_to<SIM_FP16>(in, out, p.n, by, v);
+  else scale_to<SIM_BF16>(in, out, p.n, by, v);
 }
 
 }  // namespace

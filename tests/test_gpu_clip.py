@@ -157,6 +157,23 @@ def test_parts_of_many_ranks_and_of_one(lib):
         assert all((t == 0.25).all() for t in g)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size,most", [(1e37, 1.0), (1e37, 1e-4), (1e37, 1e-7), (1e30, 1e-13), (1e20, 1e-26), (1e37, 1e-37), (1e25, 1e-30)])
+def test_factors_below_the_normal_numbers(lib, dtype, size, most):
+    """fp32: the factor and the product round by at most u; below the normal numbers what is multiplied with the factor
+    and the product by half a step of 2^-149 each."""
+    grads = make([90, 5000 if size < 1e36 else 30], [dtype], 5, size)
+    want = oracle.norm_of(grads).item()
+    most = torch.tensor(most, dtype=torch.float32).item()
+    for outs in (None, [torch.full_like(g, 7.0, device="cuda") for g in grads]):
+        mine = [g.cuda() for g in grads]
+        lib.clip_grads(mine, most, out=outs)
+        for a, g in zip(mine if outs is None else outs, grads):
+            w = g.double() * (most / want)
+            tol = (2 + 2.0 ** -16) * oracle.U * w.abs() + 2.0 ** -149
+            oracle.assert_within(a, w, oracle.rounded(tol, w, dtype) if dtype != torch.float32 else tol, f"{size} {most}")
+
+
 @pytest.mark.parametrize("sizes", [[5000], [700, 4000, 33], [40] * 130, [9000000]], ids=lambda s: f"{len(s)}x{s[0]}")
 def test_the_factor_is_formed_of_the_norm_in_64_bits(lib, sizes):
     """One rounding of the factor and one of the product, u = 2^-24 each; the sums in 64 bits are off by far less than
