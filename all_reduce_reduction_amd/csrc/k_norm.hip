@@ -1,9 +1,10 @@
 // k_norm.hip -- root-mean-square norm of x + residual, in the activations' type
 // or in e4m3 with scales (gfx950).
 //
-// Row h = x + residual in fp32: r = (sum h^2 / n + eps)^(-1/2), y = g h r.  The
-// sum is rounded to the activations' type only as it is written; y is taken of
-// the unrounded one.  In 8 bits, with m the largest |g h| of a scale's columns:
+// Row h = x + residual in fp32: r = (sum h^2 / n + eps)^(-1/2), y = g (h r): |h r| is
+// at most sqrt n, so that no product on the way is past fp32's range if y is not.  The
+// sum is rounded to the activations' type only as it is written; y is taken of the
+// unrounded one.  In 8 bits, with m the largest |g h| of a scale's columns:
 // scale = m r / 448 and q = e4m3(g h * 448 / m), so that q needs no r and y is
 // not rounded in between: of 16-bit values q is the nearest code, of two the even one.
 //
@@ -69,22 +70,39 @@ __device__ __forceinline__ float largest(const float (&x)[V]) {
 // halfway between two codes exactly, and go to the even one only if the quotient has
 // no error of its own: 448 / m as the hardware's reciprocal (1 ulp) and what it
 // leaves, together off by 2^-44, so that the fused sum is the nearest float and a
-// halfway value stays one.  Near the type's smallest values m and g h are scaled up
-// first, so that 448 / m is finite and m no denormal number, which the reciprocal
-// would take for 0.
+// halfway value stays one.
 template <int V>
 __device__ __forceinline__ void quantise(float (&x)[V], float m) {
-  if (__builtin_expect(m < 0x1p-100f, 0)) {
-#pragma unroll
-    for (int t = 0; t < V; t++) x[t] *= 0x1p100f;
-    m *= 0x1p100f;
-  }
-  const float inv = __builtin_amdgcn_rcpf(m), f = kE4m3Max * inv;
-  // (a group of zeros stays one; finite values beside an infinite one become 0)
-  const bool sane = m > 0.0f && m < __builtin_inff();
-  const float hi = sane ? f : 0.0f, lo = sane ? __builtin_fmaf(-f, m, kE4m3Max) * inv : 0.0f;
+  const float inv = __builtin_amdgcn_rcpf(m), hi = kE4m3Max * inv, lo = __builtin_fmaf(-hi, m, kE4m3Max) * inv;
 #pragma unroll
   for (int t = 0; t < V; t++) x[t] = __builtin_fmaf(x[t], hi, x[t] * lo);
+}
+
+// Near the ends of fp32's range (m = max |g h| outside [2^-100, 2^100)) g h may have
+// overflowed or lost bits although g (h r) is a normal number, and 448 / m be one that
+// the reciprocal takes for 0.  There g h is formed again, as a multiple of `unit`: the
+// smaller of both by 2^126, or the larger by 2^-126.  (Groups of zeros go that way too,
+// for those that g h alone made so.)
+__device__ __forceinline__ bool mid_range(float m) { return m >= 0x1p-100f && m < 0x1p100f; }
+struct Range {
+  float by, unit;
+  bool low;
+  __device__ __forceinline__ explicit Range(float m)
+      : by(mid_range(m) ? 1.0f : m < 1.0f ? 0x1p126f : 0x1p-126f),
+        unit(mid_range(m) ? 1.0f : m < 1.0f ? 0x1p-126f : 0x1p126f), low(m < 1.0f) {}
+  __device__ __forceinline__ float operator()(float g, float h) const {
+    const bool first = (fabsf(g) < fabsf(h)) == low;
+    return (first ? g : h) * by * (first ? h : g);
+  }
+};
+// A group without a largest value that quantise could divide by: zeros stay, and
+// finite values beside an infinite one become 0.
+template <int V>
+__device__ __forceinline__ void settle(float (&x)[V], float& m) {
+  const bool sane = m > 0.0f && m < __builtin_inff();
+#pragma unroll
+  for (int t = 0; t < V; t++) x[t] = sane ? x[t] : x[t] * 0.0f;
+  m = sane ? m : kE4m3Max;
 }
 
 // L lanes (8, 16, 32 or 64; several rows share a workgroup of 256 threads) or, with
@@ -92,7 +110,7 @@ __device__ __forceinline__ void quantise(float (&x)[V], float m) {
 template <int DT, int L, int R, bool TINY>
 __global__ void __launch_bounds__(L ? 256 : 1024) k_norm(NormArgs a) {
   constexpr int V = epv<DT>(), G = L ? L : 64;
-  // With one vector g h stays in registers; with more the gain is loaded again, so
+  // With one vector the gain stays in registers; with more the gain is loaded again, so
   // that two workgroups have room (16,384 x 8,192 bf16 151 us, 157.5 held).
   constexpr bool HOLD = R == 1;
   __shared__ float sum_s[2][16], top_s[2][16];
@@ -106,7 +124,7 @@ __global__ void __launch_bounds__(L ? 256 : 1024) k_norm(NormArgs a) {
   for (int64_t row = L ? (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G : (int64_t)blockIdx.x; row < a.rows;
        row += L ? (int64_t)gridDim.x * (256 / G) : (int64_t)gridDim.x, turn ^= 1) {
     const char* x = (const char*)a.x + row * a.x_stride * Ty<DT>::E;
-    float h[R][V], gh[HOLD ? R : 1][V];
+    float h[R][V], held[HOLD ? R : 1][V];
     u32x4 v[R], w[R];
     vectors([&](auto i, auto p) __attribute__((always_inline)) { v[i] = p.load(x); });
     if (a.residual) {
@@ -117,7 +135,7 @@ __global__ void __launch_bounds__(L ? 256 : 1024) k_norm(NormArgs a) {
       for (int i = 0; i < R; i++) w[i] = u32x4{0, 0, 0, 0};
     }
     if constexpr (HOLD)
-      vectors([&](auto i, auto p) __attribute__((always_inline)) { load_gain(a.gain, a.gain_dtype, p, gh[i]); });
+      vectors([&](auto i, auto p) __attribute__((always_inline)) { load_gain(a.gain, a.gain_dtype, p, held[i]); });
     float sum = 0.0f, top = 0.0f;
     vectors([&](auto i, auto p) __attribute__((always_inline)) {
       float f[V];
@@ -128,15 +146,25 @@ __global__ void __launch_bounds__(L ? 256 : 1024) k_norm(NormArgs a) {
       if (i == R - 1 && !exact) p.mask(h[i]);
 #pragma unroll
       for (int t = 0; t < V; t++) sum = __builtin_fmaf(h[i][t], h[i][t], sum);
+    });
+    const auto gains = [&](auto i, auto p, float (&g)[V]) __attribute__((always_inline)) {
       if constexpr (HOLD) {
 #pragma unroll
-        for (int t = 0; t < V; t++) gh[i][t] *= h[i][t];
+        for (int t = 0; t < V; t++) g[t] = held[i][t];
+      } else {
+        load_gain(a.gain, a.gain_dtype, p, g);
       }
-    });
+    };
+    // g h
     const auto gained = [&](auto i, auto p, float (&x)[V]) __attribute__((always_inline)) {
-      if constexpr (!HOLD) load_gain(a.gain, a.gain_dtype, p, x);
+      gains(i, p, x);
 #pragma unroll
-      for (int t = 0; t < V; t++) x[t] = HOLD ? gh[HOLD ? decltype(i)::value : 0][t] : x[t] * h[i][t];
+      for (int t = 0; t < V; t++) x[t] *= h[i][t];
+    };
+    const auto ranged = [&](auto i, auto p, const Range& in, float (&x)[V]) __attribute__((always_inline)) {
+      gains(i, p, x);
+#pragma unroll
+      for (int t = 0; t < V; t++) x[t] = in(x[t], h[i][t]);
     };
     sum = group_sum<G>(sum);
     if (one_scale) {
@@ -167,9 +195,9 @@ __global__ void __launch_bounds__(L ? 256 : 1024) k_norm(NormArgs a) {
       char* to = (char*)a.out + row * a.out_stride * Ty<DT>::E;
       vectors([&](auto i, auto p) __attribute__((always_inline)) {
         float x[V];
-        gained(i, p, x);
+        gains(i, p, x);
 #pragma unroll
-        for (int t = 0; t < V; t++) x[t] *= r;
+        for (int t = 0; t < V; t++) x[t] *= h[i][t] * r;
         if (p.any()) p.store(to, x);
       });
       continue;
@@ -177,14 +205,40 @@ __global__ void __launch_bounds__(L ? 256 : 1024) k_norm(NormArgs a) {
     char* to = (char*)a.out + row * a.out_stride;
     float* scales = a.scales + row * a.groups;
     const float unit = r * (1.0f / kE4m3Max);
+    // (all threads of a workgroup have one `top`)
+    const Range row_in(one_scale ? top : 1.0f);
+    const bool row_far = one_scale && __ballot(!mid_range(top)) != 0;
+    if (__builtin_expect(row_far, 0)) {
+      top = 0.0f;
+      vectors([&](auto i, auto p) __attribute__((always_inline)) {
+        float x[V];
+        ranged(i, p, row_in, x);
+        top = fmaxf(top, largest(x));
+      });
+      top = group_max<G>(top);
+      if (!L && waves > 1) {
+        __syncthreads();  // (the first one's maxima have been read)
+        if (lane == 0) top_s[turn][wave] = top;
+        __syncthreads();
+        top = group_max<16>((lane & 15) < waves ? top_s[turn][lane & 15] : 0.0f);
+      }
+    }
     vectors([&](auto i, auto p) __attribute__((always_inline)) {
       float x[V], m = top;
       gained(i, p, x);
+      if (a.group) m = max_of(largest(x), scale_lanes);
+      float scale = m * unit;
+      if (__builtin_expect(a.group ? __ballot(p.any() && !mid_range(m)) != 0 : row_far, 0)) {
+        const Range in = a.group ? Range(m) : row_in;
+        ranged(i, p, in, x);
+        if (a.group) m = max_of(largest(x), scale_lanes);
+        scale = m * unit * in.unit;
+        settle(x, m);
+      }
       if (a.group) {
-        m = max_of(largest(x), scale_lanes);
-        if (p.any() && p.col % (uint32_t)a.group == 0) scales[p.col / (uint32_t)a.group] = m * unit;
+        if (p.any() && p.col % (uint32_t)a.group == 0) scales[p.col / (uint32_t)a.group] = scale;
       } else if (p.col == 0) {
-        scales[0] = m * unit;
+        scales[0] = scale;
       }
       quantise(x, m);
       if (p.any()) store_e4m3(to, p, x);

@@ -574,7 +574,7 @@ int sim_distill_grad(const void* logits, int64_t row_stride, int dtype, int64_t 
 #define SIM_CLIP_MAX_TENSORS 65536
 
 /* Root-mean-square norm of rows of h = x + residual (residual NULL: h = x):
- *   r = 1 / sqrt(mean of h^2 + eps),   y = gain * h * r
+ *   r = 1 / sqrt(mean of h^2 + eps),   y = gain * (h * r)
  * h is held in fp32; sum (NULL: not written; it needs a residual) gets it
  * rounded to `dtype`, y is taken of the unrounded one.  gain[columns] is of
  * gain_dtype (NULL: all 1, gain_dtype still a valid one).
@@ -599,6 +599,9 @@ int sim_norm(const void* x, int64_t x_stride, int dtype, const void* residual, i
  *   dx    = r (gain dy - h r mean(gain dy h r)) + dsum      (rounded to `dtype`;
  *           the gradient of both x and residual)
  *   dgain = the sum of dy h r over the rows                 (fp32, NULL: not wanted)
+ * gain dy and the sum of its products with h are formed in fp32, before r: what
+ * lies past fp32's range there (products from 1e38 on) is not brought back by a
+ * small r, and products below 1e-38 have fewer bits.
  * dx may lie exactly on h, dy or dsum. */
 int sim_norm_grad_work(int64_t rows, int64_t columns, int dtype, size_t* bytes);
 int sim_norm_grad(const void* h, int64_t h_stride, int dtype, int64_t rows, int64_t columns, const void* gain,

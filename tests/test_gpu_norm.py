@@ -204,6 +204,47 @@ def test_codes_of_16_bit_values_are_the_nearest(lib, n, c, group):
     assert torch.equal(q.cpu().double(), nearest_codes(t))
 
 
+# (size of x, of the gain, eps): g h past fp32's range, in numbers that it holds with few bits, below it, all with
+# values of y that it holds
+FAR = [(1e10, 1e30, 1e-6), (1e15, 1e37, 1e-6), (1e15, 1e24, 1e-6), (1e-20, 1e-20, 1e-30), (1e-17, 1e-30, 1e-30), (1e-30, 1e-16, 1e-30),
+       (1e-15, 1e-24, 1e-30)]
+
+
+@pytest.mark.parametrize("size,factor,eps", FAR)
+@pytest.mark.parametrize("n,c", [(3, 3), (5, 61), (9, 300), (3, 900), (2, 5001), (2, 20000)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_products_of_gain_and_value_near_the_ends_of_the_range(lib, size, factor, eps, n, c, dtype):
+    x, gain = rand(n, c, dtype, n + c, size), (gains(c, torch.float32, c) * factor).to(dtype)
+    eps = torch.tensor(eps, dtype=torch.float32).item()
+    y, _ = lib.norm(x.cuda(), gain.cuda(), eps=eps)
+    oracle.check_norm(y, None, x, gain, None, eps)
+    for group in (32, 128, c):
+        q, s, _ = lib.norm_quant(x.cuda(), gain.cuda(), eps=eps, group=group)
+        oracle.check_quant(q, s, None, x, gain, None, eps, group, f"group {group}")
+        y = oracle.norm(x, gain, None, eps)[2]
+        assert (s > 0).all() and (q.float().abs().amax(1) == 448).all() and y.abs().max() < 3e38
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("c", [96, 500, 3000])
+def test_groups_at_both_ends_of_the_range_beside_each_other(lib, dtype, c):
+    """Each group has its own way, whatever lanes of its wave take another one; so has each row with one scale."""
+    x, gain = rand(12, c, dtype, c), gains(c, dtype, c)
+    gain[:32] *= 1e30
+    gain[32:64] *= 1e-30
+    x[1:] *= 1e10
+    x[2:, 32:64] *= 1e-25
+    x[3] = 0
+    x[4] *= 1e-18
+    x[5, 64:] = 0
+    for group in (32, 64, c):
+        q, s, _ = lib.norm_quant(x.cuda(), gain.cuda(), eps=EPS, group=group)
+        oracle.check_quant(q, s, None, x, gain, None, EPS, group, f"group {group}")
+        for row in range(12):  # alone
+            a, b, _ = lib.norm_quant(x[row:row + 1].cuda(), gain.cuda(), eps=EPS, group=group)
+            assert torch.equal(a.view(torch.uint8), q[row:row + 1].view(torch.uint8)) and torch.equal(b, s[row:row + 1])
+
+
 def test_eps_is_all_that_a_row_of_zeros_has(lib):
     x = torch.full((3, 70), 1e-15)
     for eps in (1e-30, 1.0, 1e30):
