@@ -7,6 +7,7 @@ import shutil
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
+from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -84,14 +85,24 @@ def build_pycall(out_dir: str = HERE) -> str:
     return out
 
 
-def build_pytensor(out_dir: str = HERE) -> str:
+def build_pytensor(out_dir: str = HERE) -> Optional[str]:
     """Compile the tensor extension (_pytensor) against this interpreter's and
-    the installed torch's headers; always rebuilds."""
+    the installed torch's headers; always rebuilds.  Where torch or its headers
+    are not installed, None: the package makes the same checks in Python, and an
+    extension of an earlier build is taken away."""
     import sysconfig
-    from torch.utils.cpp_extension import include_paths, library_paths
-    import torch
-    cxx = os.environ.get("CXX", "g++")
     out = os.path.join(out_dir, "_pytensor" + sysconfig.get_config_var("EXT_SUFFIX"))
+    try:
+        import torch
+        from torch.utils.cpp_extension import include_paths, library_paths
+    except ImportError:
+        torch, include_paths = None, list
+    if not any(os.path.exists(os.path.join(p, "torch", "csrc", "autograd", "python_variable.h")) for p in include_paths()):
+        print("no torch headers: tensors are checked in Python", file=sys.stderr)
+        if os.path.exists(out):
+            os.remove(out)
+        return None
+    cxx = os.environ.get("CXX", "g++")
     tmp = out + ".tmp"
     cmd = [cxx, "-O2", "-shared", "-fPIC", "-std=c++17", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", sysconfig.get_paths()["include"], *(f"-isystem{p}" for p in include_paths()),

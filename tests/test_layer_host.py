@@ -325,3 +325,27 @@ def test_expert_gradients_are_those_of_the_objective():
         v, u = torch.randn(t, c, generator=g, dtype=torch.float64), torch.randn(t, k, generator=g, dtype=torch.float64)
         ends = [objective(x + s * 1e-5 * v, w + s * 1e-5 * u) for s in (1, -1)]
         assert abs((ends[0] - ends[1]) / 2e-5 - (dx * v).sum() - (dw * u).sum()) < 1e-8
+
+
+# ---- the tensor extension -----------------------------------------------------------
+def build_script():
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("build_script", os.path.join(ROOT, "all_reduce_reduction_amd", "_build.py"))
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+@pytest.mark.parametrize("missing", ["headers", "torch"])
+def test_a_build_without_torch_headers_leaves_the_tensor_extension_out(tmp_path, monkeypatch, missing):
+    """The package treats it as optional, and so does the build; one that is there already is of another build."""
+    import sys
+    import sysconfig
+    if missing == "headers":
+        import torch.utils.cpp_extension as ext
+        monkeypatch.setattr(ext, "include_paths", lambda *a, **k: [str(tmp_path)])
+    else:
+        monkeypatch.setitem(sys.modules, "torch", None)
+    old = tmp_path / ("_pytensor" + sysconfig.get_config_var("EXT_SUFFIX"))
+    old.write_bytes(b"of an earlier build")
+    assert build_script().build_pytensor(str(tmp_path)) is None and not old.exists()
