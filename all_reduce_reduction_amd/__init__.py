@@ -133,7 +133,9 @@ except ImportError:  # not built: prepare_allreduce falls back to a ctypes call 
 
 try:  # tensors' pointers, sizes and types (csrc/pytensor.cpp), built beside it
     from . import _pytensor
-except ImportError:  # not built, or without torch: the same checks in Python
+    if _pytensor.torch_version != str(torch.__version__):  # another torch may lay its tensors out in another way
+        _pytensor = None
+except (ImportError, AttributeError):  # not built, or without torch: the same checks in Python
     _pytensor = None
 
 

@@ -105,7 +105,7 @@ def build_pytensor(out_dir: str = HERE) -> Optional[str]:
     cxx = os.environ.get("CXX", "g++")
     tmp = out + ".tmp"
     cmd = [cxx, "-O2", "-shared", "-fPIC", "-std=c++17", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-I", sysconfig.get_paths()["include"], *(f"-isystem{p}" for p in include_paths()),
+           f'-DSIMAR_TORCH="{torch.__version__}"', "-I", sysconfig.get_paths()["include"], *(f"-isystem{p}" for p in include_paths()),
            os.path.join(CSRC, "pytensor.cpp"), "-o", tmp, *(f"-L{p}" for p in library_paths()),
            "-ltorch_python", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)

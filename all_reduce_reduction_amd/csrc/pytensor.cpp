@@ -3,8 +3,9 @@
 // Python's attributes and methods each of them costs 30 to 60 ns, five or more to
 // a tensor, which was most of a small call's time on the host.
 //
-// Built against torch's headers into the module _pytensor; without it the package
-// takes the same checks in Python.
+// Built against torch's headers into the module _pytensor; without it, or with another
+// torch than the one whose headers it was built with (SIMAR_TORCH, the version that
+// torch's Python side gives), the package takes the same checks in Python.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <torch/csrc/DynamicTypes.h>
@@ -262,4 +263,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pytensor", "Tensors' pointers, si
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__pytensor(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__pytensor(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", SIMAR_TORCH) < 0) Py_CLEAR(m);
+  return m;
+}

@@ -349,3 +349,17 @@ def test_a_build_without_torch_headers_leaves_the_tensor_extension_out(tmp_path,
     old = tmp_path / ("_pytensor" + sysconfig.get_config_var("EXT_SUFFIX"))
     old.write_bytes(b"of an earlier build")
     assert build_script().build_pytensor(str(tmp_path)) is None and not old.exists()
+
+
+@pytest.mark.parametrize("version", [None, "1.0.0"])
+def test_the_tensor_extension_is_of_the_torch_that_runs(version):
+    """One that was built with another torch's headers may read tensors by the wrong layout: it is not used."""
+    import sys
+    import all_reduce_reduction_amd as sim
+    if sim._pytensor is None:
+        pytest.skip("the tensor extension is not built")
+    code = ("import torch\n" + (f"torch.__version__ = {version!r}\n" if version else "") +
+            "import all_reduce_reduction_amd as sim\n"
+            "print(sim._pytensor is not None, sim._rows is sim._rows_py, sim._tensors is sim._tensors_py, sim._vec is sim._vec_py)")
+    got = subprocess.run([sys.executable, "-c", code], cwd=ROOT, check=True, capture_output=True, text=True).stdout.split()
+    assert got == (["False"] + ["True"] * 3 if version else ["True"] + ["False"] * 3)
