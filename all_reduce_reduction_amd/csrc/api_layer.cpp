@@ -42,7 +42,7 @@ int check_slots(int64_t tokens, int topk) {
 }
 int64_t dispatch_work_bytes(int64_t tokens, int topk, int experts) {
   int64_t chunk;
-  const int64_t chunks = dispatch_chunks(tokens * topk, &chunk);
+  const int64_t chunks = dispatch_chunks(tokens * topk, experts, &chunk);
   return dispatch_counts(tokens * topk, experts) ? chunks * experts * 4 : 0;
 }
 
@@ -245,7 +245,7 @@ int sim_dispatch(const void* x, int64_t x_pitch, int64_t row_bytes, const float*
   if ((rc = library_device())) return rc;
   DispatchArgs a{x, x_pitch, row_bytes, groups > 0 ? scales : nullptr, groups * 4, chosen, tokens, topk, experts, rows,
                  rows_pitch, row_scales, place, offsets, need ? (uint32_t*)work : nullptr, 0, 0};
-  a.chunks = dispatch_chunks(slots, &a.chunk);
+  a.chunks = dispatch_chunks(slots, experts, &a.chunk);
   return hip_status(launch_dispatch(a, (hipStream_t)stream));
 }
 

@@ -149,7 +149,7 @@ struct NormGradShape {
 };
 NormGradShape norm_grad_shape(int64_t cols, int per_vector);
 int norm_grad_workgroups(int64_t rows, int64_t cols, int dtype);
-int dispatch_chunks(int64_t slots, int64_t* chunk);  // 0: one launch for all slots
+int dispatch_chunks(int64_t slots, int experts, int64_t* chunk);  // 0: one launch for all slots
 bool dispatch_counts(int64_t slots, int experts);     // whether a launch of its own counts the chunks' slots
 int64_t clip_pieces(int64_t count, int dtype);
 int clip_workgroups(uint32_t pieces);

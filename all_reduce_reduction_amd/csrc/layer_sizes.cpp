@@ -44,11 +44,23 @@ int norm_grad_workgroups(int64_t rows, int64_t cols, int dtype) {
 // KiB, 8 slots: 8.8 us, 10.3 in two launches; 1,000 tokens, 6 slots: 15.0, 14.6 in
 // three).
 constexpr int64_t kFewSlots = 4096;
-int dispatch_chunks(int64_t slots, int64_t* chunk) {
+// More slots are cut into chunks of 1,024, or so many more that there are at most 512.
+// Each chunk's workgroup reads the counts of all chunks, kCountsPerSlot at most for each
+// of its own slots (what all of them read would else grow with the square of the slots):
+// chunks are made longer until that holds.  Places alone, with that many counts per slot
+// or less, and with chunks of half the length: 16,384 tokens, 32 slots, 1,024 experts
+// 23.1 us, 30.8 (75.4 with a quarter); 65,536, 32 slots, 1,024 experts 41.5, 83; 65,536,
+// 8 slots, 256 experts 13.8, 25.7; 16,384, 16 slots, 512 experts 14.3, 18.3.  Longer ones
+// than that: 65,536, 32 slots, 1,024 experts 60.9; 16,384, 8 slots, 256 experts 10.5
+// with twice the length, 9.5.
+constexpr int64_t kCountsPerSlot = 64;
+int dispatch_chunks(int64_t slots, int experts, int64_t* chunk) {
   *chunk = 0;
   if (slots <= kFewSlots) return 0;
   *chunk = std::max<int64_t>(1024, ((slots + 511) / 512 + 1023) / 1024 * 1024);
-  return (int)((slots + *chunk - 1) / *chunk);
+  const auto chunks = [&] { return (slots + *chunk - 1) / *chunk; };
+  while (chunks() * experts > kCountsPerSlot * *chunk) *chunk *= 2;
+  return (int)chunks();
 }
 
 // Up to so many slots every chunk's workgroup counts all of them.  5,120 slots of 64

@@ -163,6 +163,24 @@ def test_large_batches_place_every_slot(lib):
         assert torch.equal(rows[:n, 0].long(), order[:n] // k)
 
 
+@pytest.mark.parametrize("t,k,e", [(16384, 16, 512), (16384, 32, 1024), (16400, 8, 1024), (65537, 8, 256), (300001, 4, 1000)])
+def test_many_slots_of_many_experts(lib, t, k, e):
+    """Chunks of more slots than the least because of the experts, against a sort by torch."""
+    g = torch.Generator("cuda").manual_seed(t + e)
+    chosen = torch.randint(-1, e, (t, k), device="cuda", generator=g, dtype=torch.int32)
+    x = torch.arange(t, device="cuda", dtype=torch.int32)[:, None].contiguous()
+    rows, place, offsets, _ = lib.dispatch(x, chosen, e)
+    flat = chosen.reshape(-1).long()
+    key = torch.where(flat >= 0, flat, e)
+    order = torch.sort(key, stable=True).indices
+    n = int((flat >= 0).sum())
+    at = torch.full_like(flat, -1)
+    at[order[:n]] = torch.arange(n, device="cuda")
+    assert torch.equal(place.reshape(-1).long(), at)
+    assert offsets[0] == 0 and torch.equal(offsets[1:].long(), torch.bincount(key, minlength=e + 1)[:e].cumsum(0))
+    assert torch.equal(rows[:n, 0].long(), order[:n] // k)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, oracle.E4M3])
 def test_dispatch_slices(lib, dtype):
     t, k, e, c = 50, 4, 9, 37

@@ -363,3 +363,19 @@ def test_the_tensor_extension_is_of_the_torch_that_runs(version):
             "print(sim._pytensor is not None, sim._rows is sim._rows_py, sim._tensors is sim._tensors_py, sim._vec is sim._vec_py)")
     got = subprocess.run([sys.executable, "-c", code], cwd=ROOT, check=True, capture_output=True, text=True).stdout.split()
     assert got == (["False"] + ["True"] * 3 if version else ["True"] + ["False"] * 3)
+
+
+def test_counts_read_by_all_chunks_do_not_grow_with_their_square(checks):
+    """Each chunk's workgroup reads all chunks' counts, which are dispatch's scratch: at most 64 for each of its slots, with
+    no fewer than half as many chunks as that allows."""
+    for tokens, topk, experts in ((16384, 8, 256), (16384, 8, 1024), (16384, 16, 512), (65536, 8, 256), (16384, 32, 1024), (65536, 32, 1024),
+                                  (1 << 20, 32, 1024), ((1 << 31) - 1, 1, 1024), (60000000, 32, 4), (4097, 4, 1024)):
+        n = ctypes.c_size_t(0)
+        assert checks.sim_dispatch_work(tokens, topk, experts, ctypes.byref(n)) == 0
+        chunks = n.value // (4 * experts)
+        assert chunks * (chunks - 1) * experts <= 64 * tokens * topk, (tokens, topk, experts, chunks)
+        assert chunks >= min(tokens * topk // 1024, 256, (64 * tokens * topk / experts) ** 0.5 / 2.01), (tokens, topk, experts, chunks)
+        at = [(i + 1) << 36 for i in range(4)]
+        before = checks.stub_bad()
+        assert checks.sim_dispatch(None, 0, 0, None, 0, at[0], tokens, topk, experts, None, 0, None, at[1], at[2], at[3], n.value, None) == 0
+        assert checks.stub_bad() == before
