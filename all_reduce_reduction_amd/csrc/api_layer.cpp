@@ -33,7 +33,7 @@ int check_norm(int64_t rows, int64_t cols, int dtype, int gain_dtype, float eps)
   return rows < 0 || rows > kMaxGrid || cols < 1 || cols > SIM_NORM_MAX_COLUMNS ? SIM_ERR_INVALID_ARG : SIM_OK;
 }
 int64_t norm_grad_work_bytes(int64_t rows, int64_t cols, int dtype) {
-  const int64_t wg = norm_grad_workgroups(rows, cols, dtype);
+  const int64_t wg = norm_grad_workgroups(rows, cols, dtype, true);
   return wg > 1 ? wg * cols * 4 : 0;
 }
 
@@ -205,7 +205,7 @@ int sim_norm_grad(const void* h, int64_t h_stride, int dtype, int64_t rows, int6
   if ((rc = check_arrays(all, may))) return rc;
   if ((rc = library_device())) return rc;
   const NormGradArgs a{h, h_stride, rows, (int)columns, gain, gain_dtype, eps, dy, dy_stride, dsum, dsum_stride, dx,
-                       dx_stride, dgain, (float*)work, norm_grad_workgroups(rows, columns, dtype)};
+                       dx_stride, dgain, (float*)work, norm_grad_workgroups(rows, columns, dtype, dgain != nullptr)};
   return hip_status(launch_norm_grad(a, dtype, (hipStream_t)stream));
 }
 

@@ -148,7 +148,7 @@ struct NormGradShape {
   int lanes, per_thread, threads;
 };
 NormGradShape norm_grad_shape(int64_t cols, int per_vector);
-int norm_grad_workgroups(int64_t rows, int64_t cols, int dtype);
+int norm_grad_workgroups(int64_t rows, int64_t cols, int dtype, bool dgain);
 int dispatch_chunks(int64_t slots, int experts, int64_t* chunk);  // 0: one launch for all slots
 bool dispatch_counts(int64_t slots, int experts);     // whether a launch of its own counts the chunks' slots
 int64_t clip_pieces(int64_t count, int dtype);

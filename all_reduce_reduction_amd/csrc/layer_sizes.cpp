@@ -14,7 +14,7 @@ NormGradShape norm_grad_shape(int64_t cols, int per_vector) {
   const int r = nv <= 1024 && per_vector == 8 ? 1 : nv <= 2048 ? 2 : nv <= 4096 ? 4 : 8;
   return {0, r, row_threads(nv, r)};
 }
-int norm_grad_workgroups(int64_t rows, int64_t cols, int dtype) {
+int norm_grad_workgroups(int64_t rows, int64_t cols, int dtype, bool dgain) {
   const int per_vector = dtype == SIM_FP32 ? 4 : 8;
   const NormGradShape f = norm_grad_shape(cols, per_vector);
   const bool ahead = f.per_thread * per_vector <= 8;  // (the next row's loads under way)
@@ -22,7 +22,9 @@ int norm_grad_workgroups(int64_t rows, int64_t cols, int dtype) {
   // One workgroup where its turns cost less than a second launch: 2 rows x 4,096 bf16
   // 4.1 us, 8.6 with a workgroup each, 4 rows 6.0, 8.7, 8 rows 10.0, 8.7; 60 x 320,
   // 8 turns, 7.2, 8.7; without loads ahead 2 x 10,933 7.1, 8.7, 8 x 12,000 18.2, 8.7.
-  if (turns <= (f.lanes ? 8 : ahead ? 4 : f.per_thread == 2 ? 2 : 1)) return 1;
+  // Without dgain there is no second launch, and there are no partial sums below: 512
+  // rows x 64 bf16 4.6 us, 7.2 in one workgroup; 249 x 10,216 5.3, 7.1 with two rows each.
+  if (turns <= (!dgain ? 1 : f.lanes ? 8 : ahead ? 4 : f.per_thread == 2 ? 2 : 1)) return 1;
   // 16 waves on each compute unit (32, without the next row's loads ahead, read and
   // write more rows at once, which costs memory more than it hides: 16,384 x 8,192
   // bf16 181 us, 185; 4,096 x 5,120 38 us, 45.5); each takes the same number of
@@ -35,7 +37,7 @@ int norm_grad_workgroups(int64_t rows, int64_t cols, int dtype) {
   // with two; 200 x 4,096, 3 MB, 8.9, 8.7 with one.  Four vectors per thread, whose
   // rows follow each other without loads ahead, lose by it (152 x 16,010 fp32 26.9,
   // 23.0 with one).
-  if (!f.lanes && f.per_thread <= 2 && rows * cols >= 1 << 20)
+  if (dgain && !f.lanes && f.per_thread <= 2 && rows * cols >= 1 << 20)
     each = std::max(each, ahead ? std::min<int64_t>(4, std::max<int64_t>(2, (turns + library_cus() - 1) / library_cus())) : 2);
   return (int)std::max<int64_t>(1, (turns + each - 1) / each);
 }

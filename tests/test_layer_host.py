@@ -379,3 +379,15 @@ def test_counts_read_by_all_chunks_do_not_grow_with_their_square(checks):
         before = checks.stub_bad()
         assert checks.sim_dispatch(None, 0, 0, None, 0, at[0], tokens, topk, experts, None, 0, None, at[1], at[2], at[3], n.value, None) == 0
         assert checks.stub_bad() == before
+
+
+def test_without_a_gains_gradient_rows_share_workgroups_only_where_the_gpu_is_full(checks):
+    """What one workgroup for few rows, or several rows each, saves is the launch that adds up the gain's gradient."""
+    of = checks._ZN5simar20norm_grad_workgroupsEllib
+    of.argtypes, of.restype = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_bool], ctypes.c_int
+    for dtype in (FP32, BF16):
+        for rows, cols in ((2, 4096), (4, 4096), (8, 5000), (250, 10000), (4, 2000), (256, 32768)):
+            assert of(rows, cols, dtype, False) == rows >= of(rows, cols, dtype, True)
+        for rows, cols, turns in ((512, 30, 8), (64, 250, 4), (60, 130, 2), (1, 64, 1)):
+            assert of(rows, cols, dtype, False) >= turns and of(rows, cols, dtype, True) == 1
+        assert of(0, 64, dtype, True) == of(0, 64, dtype, False) == 1
