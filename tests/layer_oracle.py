@@ -8,8 +8,10 @@ squares is off by less than 44 u relative and r = 1 / sqrt(mean + eps) by less
 than 22 u + 4 u; y = g h r has three more roundings: 32 u.  A sum of products
 that may cancel is off by less than 48 u times the sum of their sizes.
 Combine: topk fused multiply-adds, topk u times the sum of the sizes.
-Products over a row: a thread adds at most 16 + cols / 256 terms, then 10
-levels.  Clipping: squares in 64 bits, of halves eight at a time in 32 (8 u, so
+Products over a row: a lane adds cols / 64 + 8 terms where one wave takes a token,
+less where two to eight waves share it, then 6 to 9 levels: products_tolerance().  Up
+to 2,200 columns of one wave, and for all shared rows, that is within the (40 + cols /
+256) u of combine_grad below.  Clipping: squares in 64 bits, of halves eight at a time in 32 (8 u, so
 4 u of the norm), the norm rounds once, the factor once, the product once."""
 import torch
 
@@ -118,6 +120,11 @@ def combine_grad(dy, rows, place, weights):
                 dw[i, j] = (d * rows[p].double()).sum()
                 tol[i, j] = (40 + c / 256) * U * (d * rows[p].double()).abs().sum()
     return drows, dw, tol + 1e-37
+
+
+def products_tolerance(terms):
+    """Of a sum over the last dimension of these products, in 32 bits by one wave."""
+    return (terms.shape[-1] / 64 + 17) * U * terms.abs().sum(-1) + 1e-37
 
 
 # ---- clipping ------------------------------------------------------------------------

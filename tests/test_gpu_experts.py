@@ -274,6 +274,39 @@ def test_combine_grad_of_more_rows_than_the_caches_hold(lib, t, k, c, dtype):
     assert torch.equal(rows[:n], out[0][:n]) and torch.equal(dw, out[1])
 
 
+# (a wave takes a token, and its columns in several turns: rows that start on a line, whose loads stream, and others;
+# weights and rows in one launch, and in two where the rows are more than the caches hold)
+@pytest.mark.parametrize("t,k,c,dtype", [(6500, 8, 2048, torch.bfloat16), (5000, 2, 2048, torch.bfloat16), (5000, 2, 2051, torch.bfloat16),
+                                         (5000, 3, 2048, torch.float16), (4100, 3, 1024, torch.float32), (4100, 1, 1029, torch.float32),
+                                         (4097, 9, 1536, torch.bfloat16), (13000, 2, 5120, torch.bfloat16)])
+def test_combine_grad_of_batches(lib, t, k, c, dtype):
+    g = torch.Generator("cuda").manual_seed(t + c)
+    chosen = torch.randint(-1, 40, (t, k), device="cuda", generator=g, dtype=torch.int32)
+    _, place, offsets, _ = lib.dispatch(torch.empty(t, 1, device="cuda"), chosen, 40)
+    n = int(offsets[40])
+    rows = torch.randn(t * k, c, device="cuda", generator=g).to(dtype)
+    dy = torch.randn(t, c, device="cuda", generator=g).to(dtype)
+    w = torch.rand(t, k, device="cuda", generator=g) + 0.1
+    full = place.reshape(-1) >= 0
+    at, token = place.reshape(-1)[full].long(), torch.arange(t * k, device="cuda")[full] // k
+    drows = torch.full((t * k, c), 7.0, dtype=dtype, device="cuda")
+    want = drows.clone()
+    want[at] = (w.reshape(-1)[full][:, None] * dy[token].float()).to(dtype)  # one product, rounded once more
+    _, dw = lib.combine_grad(dy, rows, place, w, out=(drows, torch.empty(t, k, device="cuda")))
+    assert torch.equal(drows, want)
+    for a in range(0, n, 8000):
+        terms = dy[token[a:a + 8000]].double() * rows[at[a:a + 8000]].double()
+        oracle.assert_within(dw.reshape(-1)[full][a:a + 8000].cpu(), terms.sum(1).cpu(), oracle.products_tolerance(terms).cpu(), "dweights")
+    assert not dw.reshape(-1)[~full].any()
+    alone = lib.combine_grad(dy, rows, place, w, out=(None, torch.empty_like(dw)))[1]
+    over, twice = rows.clone(), torch.empty_like(dw)
+    lib.combine_grad(dy, over, place, w, out=(over, twice))
+    assert torch.equal(over[:n], want[:n]) and torch.equal(over[n:], rows[n:]) and torch.equal(twice, dw) and torch.equal(alone, dw)
+    # without weights: the rows are dy itself
+    lib.combine_grad(dy, rows, place, out=(over, twice))
+    assert torch.equal(over[at], dy[token]) and torch.equal(twice, dw)
+
+
 def test_places_outside_the_rows_are_empty_slots(lib):
     rows = torch.randn(6, 70)
     place = torch.tensor([[0, 6, -1], [2 ** 31 - 1, -2 ** 31, 5], [7, 100, -7]], dtype=torch.int32)
