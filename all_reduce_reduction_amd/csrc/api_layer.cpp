@@ -332,7 +332,7 @@ int sim_clip_norm(const void* const* grads, const int64_t* counts, const int* dt
   const hipStream_t s = (hipStream_t)stream;
   const hipError_t e = squares_of_list(grads, counts, dtypes, ntensors, (double*)work, s);
   if (e != hipSuccess) return hip_status(e);
-  return hip_status(launch_clip_join(ClipNorm{(const double*)work, sizes.squares, nullptr, 0, 0.0f, norm, 0, nullptr}, s));
+  return hip_status(launch_clip_join(ClipNorm{(const double*)work, sizes.squares, nullptr, 0, 0.0f, norm, 0, nullptr, nullptr}, s));
 }
 
 int sim_clip(const void* const* grads, void* const* outs, const int64_t* counts, const int* dtypes, int ntensors,
@@ -373,14 +373,14 @@ int sim_clip(const void* const* grads, void* const* outs, const int64_t* counts,
   const hipStream_t s = (hipStream_t)stream;
   double* squares = (double*)work;
   hipError_t e = hipSuccess;
-  ClipNorm n{squares, parts ? 0 : sizes.squares, parts, nparts, max_norm, norm, in_place, nullptr};
+  ClipNorm n{squares, parts ? 0 : sizes.squares, parts, nparts, max_norm, norm, in_place, nullptr, nullptr};
   if (!parts && (e = squares_of_list(grads, counts, dtypes, ntensors, squares, s)) != hipSuccess) return hip_status(e);
   if (sizes.launches != 1 || sizes.pieces > kJoinPieces) {
-    // the sum by itself, or the norm of the parts, read by every workgroup that scales
-    n.total = parts || sizes.squares == 0 ? nullptr : squares;
+    // the norm by itself, read by every workgroup that scales
+    n.keep = parts || sizes.squares == 0 ? nullptr : squares;
     if ((e = launch_clip_join(n, s)) != hipSuccess) return hip_status(e);
-    n = n.total ? ClipNorm{squares, 1, nullptr, 0, max_norm, nullptr, in_place, nullptr}
-                : ClipNorm{nullptr, 0, norm, 1, max_norm, nullptr, in_place, nullptr};
+    n = n.keep ? ClipNorm{squares, 0, nullptr, 0, max_norm, nullptr, in_place, squares, nullptr}
+               : ClipNorm{nullptr, 0, norm, 1, max_norm, nullptr, in_place, nullptr, nullptr};
   }
   for (int i = 0; i < ntensors;) {
     ClipList l;

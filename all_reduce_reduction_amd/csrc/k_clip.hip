@@ -175,6 +175,7 @@ __device__ __forceinline__ double sum_of(const ClipNorm& n) {
 // holds it, so that all ranks have the same factor whatever launches their own lists
 // take.  Past fp32's range it is infinite, as norm[0] is.
 __device__ __forceinline__ double norm_of(const ClipNorm& n) {
+  if (n.known) return n.known[0];
   if (n.parts && n.nparts == 1) return (double)fabsf(n.parts[0]);
   const double norm = sqrt(sum_of(n));
   const float rounded = (float)norm;
@@ -182,16 +183,11 @@ __device__ __forceinline__ double norm_of(const ClipNorm& n) {
 }
 
 __global__ void __launch_bounds__(kBlock) k_clip_join(ClipNorm n) {
-  if (n.total) {
-    // (every thread has read its squares before the sum is there)
-    const double sum = sum_of(n);
-    if (threadIdx.x == 0) {
-      n.norm[0] = (float)sqrt(sum);
-      n.total[0] = sum;
-    }
-  } else {
-    const double norm = norm_of(n);
-    if (threadIdx.x == 0) n.norm[0] = (float)norm;
+  const double norm = norm_of(n);
+  if (threadIdx.x == 0) {
+    n.norm[0] = (float)norm;
+    // (every thread has read its squares before the norm is there)
+    if (n.keep) n.keep[0] = norm;
   }
 }
 

@@ -127,7 +127,8 @@ struct ClipNorm {
   float max_norm;
   float* norm;            // NULL: another launch writes it
   int in_place;
-  double* total;          // NULL, or where launch_clip_join leaves the squares' sum (squares itself, say)
+  const double* known;    // NULL, or the norm itself, as another launch left it
+  double* keep;           // NULL, or where launch_clip_join leaves the norm (over the squares, say)
 };
 
 // layer_sizes.cpp
