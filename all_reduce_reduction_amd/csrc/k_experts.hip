@@ -387,11 +387,9 @@ __device__ __forceinline__ void add_rows(const CombineArgs& a, const TokenSlots&
     for (int t = 0; t < V; t++) acc[t] = __builtin_fmaf(w[i], f[t], acc[t]);
   }
 }
-// A wave takes part of a token's columns, 64 vectors.  With many loads of a wave
-// under way WAVES per SIMD are enough, and more would only interleave more rows in
-// memory (16,384 tokens of 8 KiB, 8 slots: three 198 us, four 204, eight 214; 4,096
-// of 16 KiB, 6 slots: three 74 us, four 70.5, eight 73; 16,384 of 8 KiB, 2 slots:
-// four 73 us, eight 65).
+// A wave takes part of a token's columns, 64 vectors.  Where the rows are more than the
+// caches hold and a wave has many loads under way, fewer WAVES per SIMD than eight are
+// enough, and more only interleave more rows in memory (launch below).
 template <int DT, int WAVES>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES < 8 ? WAVES : 4, WAVES))) k_combine(CombineArgs a, int parts) {
   constexpr int V = epv<DT>();
@@ -593,8 +591,17 @@ hipError_t combine(const CombineArgs& a, hipStream_t s) {
   if (nv <= 32) return launch<k_combine_short<DT, 32, false>>(dim3(grid_of(a.tokens, 8)), dim3(256), s, a);
   const int parts = (int)((nv + 63) / 64);
   const dim3 grid(grid_of(a.tokens * parts, 4));
-  if (a.topk >= 8) return launch<k_combine<DT, 3>>(grid, dim3(256), s, a, parts);
-  if (a.topk > 4) return launch<k_combine<DT, 4>>(grid, dim3(256), s, a, parts);
+  // By slots (three, four, eight waves, us; bf16): 16,384 tokens of 8 KiB, 2 slots 85, 74,
+  // 65; 4 slots 116, 110, 110; 6 slots 160, 151, 160; 8 slots 196, 200, 213; 16 slots 380,
+  // 397, 399.  By bytes, in what all slots would read: 4,096 of 16 KiB, 6 slots, 384 MiB
+  // 80.7, 76.0, 77.5; 6,000 of 8 KiB, 6 slots, 281 MiB 60.0, 57.8, 56.7; 8 slots, 375 MiB
+  // 72.9, 72.7, 74.1; 8,192 of 4 KiB, 8 slots, 256 MiB 49.8, 48.1, 49.5; 4,096 of 4 KiB, 8
+  // slots, 128 MiB 25.9, 24.5, 23.6; 1,000 of 8 KiB, 8 slots 12.6, 11.6, 10.7.  How many
+  // slots are empty is not known here: with every other one of 8 x 16,384 of 8 KiB three
+  // waves lose (125, 112, 112).
+  const bool many = (double)a.tokens * a.topk * (double)a.cols * Ty<DT>::E > (double)(320 << 20);
+  if (many && a.topk >= 8) return launch<k_combine<DT, 3>>(grid, dim3(256), s, a, parts);
+  if (many && a.topk > 4) return launch<k_combine<DT, 4>>(grid, dim3(256), s, a, parts);
   return launch<k_combine<DT, 8>>(grid, dim3(256), s, a, parts);
 }
 // W waves share a token

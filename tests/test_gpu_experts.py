@@ -274,6 +274,25 @@ def test_combine_grad_of_more_rows_than_the_caches_hold(lib, t, k, c, dtype):
     assert torch.equal(rows[:n], out[0][:n]) and torch.equal(dw, out[1])
 
 
+@pytest.mark.parametrize("t,k,c,dtype", [(21000, 8, 1001, torch.bfloat16), (30000, 6, 1024, torch.bfloat16), (9000, 9, 1061, torch.float32),
+                                         (13000, 7, 1000, torch.float32), (7000, 16, 1550, torch.float16), (20000, 5, 1700, torch.float16)])
+def test_combine_of_more_rows_than_the_caches_hold(lib, t, k, c, dtype):
+    g = torch.Generator("cuda").manual_seed(t)
+    chosen = torch.randint(-1, 40, (t, k), device="cuda", generator=g, dtype=torch.int32)
+    _, place, offsets, _ = lib.dispatch(torch.empty(t, 1, device="cuda"), chosen, 40)
+    rows = torch.randn(t * k, c, device="cuda", generator=g).to(dtype)
+    rows[int(offsets[40]):] = NAN
+    w = torch.randn(t, k, device="cuda", generator=g)
+    w[place < 0] = NAN
+    got = lib.combine(rows, place, w)
+    for a in range(0, t, 3000):
+        full = (place[a:a + 3000] >= 0)[:, :, None]
+        picked = rows[place[a:a + 3000].clamp(min=0).long()].double()
+        terms = torch.where(full, picked * w[a:a + 3000, :, None].double(), 0.0)
+        want = terms.sum(1)
+        oracle.assert_within(got[a:a + 3000].cpu(), want.cpu(), oracle.rounded((k + 1) * oracle.U * terms.abs().sum(1), want, dtype).cpu(), "out")
+
+
 # (a wave takes a token, and its columns in several turns: rows that start on a line, whose loads stream, and others;
 # weights and rows in one launch, and in two where the rows are more than the caches hold)
 @pytest.mark.parametrize("t,k,c,dtype", [(6500, 8, 2048, torch.bfloat16), (5000, 2, 2048, torch.bfloat16), (5000, 2, 2051, torch.bfloat16),
