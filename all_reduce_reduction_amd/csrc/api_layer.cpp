@@ -47,8 +47,9 @@ int64_t dispatch_work_bytes(int64_t tokens, int topk, int experts) {
 }
 
 // Up to so many pieces the workgroups that scale them each add up the squares'
-// sums (2.6 M halves in 322 pieces 13.8 us, 15.2 with a launch for it); with more,
-// that costs them more than a launch (98,824 pieces 774 us, 770 with it).
+// sums (322 pieces 12.9 us, 15.8 with a launch for it; 1,000 12.7, 14.4; 2,000 23.2,
+// 24.4); with more, that costs them more than a launch (3,000 pieces 33.9, 31.8; 8,000
+// 77, 67; 98,824 864, 747).
 constexpr int64_t kJoinPieces = 2048;
 
 // ---- lists of tensors ---------------------------------------------------------

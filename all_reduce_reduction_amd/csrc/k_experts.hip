@@ -15,12 +15,17 @@
 // costs a load.
 //
 // Bound by memory, and by how it takes rows in no order: 16,384 tokens and 8 slots,
-// combine of 8 KiB rows 198 us (1,209 MB at 6.1 TB/s; a copy of as many bytes 182),
+// combine of 8 KiB rows 197 us (1,209 MB at 6.1 TB/s; a copy of as many bytes 182),
 // its gradient 406 (weights 185, rows 221; 2,283 MB, 343), dispatch of 4 KiB rows 127
-// (places 12, rows 115; 624 MB, 94).  Writes alone that fill memory from its start
-// reach 6.7 TB/s when every wave writes once, 5.5 when it writes eight times, 4.5 to
-// rows of 4 KiB in no order; taking the slots in their rows' order instead, each
-// row's token read again from the caches, was slower (146 us for the rows).
+// (places 10.5, rows and scales 115; 624 MB, 94; without the scales 120 in all).  What
+// bounds dispatch is how memory takes writes: 537 MB written from its start to its end
+// take 80 us when every wave writes 1 KiB once, 97 when it writes eight times in a row,
+// 101 when it writes to the rows of a token's eight experts, and 119 with the token's
+// row read before (a kernel that does nothing else).  Taking the slots in their rows'
+// order instead, each row's token read again from the caches, was slower (146 us).
+// Rows of an odd number of 16-bit elements lie across lines that two waves write: 16,384
+// tokens, 8 slots of 2,049 and 2,048 bf16 columns dispatch 154 us, 120; combine 130, 97;
+// its gradient 278, 210.
 #include <algorithm>
 
 #include "launch.h"
@@ -529,6 +534,9 @@ __device__ __forceinline__ void grad_rows(const CombineGradArgs& a, const TokenS
     for (int i = 0; i < N; i++) a.dweights[token * a.topk + slot[i]] = dot[i];
   }
 }
+// (Rows of up to 64 vectors have a whole wave too, most of whose lanes idle in short ones:
+// 16,384 tokens, 16 slots of 64 bf16 columns 36 us, bound by instructions; 10 for the
+// bytes.)
 // Where there are too few tokens to fill the GPU with a wave each, up to eight waves
 // share one (333 tokens x 2,263 fp32, 6 slots: 9.2 us, four 9.9, sixteen 11.3), but
 // no more than its row has 64 vectors for: the others would only wait (bf16, 1,116
@@ -649,10 +657,10 @@ hipError_t combine_grad(const CombineGradArgs& a, hipStream_t s) {
 
 // Few slots go in one launch while a workgroup reads few of them, once for every 8
 // of its token's slots, and all workgroups together not too many; else in two.
-// A workgroup's own: 512 tokens of 4 KiB, 8 slots, 4,096 read: 8.8 us, 10.3 in two
-// launches; 128, 16 slots, 4,096: 8.5, 9.4; 400, 10 slots, 8,000: 13.4, 10.4; 128, 32
-// slots, 16,384: 22.8, 11.2.  All of them: 1,024 of 8 KiB, 2 slots, 4.2 M: 9.9, 12.0;
-// 1,600 of 4 KiB, 2 slots, 5.1 M: 11.6, 10.9; 4,096, one slot, 16.8 M: 22.7, 14.1.
+// A workgroup's own: 512 tokens of 4 KiB, 8 slots, 4,096 read: 9.2 us, 11.2 in two
+// launches; 128, 16 slots, 4,096: 8.7, 9.9; 400, 10 slots, 8,000: 13.1, 10.7; 128, 32
+// slots, 16,384: 23.1, 12.0.  All of them: 1,024 of 8 KiB, 2 slots, 4.2 M: 10.8, 11.7;
+// 1,600 of 4 KiB, 2 slots, 5.1 M: 11.6, 11.6; 4,096, one slot, 16.8 M: 23.9, 14.7.
 constexpr int64_t kFewChunk = 1024, kFewOwn = 6 << 10, kFewReads = 9 << 19;
 hipError_t launch_dispatch(const DispatchArgs& args, hipStream_t s) {
   DispatchArgs a = args;

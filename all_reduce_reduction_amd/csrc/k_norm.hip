@@ -14,8 +14,9 @@
 //
 // Bound by memory that reads and writes at once: 151 us for 16,384 rows x 8,192
 // bf16 with residual to e4m3 (944 MB at 6.3 TB/s; a copy of as many bytes 142), the
-// vector units beside it busy for 60 % of that.  One row of 8,192: 3.7 us on the GPU
-// (load, sum over eight waves, store), 4.2 a call.
+// vector units beside it busy for 65 % of that.  fp32 and fp16 rows of more than 16,384
+// columns spill registers (44, 8): 1,024 x 32,768 fp32 134 us, fp16 52, bf16 47.5.  One
+// row of 8,192: 3.7 us on the GPU (load, sum over eight waves, store), 4.2 a call.
 #include "launch.h"
 #include "layer.h"
 #include "row_device.h"
@@ -111,7 +112,7 @@ template <int DT, int L, int R, bool TINY>
 __global__ void __launch_bounds__(L ? 256 : 1024) k_norm(NormArgs a) {
   constexpr int V = epv<DT>(), G = L ? L : 64;
   // With one vector the gain stays in registers; with more the gain is loaded again, so
-  // that two workgroups have room (16,384 x 8,192 bf16 151 us, 157.5 held).
+  // that two workgroups have room (16,384 x 8,192 bf16 151 us, 184 held).
   constexpr bool HOLD = R == 1;
   __shared__ float sum_s[2][16], top_s[2][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -265,7 +266,7 @@ hipError_t pick(const NormArgs& a, hipStream_t s) {
   if (nv <= 64) return go<DT, 64, 1>(a, 64, s);
   if (nv <= 128) return go<DT, 64, 2>(a, 64, s);
   // Two vectors per thread leave room for another row's workgroup on the same
-  // compute unit (16,384 x 8,192 bf16 157 us, 219 with one; a few rows by
+  // compute unit (16,384 x 8,192 bf16 151 us, 220 with one; a few rows by
   // themselves take the same with either, 1 x 8,192 3.7 us).
   if (nv <= 2048) return go<DT, 0, 2>(a, row_threads(nv, 2), s);
   if (nv <= 4096) return go<DT, 0, 4>(a, row_threads(nv, 4), s);

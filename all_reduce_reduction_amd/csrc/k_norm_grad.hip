@@ -7,10 +7,13 @@
 // dgain in registers from the first row to the last; the workgroups' shares are
 // added up by a second launch, in the workgroups' order.
 //
-// Bound by memory that reads and writes at once: 184 us for 16,384 rows x 8,192
-// bf16 with dsum (1,074 MB; a copy of as many bytes 161), of which the second launch
-// and its gap are 6; 1,003 rows x 2,261 fp32 11 us, where a workgroup's four rows
-// follow each other; 2 rows x 4,096 bf16 4.1 us, in one workgroup and one launch.
+// Bound by memory that reads and writes at once: 183 us for 16,384 rows x 8,192
+// bf16 with dsum (1,074 MB; a copy of as many bytes 161; without the next row's loads
+// ahead 186), of which the second launch and its gap are 6; 1,003 rows x 2,261 fp32 11
+// us, where a workgroup's four rows follow each other; 2 rows x 4,096 bf16 4.1 us, in one
+// workgroup and one launch.  Four vectors of 16 bits or eight of fp32 per thread spill
+// (fp32 84 registers, fp16 68, bf16 32): 1,024 x 32,768 without dsum fp32 169 us, fp16
+// 133, bf16 82.
 #include "launch.h"
 #include "layer.h"
 #include "row_device.h"

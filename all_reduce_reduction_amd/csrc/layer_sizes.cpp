@@ -27,8 +27,8 @@ int norm_grad_workgroups(int64_t rows, int64_t cols, int dtype, bool dgain) {
   if (turns <= (!dgain ? 1 : f.lanes ? 8 : ahead ? 4 : f.per_thread == 2 ? 2 : 1)) return 1;
   // 16 waves on each compute unit (32, without the next row's loads ahead, read and
   // write more rows at once, which costs memory more than it hides: 16,384 x 8,192
-  // bf16 181 us, 185; 4,096 x 5,120 38 us, 45.5); each takes the same number of
-  // rows, or one less.
+  // bf16 183 us, 186.5; 16,384 x 4,096 92, 108; 4,096 x 5,120 36.7, 42.0); each takes the
+  // same number of rows, or one less.
   const int64_t most = library_cus() * std::max<int64_t>(1, 16 / (f.threads / 64));
   int64_t each = std::max<int64_t>(1, (turns + most - 1) / most);
   // Where a row each would make 4 MB of partial sums, two rows each, or up to four
@@ -42,9 +42,9 @@ int norm_grad_workgroups(int64_t rows, int64_t cols, int dtype, bool dgain) {
   return (int)std::max<int64_t>(1, (turns + each - 1) / each);
 }
 
-// Up to so many slots each token's workgroup may read all of them (512 tokens of 4
-// KiB, 8 slots: 8.8 us, 10.3 in two launches; 1,000 tokens, 6 slots: 15.0, 14.6 in
-// three).
+// Up to so many slots each token's workgroup may read all of them (tokens of 4 KiB: 512
+// with 8 slots 9.2 us, 11.2 in two launches; 640 with 8 slots 12.1, 12.2; 1,000 with 6
+// slots 14.9, 12.8).
 constexpr int64_t kFewSlots = 4096;
 // More slots are cut into chunks of 1,024, or so many more that there are at most 512.
 // Each chunk's workgroup reads the counts of all chunks, kCountsPerSlot at most for each

@@ -583,8 +583,9 @@ int sim_distill_grad(const void* logits, int64_t row_stride, int dtype, int64_t 
  *                 rows lie out_stride bytes apart, with
  *                 scales[t][g] = the largest |y| of the row's columns
  *                 [g group, (g + 1) group) / 448,  out = y / scale, rounded to
- *                 nearest even; group is 32, 64 or 128, or 0: one scale for a
- *                 row.  A group of zeros has scale 0.
+ *                 nearest even (the quotient of gain * h, where r divides
+ *                 out); group is 32, 64 or 128, or 0: one scale for a row.  A
+ *                 group of zeros has scale 0.
  * sum and out may each lie exactly on x or residual (same address and stride;
  * out only in `dtype`).  eps lies in [1e-30, 1e30]; the sum of squares is held
  * in fp32 (values past 1e19 overflow it: r is 0).  A NaN makes its row's y (in
@@ -649,7 +650,8 @@ int sim_combine_grad(const void* dy, int64_t dy_stride, int dtype, const void* r
  * host memory, read before the call returns.
  *   sim_clip_norm  norm[0] = sqrt(the sum of all elements' squares), summed in
  *                  fp64
- *   sim_clip       outs[i] = grads[i] * min(1, max_norm / norm), rounded once;
+ *   sim_clip       outs[i] = grads[i] * min(1, max_norm / norm), the product in
+ *                  fp32 and rounded to dtypes[i];
  *                  outs NULL: in place, where a factor of 1 writes nothing.
  *                  norm[0] is the norm; with parts[nparts] (the norms of all
  *                  ranks' own gradients, as sim_all_gather leaves them) it is
